@@ -10,6 +10,8 @@ Functions carry the C names:
   lora_workspace_size, lora_plan_build, lora_apply, lora_apply_noalloc, lora_shrink, lora_expand,
   lora_apply_planned, lora_shrink_planned, lora_expand_planned,
   lora_apply_multi, lora_apply_sliced, lora_read_device_errors, lora_status_string,
+  the operators around a LoRA layer (include/lora_base.h): lora_quantize_rows, lora_base_product, lora_base_apply,
+  lora_base_workspace_size, lora_rotary_apply, lora_rotary_frequencies,
   and the measurement aids lora_calib_gather_read and lora_calib_tile_stream
   (include/lora_calib.h).
 
@@ -20,6 +22,7 @@ x [T][ldx], y [T][ldy] with unit column stride (ld = stride(0)); idx int32
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -57,6 +60,25 @@ class lora_problem(ctypes.Structure):
                 ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
+class lora_base_weight(ctypes.Structure):
+    _fields_ = [("W", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+                ("d_in", ctypes.c_int32), ("d_out", ctypes.c_int32)]
+
+
+class lora_rotary(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float)]
+
+
+class lora_rotary_slice(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("src_token", ctypes.c_int64),
+                ("src_head", ctypes.c_int64), ("dst_token", ctypes.c_int64), ("dst_head", ctypes.c_int64),
+                ("n_heads", ctypes.c_int32)]
+
+
+LORA_ROTARY_PLAIN, LORA_ROTARY_LINEAR, LORA_ROTARY_BASE, LORA_ROTARY_PARTS = 0, 1, 2, 3
+LORA_MAX_SLICES = 8
+
 _lib = None
 
 
@@ -87,6 +109,12 @@ def lib() -> ctypes.CDLL:
             "lora_pool_load": (ctypes.c_int, [pp, I32, P, P, P]),
             "lora_calib_gather_read": (ctypes.c_int, [P, P, I32, I32, I32, P, I32, I32, P, P]),
             "lora_calib_tile_stream": (ctypes.c_int, [P, P, I32, I32, I32, P, I32, I32, I32, P, P]),
+            "lora_quantize_rows": (ctypes.c_int, [P, I64, ctypes.c_int, I32, I32, P, I64, P, P]),
+            "lora_base_product": (ctypes.c_int, [P, P, I64, P, I32, P, I64, ctypes.c_int, P]),
+            "lora_base_workspace_size": (SZ, [P, I32]),
+            "lora_base_apply": (ctypes.c_int, [P, P, I64, I32, P, I64, ctypes.c_int, P, SZ, P]),
+            "lora_rotary_apply": (ctypes.c_int, [P, P, I32, I32, P, ctypes.c_int, I32, P]),
+            "lora_rotary_frequencies": (ctypes.c_int, [ctypes.c_int, ctypes.c_double, I32] + [ctypes.c_double] * 4 + [P]),
             "lora_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "lora_abi_version": (I32, []),
         }
@@ -365,6 +393,168 @@ def lora_pool_load(pool: Pool, slot: int, A_host, B_host, stream=None):
         raise LoraError(-2, "A_host must be [r][d_in] and B_host [d_out][r], contiguous, of the pool's dtype")
     s = (stream or torch.cuda.current_stream(pool.A.device)).cuda_stream
     _check(lib().lora_pool_load(ctypes.byref(pool.c), int(slot), _ptr(A_host), _ptr(B_host), s), "lora_pool_load")
+
+
+# ------------------------------------------- around a LoRA layer (lora_base.h) --
+def _device_guard(dev):
+    """The tensors' device as the current one: a launch goes to the current device."""
+    if dev.index == _torch().cuda.current_device():
+        return contextlib.nullcontext()
+    return _torch().cuda.device(dev)
+
+
+def _rows_2d(what: str, name: str, t, dtypes, dev, cols: int, rows: Optional[int] = None) -> int:
+    """Checks one 2-D tensor of a call and returns its row stride."""
+    if t.device != dev or dev.type != "cuda":
+        raise LoraError(-1, f"{what}: {name} must be in device memory, every tensor on {dev} (found {t.device})")
+    if t.dtype not in dtypes:
+        raise LoraError(-2, f"{what}: {name} must be {' or '.join(str(d) for d in dtypes)} (got {t.dtype})")
+    if t.dim() != 2 or t.shape[1] < cols or (rows is not None and t.shape[0] < rows):
+        raise LoraError(-2, f"{what}: {name} must be at least [{'*' if rows is None else rows}][{cols}] "
+                            f"(got {tuple(t.shape)})")
+    if t.shape[0] == 0:
+        return max(int(t.shape[1]), 1)
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise LoraError(-2, f"{what}: {name} must have unit column stride")
+    if t.shape[0] == 1:
+        return int(t.shape[1])
+    return int(t.stride(0))
+
+
+def _vector(what: str, name: str, t, dtype, dev, n: int):
+    if t.device != dev or t.dtype != dtype or t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
+        raise LoraError(-2, f"{what}: {name} must be {dtype} [{n}] on {dev}, contiguous")
+
+
+class BaseWeight:
+    """A base weight in 8 bits (lora_base_weight): W int8 [d_out][d_in] (unit column stride), scale float32 [d_out],
+    bias float32 [d_out] or None.  Keeps the tensors alive."""
+
+    def __init__(self, W, scale, bias=None):
+        torch = _torch()
+        if W.dim() != 2 or W.shape[0] < 1 or W.shape[1] < 1:
+            raise LoraError(-2, "W must be [d_out][d_in]")
+        self.ld = _rows_2d("BaseWeight", "W", W, (torch.int8,), W.device, 1)
+        self.d_out, self.d_in = int(W.shape[0]), int(W.shape[1])
+        for name, t in (("scale", scale), ("bias", bias)):
+            if t is not None:
+                _vector("BaseWeight", name, t, torch.float32, W.device, self.d_out)
+                if t.shape[0] != self.d_out:
+                    raise LoraError(-2, f"BaseWeight: {name} must be [{self.d_out}]")
+        self.W, self.scale, self.bias, self.device = W, scale, bias, W.device
+        self.c = lora_base_weight(_ptr(W), _ptr(scale), _ptr(bias), self.ld, self.d_in, self.d_out)
+        self.ref = ctypes.addressof(self.c)
+
+
+def lora_quantize_rows(x, q, scale):
+    """q[t] = rint(127 x[t] / max|x[t]|) and scale[t] = max|x[t]| / 127 for every row of x [T][d]
+    (bfloat16 or float32) into q int8 [T][d] and scale float32 [T]."""
+    torch = _torch()
+    what, dev = "lora_quantize_rows", x.device
+    if x.dim() != 2 or q.dim() != 2 or x.shape != q.shape:
+        raise LoraError(-2, f"{what}: x and q must be of one shape [T][d]")
+    ldx = _rows_2d(what, "x", x, (torch.bfloat16, torch.float32), dev, 1)
+    ldq = _rows_2d(what, "q", q, (torch.int8,), dev, 1)
+    _vector(what, "scale", scale, torch.float32, dev, x.shape[0])
+    with _device_guard(dev):
+        _check(lib().lora_quantize_rows(_ptr(x), ldx, _dtype_code(x), x.shape[0], x.shape[1], _ptr(q), ldq, _ptr(scale),
+                                        _stream(x)), what)
+
+
+def lora_base_product(weight: BaseWeight, q, q_scale, y):
+    """y[t][o] = q_scale[t] scale[o] sum_c q[t][c] W[o][c] (+ bias[o]) for every row of q int8 [T][d_in] into
+    y [T][>= d_out] (bfloat16 or float32; further rows and columns are left as they are)."""
+    torch = _torch()
+    what, dev = "lora_base_product", weight.device
+    ldq = _rows_2d(what, "q", q, (torch.int8,), dev, weight.d_in)
+    T = q.shape[0]
+    if q.shape[1] != weight.d_in:
+        raise LoraError(-2, f"{what}: q must be [T][{weight.d_in}]")
+    ldy = _rows_2d(what, "y", y, (torch.bfloat16, torch.float32), dev, weight.d_out, T)
+    _vector(what, "q_scale", q_scale, torch.float32, dev, T)
+    with _device_guard(dev):
+        _check(lib().lora_base_product(weight.ref, _ptr(q), ldq, _ptr(q_scale), T, _ptr(y), ldy, _dtype_code(y),
+                                       _stream(y)), what)
+
+
+def lora_base_workspace_size(weight: BaseWeight, n_tokens: int) -> int:
+    return int(lib().lora_base_workspace_size(weight.ref, n_tokens))
+
+
+def new_base_workspace(weight: BaseWeight, n_tokens: int):
+    """A workspace for lora_base_apply on up to n_tokens rows of this weight."""
+    return _torch().empty(max(lora_base_workspace_size(weight, n_tokens), 16), dtype=_torch().uint8, device=weight.device)
+
+
+def lora_base_apply(weight: BaseWeight, x, y, ws):
+    """lora_quantize_rows and lora_base_product in one call: y [T][>= d_out] from x [T][d_in] of the same type, the
+    quantised rows in the uint8 workspace ws (new_base_workspace)."""
+    torch = _torch()
+    what, dev = "lora_base_apply", weight.device
+    ldx = _rows_2d(what, "x", x, (torch.bfloat16, torch.float32), dev, weight.d_in)
+    T = x.shape[0]
+    if x.shape[1] != weight.d_in:
+        raise LoraError(-2, f"{what}: x must be [T][{weight.d_in}]")
+    ldy = _rows_2d(what, "y", y, (x.dtype,), dev, weight.d_out, T)
+    _vector(what, "ws", ws, torch.uint8, dev, 0)
+    with _device_guard(dev):
+        _check(lib().lora_base_apply(weight.ref, _ptr(x), ldx, T, _ptr(y), ldy, _dtype_code(x), _ptr(ws), ws.numel(),
+                                     _stream(y)), what)
+
+
+class Rotary:
+    """Rotary positions of one model (lora_rotary): freq float64 [rot_dim / 2] on the device, radians per position
+    (lora_rotary_frequencies), the heads' size, which values are pairs, and a factor of the rotated ones."""
+
+    def __init__(self, freq, head_dim: int, interleaved: bool = False, mscale: float = 1.0):
+        if freq.device.type != "cuda":
+            raise LoraError(-1, "Rotary: freq must be in device memory")
+        if freq.numel() < 1 or 2 * freq.numel() > head_dim:
+            raise LoraError(-2, "Rotary: freq must be [rot_dim / 2] with rot_dim <= head_dim")
+        _vector("Rotary", "freq", freq, _torch().float64, freq.device, freq.numel())
+        self.freq, self.device, self.head_dim = freq, freq.device, int(head_dim)
+        self.c = lora_rotary(_ptr(freq), self.head_dim, 2 * freq.numel(), int(bool(interleaved)), float(mscale))
+        self.ref = ctypes.addressof(self.c)
+
+
+def lora_rotary_apply(rotary: Rotary, positions, src: Sequence, dst: Optional[Sequence] = None, inverse: bool = False):
+    """Rotates the heads of src, up to 8 tensors [T][heads][head_dim] of the same tokens (any token and head
+    strides), into dst (in place by default).  positions int32 [T]; tokens of a negative position are skipped."""
+    torch = _torch()
+    what, dev = "lora_rotary_apply", rotary.device
+    dst = src if dst is None else dst
+    n, T = len(src), positions.shape[0] if positions.dim() else 0
+    if not 1 <= n <= LORA_MAX_SLICES or len(dst) != n:
+        raise LoraError(-2, f"{what}: 1 to {LORA_MAX_SLICES} tensors, as many in dst as in src")
+    _vector(what, "positions", positions, torch.int32, dev, T)
+    t0 = src[0].dtype
+    if t0 not in (torch.bfloat16, torch.float32):
+        raise LoraError(-2, f"{what}: heads must be bfloat16 or float32 (got {t0})")
+    slices = (lora_rotary_slice * n)()
+    for i in range(n):
+        a, b = src[i], dst[i]
+        for t in (a, b) if b is not a else (a,):
+            if t.dim() != 3 or t.shape[0] != T or t.shape[2] != rotary.head_dim or t.shape != a.shape:
+                raise LoraError(-2, f"{what}: heads must be [{T}][heads][{rotary.head_dim}] (got {tuple(t.shape)})")
+            if t.dtype != t0 or t.device != dev:
+                raise LoraError(-2, f"{what}: heads must all be {t0} on {dev} (found {t.dtype} on {t.device})")
+            if t.stride(2) != 1 and t.shape[2] > 1:
+                raise LoraError(-2, f"{what}: heads must have unit stride within a head")
+        sa, sb = a.stride(), b.stride()
+        slices[i] = lora_rotary_slice(a.data_ptr(), b.data_ptr(), sa[0], sa[1], sb[0], sb[1], a.shape[1])
+    with _device_guard(dev):
+        _check(lib().lora_rotary_apply(rotary.ref, _ptr(positions), T, n, ctypes.addressof(slices), _dtype_code(src[0]),
+                                       int(bool(inverse)), _stream(positions)), what)
+
+
+def lora_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = LORA_ROTARY_PLAIN, factor: float = 1.0,
+                            length: float = 1.0, low: float = 0.0, high: float = 1.0):
+    """Frequencies float64 [rot_dim / 2] on the host (include/lora_base.h: the scalings of long contexts)."""
+    freq = _torch().empty(max(int(rot_dim), 0) // 2, dtype=_torch().float64)
+    _check(lib().lora_rotary_frequencies(int(scaling), float(base), int(rot_dim), float(factor), float(length),
+                                         float(low), float(high), _ptr(freq) if freq.numel() else None),
+           "lora_rotary_frequencies")
+    return freq
 
 
 def lora_read_device_errors(plan) -> int:

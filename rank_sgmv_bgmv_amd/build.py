@@ -24,7 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "liblora_hip.so")
-SOURCES = ["lora_api.hip", "lora_plan.hip", "lora_valu.hip", "lora_mfma.hip", "lora_merge.hip", "lora_calib.hip"]
+SOURCES = ["lora_api.hip", "lora_plan.hip", "lora_valu.hip", "lora_mfma.hip", "lora_merge.hip", "lora_calib.hip",
+           "lora_base_api.hip", "lora_quantize.hip", "lora_product.hip", "lora_rotary.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -46,10 +46,6 @@ const Tune &tune() {
   return t;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int elem_bytes(lora_dtype d) { return d == LORA_BF16 ? 2 : 4; }
-
 struct BatchDims {
   int T, S, K, per_token;
 };
@@ -82,16 +78,6 @@ lora_status check_pool(const lora_pool *p) {
   if (st) return st;
   if (!p->A || !p->B) return LORA_EINVAL;
   return LORA_OK;
-}
-
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-  const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
-  return na && nb && x < y + nb && y < x + na;
-}
-
-size_t span_bytes(int rows, int64_t ld, int cols, int eb) {
-  if (rows <= 0) return 0;
-  return (size_t(rows - 1) * size_t(ld) + size_t(cols)) * size_t(eb);
 }
 
 struct Plan {

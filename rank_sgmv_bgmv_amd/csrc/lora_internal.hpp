@@ -65,6 +65,18 @@ struct PlanLayout {
 // The plan kernel keeps its working arrays in LDS when they fit in this budget.
 constexpr size_t kPlanLdsBudget = 144 * 1024;
 
+// Host checks shared by the C-ABI entry points.
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline int elem_bytes(lora_dtype d) { return d == LORA_BF16 ? 2 : 4; }
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+  const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+  return na && nb && x < y + nb && y < x + na;
+}
+inline size_t span_bytes(int rows, int64_t ld, int cols, int eb) {
+  if (rows <= 0) return 0;
+  return (size_t(rows - 1) * size_t(ld) + size_t(cols)) * size_t(eb);
+}
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 inline PlanLayout plan_layout(int S, int T, int n) {
