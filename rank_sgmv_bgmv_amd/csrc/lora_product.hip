@@ -6,6 +6,8 @@
 // which is the order in which v_mfma_i32_16x16x64_i8 takes them: a lane holds
 // 16 consecutive values of one row.
 
+#include <type_traits>
+
 #include "lora_base.hpp"
 #include "lora_device.hpp"
 
@@ -104,15 +106,218 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
   }
 }
 
+// ------------------------------------------------------------ large tiles --
+//
+// MT * 64 channels x NT * 64 tokens by four waves (2 x 2, each MT x NT blocks
+// of v_mfma_i32_32x32x32_i8).  The sum's axis goes in stages of 128 values,
+// copied to LDS without passing registers, two stages in LDS: stage i + 2 is on
+// its way while stage i + 1 lies ready and i is multiplied.  Within a stage
+// the operands of one 32-value step are read from LDS while the step before
+// is multiplied, across stages too, so the matrix unit waits for nothing but
+// the one barrier of a stage.
+//
+// A row of a stage is 128 bytes, eight 16-byte pieces; piece c of row r lies
+// at place c ^ (r & 7), so that eight lanes reading one piece of neighbouring
+// rows meet every bank once.  The copy writes LDS in lane order, so the lanes
+// take their global pieces in that order instead.
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+constexpr int kStage = 128;
+
+// 16 bytes a lane from base + off straight to LDS at `lds` (wave-uniform) + 16 lane.
+__device__ __forceinline__ void copy_to_lds(const int8_t *base, uint32_t off, uint32_t lds) {
+  __builtin_amdgcn_global_load_lds((const LORA_GLOBAL void *)((const LORA_GLOBAL char *)base + off),
+                                   (__attribute__((address_space(3))) void *)(uintptr_t)lds, 16, 0, 0);
+}
+// Every copy of this wave has landed and every LDS read has returned, for all waves.
+__device__ __forceinline__ void stage_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+template <int MT, int NT>
+struct TileShape {
+  static constexpr int kO = MT * 64, kT = NT * 64;                 // channels and tokens of a tile
+  static constexpr int kBytes = (kO + kT) * kStage;                // one stage
+  static constexpr int kScales = 2 * kBytes;                       // then the scales and biases
+  static constexpr int kLds = kScales + (2 * kO + kT) * 4;
+};
+
+template <typename E, int MT, int NT>
+__global__ __launch_bounds__(256, 1) void product_tile_kernel(ProductArgs a, int tiles_o) {
+  typedef TileShape<MT, NT> S;
+  extern __shared__ __align__(16) int8_t lds[];
+  const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64);
+  const int o0 = int(blockIdx.x) % tiles_o * S::kO;
+  const int64_t t0 = int64_t(int(blockIdx.x) / tiles_o) * S::kT;
+  const int n_o = min(S::kO, a.d_out - o0), n_t = int(min(int64_t(S::kT), a.T - t0));
+
+  float *s_o = reinterpret_cast<float *>(lds + S::kScales), *b_o = s_o + S::kO, *s_t = b_o + S::kO;
+  for (int i = tid; i < S::kO; i += 256) {
+    const int o = o0 + min(i, n_o - 1);
+    s_o[i] = gload<float>(a.w_scale + o);
+    b_o[i] = bias_of(a, o);
+  }
+  for (int i = tid; i < S::kT; i += 256) s_t[i] = gload<float>(a.q_scale + t0 + min(i, n_t - 1));
+
+  // this lane's pieces: 2 MT rows of W and 2 NT of q a stage (rows past the end: the last row again)
+  const int8_t *W = a.W + int64_t(o0) * a.ldw, *q = a.q + t0 * a.ldq;
+  const int piece = (lane % 8) ^ (lane / 8);
+  uint32_t off[2 * (MT + NT)];
+#pragma unroll
+  for (int i = 0; i < 2 * MT; ++i)
+    off[i] = uint32_t(min((wave * 2 * MT + i) * 8 + lane / 8, n_o - 1)) * uint32_t(a.ldw) + piece * 16;
+#pragma unroll
+  for (int i = 0; i < 2 * NT; ++i)
+    off[2 * MT + i] = uint32_t(min((wave * 2 * NT + i) * 8 + lane / 8, n_t - 1)) * uint32_t(a.ldq) + piece * 16;
+  const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) int8_t *)lds));
+
+  auto copy = [&](int i, int stage, uint32_t back) {
+    const uint32_t at = lds0 + (stage & 1) * S::kBytes;
+    if (i < 2 * MT)
+      copy_to_lds(W + stage * kStage, off[i] - back, at + (wave * 2 * MT + i) * 1024);
+    else
+      copy_to_lds(q + stage * kStage, off[i] - back, at + S::kO * kStage + (wave * 2 * NT + i - 2 * MT) * 1024);
+  };
+  // pieces past the end of the rows are not read: the stage's first piece stands in (and is masked below)
+  auto back_of = [&](int stage) -> uint32_t { return stage * kStage + piece * 16 < a.d_in ? 0u : piece * 16u; };
+
+  const int wm = wave / 2, wn = wave % 2;
+  const int8_t *lw = lds + (wm * MT * 32 + lane % 32) * kStage, *lx = lds + (S::kO + wn * NT * 32 + lane % 32) * kStage;
+  i32x4 fw[2][MT], fx[2][NT];
+  i32x16 acc[MT][NT] = {};
+  auto read = [&](int stage, int s, int set) {
+    const int p = (stage & 1) * S::kBytes + (((s * 2 + lane / 32) ^ (lane & 7)) * 16);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) fw[set][i] = *reinterpret_cast<const i32x4 *>(lw + p + i * 32 * kStage);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fx[set][j] = *reinterpret_cast<const i32x4 *>(lx + p + j * 32 * kStage);
+  };
+
+  const int n = (a.d_in + kStage - 1) / kStage;
+  for (int st = 0; st < min(n, 2); ++st) {
+    const uint32_t back = back_of(st);
+#pragma unroll
+    for (int i = 0; i < 2 * (MT + NT); ++i) copy(i, st, back);
+  }
+  stage_barrier();
+  read(0, 0, 0);
+
+  auto stage = [&](int i, auto more, auto masked) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      uint32_t back = 0;
+      if (s == 3) {
+        stage_barrier();
+        if constexpr (more) back = back_of(i + 2);
+      }
+      read(s == 3 ? i + 1 : i, (s + 1) & 3, (s + 1) & 1);
+      if constexpr (masked) {
+        // past the end of the sum's axis q counts as zero
+        const bool in = i * kStage + s * 32 + lane / 32 * 16 < a.d_in;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) fx[s & 1][j][e] = in ? fx[s & 1][j][e] : 0;
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          if constexpr (more) {
+            constexpr int kCopies = 2 * (MT + NT), kMul = MT * NT;
+            if (s == 3)
+              for (int c = (m * NT + j) * kCopies / kMul; c < (m * NT + j + 1) * kCopies / kMul; ++c) copy(c, i + 2, back);
+          }
+          acc[m][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[s & 1][m], fx[s & 1][j], acc[m][j], 0, 0, 0);
+        }
+      // the order of issue: LDS reads spread over the products, then the copies
+      constexpr int kReads = MT + NT, kMul = MT * NT, kCopies = 2 * kReads;
+      static_assert(kReads <= kMul, "a read goes with a product");
+#pragma unroll
+      for (int k = 0; k < kReads; ++k) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(8, 1, 0);
+      }
+      if (more && s == 3) {
+#pragma unroll
+        for (int k = 0; k < kMul - kReads; ++k) {
+          __builtin_amdgcn_sched_group_barrier(0x20, kCopies / (kMul - kReads), 0);
+          __builtin_amdgcn_sched_group_barrier(8, 1, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  int i = 0;
+  for (; i < n - 2; ++i) stage(i, std::true_type{}, std::false_type{});
+  for (; i < n - 1; ++i) stage(i, std::false_type{}, std::false_type{});
+  stage(i, std::false_type{}, std::true_type{});
+
+  // Results: 32 tokens at a time through LDS, so that a token's channels leave in whole lines.
+  __syncthreads();
+  constexpr int kRow = MT * 32 * int(sizeof(E)) + 16;
+  int8_t *mine = lds + wave * 32 * kRow;
+  constexpr int kVec = 16 / int(sizeof(E)), kPer = MT * 32 / kVec;  // 16-byte vectors of a token's row
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const float sx = s_t[wn * NT * 32 + j * 32 + lane % 32];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int o = m * 32 + g * 8 + lane / 32 * 4;
+        const float4 sw = *reinterpret_cast<const float4 *>(s_o + wm * MT * 32 + o);
+        const float4 b = *reinterpret_cast<const float4 *>(b_o + wm * MT * 32 + o);
+        const float v0 = float(acc[m][j][g * 4]) * sx * sw.x + b.x, v1 = float(acc[m][j][g * 4 + 1]) * sx * sw.y + b.y;
+        const float v2 = float(acc[m][j][g * 4 + 2]) * sx * sw.z + b.z, v3 = float(acc[m][j][g * 4 + 3]) * sx * sw.w + b.w;
+        int8_t *p = mine + lane % 32 * kRow + o * int(sizeof(E));
+        if constexpr (sizeof(E) == 2)
+          *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf2(v0, v1), pack_bf2(v2, v3));
+        else
+          *reinterpret_cast<float4 *>(p) = make_float4(v0, v1, v2, v3);
+      }
+    __syncthreads();
+    for (int v = lane; v < 32 * kPer; v += 64) {
+      const int r = v / kPer, c = v % kPer * kVec;
+      const int tt = wn * NT * 32 + j * 32 + r, oo = wm * MT * 32 + c;
+      if (tt >= n_t || oo >= n_o) continue;
+      const int8_t *p = mine + r * kRow + c * int(sizeof(E));
+      E *y = static_cast<E *>(a.y) + (t0 + tt) * a.ldy + o0 + oo;
+      if (oo + kVec <= n_o && a.y_vec) {
+        gstore(y, *reinterpret_cast<const uint4 *>(p));
+      } else {
+        for (int e = 0; e < kVec; ++e)
+          if (oo + e < n_o) gstore(y + e, reinterpret_cast<const E *>(p)[e]);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename E, int MT, int NT>
+hipError_t launch_tiles(const ProductArgs &a, hipStream_t stream) {
+  typedef TileShape<MT, NT> S;
+  static const bool ready = raise_lds_limit(reinterpret_cast<const void *>(product_tile_kernel<E, MT, NT>), S::kLds);
+  (void)ready;
+  const int tiles_o = (a.d_out + S::kO - 1) / S::kO;
+  const int64_t tiles = int64_t(tiles_o) * ((a.T + S::kT - 1) / S::kT);
+  product_tile_kernel<E, MT, NT><<<dim3(uint32_t(tiles)), 256, S::kLds, stream>>>(a, tiles_o);
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
+  ProductArgs a = args;
+  a.y_vec = aligned16(a.y) && a.ldy * int64_t(sizeof(E)) % 16 == 0;
+  const bool lines = aligned16(a.q) && aligned16(a.W) && a.ldq % 16 == 0 && a.ldw % 16 == 0 && a.d_in % 16 == 0 &&
+                     a.ldq <= (1 << 22) && a.ldw <= (1 << 22);
+  if (lines && a.T > 128) return launch_tiles<E, 4, 4>(a, stream);
+  const dim3 grid((a.d_out + kAnyTile - 1) / kAnyTile, (a.T + kAnyTile - 1) / kAnyTile);
+  product_any_kernel<E><<<grid, 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_product(const ProductArgs &a, int dtype, hipStream_t stream) {
-  const dim3 grid((a.d_out + kAnyTile - 1) / kAnyTile, (a.T + kAnyTile - 1) / kAnyTile);
-  if (dtype == LORA_BF16)
-    product_any_kernel<uint16_t><<<grid, 256, 0, stream>>>(a);
-  else
-    product_any_kernel<float><<<grid, 256, 0, stream>>>(a);
-  return hipGetLastError();
+  return dtype == LORA_BF16 ? launch_typed<uint16_t>(a, stream) : launch_typed<float>(a, stream);
 }
 
 }  // namespace lora
