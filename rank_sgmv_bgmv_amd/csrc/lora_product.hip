@@ -131,30 +131,27 @@ __device__ __forceinline__ void copy_to_lds(const int8_t *base, uint32_t off, ui
 // Every copy of this wave has landed and every LDS read has returned, for all waves.
 __device__ __forceinline__ void stage_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <int MT, int NT>
+template <typename E, int MT, int NT>
 struct TileShape {
-  static constexpr int kO = MT * 64, kT = NT * 64;                 // channels and tokens of a tile
-  static constexpr int kBytes = (kO + kT) * kStage;                // one stage
-  static constexpr int kScales = 2 * kBytes;                       // then the scales and biases
+  static constexpr int kO = MT * 64, kT = NT * 64;   // channels and tokens of a tile
+  static constexpr int kBytes = (kO + kT) * kStage;  // one stage
+  // results on their way out: up to 256 bytes of channels of each of a wave's tokens
+  static constexpr int kOutM = MT * 32 * int(sizeof(E)) <= 256 ? MT : 256 / (32 * int(sizeof(E)));
+  static constexpr int kOutRow = kOutM * 32 * int(sizeof(E)), kOutPitch = kOutRow + 16;
+  static constexpr int kOut = 4 * NT * 32 * kOutPitch;
+  static constexpr int kScales = 2 * kBytes > kOut ? 2 * kBytes : kOut;  // then the scales and biases
   static constexpr int kLds = kScales + (2 * kO + kT) * 4;
+  static_assert(MT % kOutM == 0 && kLds <= kMaxLdsBytes, "");
 };
 
 template <typename E, int MT, int NT>
 __global__ __launch_bounds__(256, 1) void product_tile_kernel(ProductArgs a, int tiles_o) {
-  typedef TileShape<MT, NT> S;
+  typedef TileShape<E, MT, NT> S;
   extern __shared__ __align__(16) int8_t lds[];
   const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64);
   const int o0 = int(blockIdx.x) % tiles_o * S::kO;
   const int64_t t0 = int64_t(int(blockIdx.x) / tiles_o) * S::kT;
   const int n_o = min(S::kO, a.d_out - o0), n_t = int(min(int64_t(S::kT), a.T - t0));
-
-  float *s_o = reinterpret_cast<float *>(lds + S::kScales), *b_o = s_o + S::kO, *s_t = b_o + S::kO;
-  for (int i = tid; i < S::kO; i += 256) {
-    const int o = o0 + min(i, n_o - 1);
-    s_o[i] = gload<float>(a.w_scale + o);
-    b_o[i] = bias_of(a, o);
-  }
-  for (int i = tid; i < S::kT; i += 256) s_t[i] = gload<float>(a.q_scale + t0 + min(i, n_t - 1));
 
   // this lane's pieces: 2 MT rows of W and 2 NT of q a stage (rows past the end: the last row again)
   const int8_t *W = a.W + int64_t(o0) * a.ldw, *q = a.q + t0 * a.ldq;
@@ -196,6 +193,13 @@ __global__ __launch_bounds__(256, 1) void product_tile_kernel(ProductArgs a, int
 #pragma unroll
     for (int i = 0; i < 2 * (MT + NT); ++i) copy(i, st, back);
   }
+  float *s_o = reinterpret_cast<float *>(lds + S::kScales), *b_o = s_o + S::kO, *s_t = b_o + S::kO;
+  for (int i = tid; i < S::kO; i += 256) {
+    const int o = o0 + min(i, n_o - 1);
+    s_o[i] = gload<float>(a.w_scale + o);
+    b_o[i] = bias_of(a, o);
+  }
+  for (int i = tid; i < S::kT; i += 256) s_t[i] = gload<float>(a.q_scale + t0 + min(i, n_t - 1));
   stage_barrier();
   read(0, 0, 0);
 
@@ -250,50 +254,75 @@ __global__ __launch_bounds__(256, 1) void product_tile_kernel(ProductArgs a, int
   for (; i < n - 1; ++i) stage(i, std::false_type{}, std::false_type{});
   stage(i, std::false_type{}, std::true_type{});
 
-  // Results: 32 tokens at a time through LDS, so that a token's channels leave in whole lines.
-  __syncthreads();
-  constexpr int kRow = MT * 32 * int(sizeof(E)) + 16;
-  int8_t *mine = lds + wave * 32 * kRow;
-  constexpr int kVec = 16 / int(sizeof(E)), kPer = MT * 32 / kVec;  // 16-byte vectors of a token's row
+  // Results through LDS, so that a token's channels leave in whole lines.  Each
+  // wave has its own place there, which it writes and reads in order: no
+  // barrier after the first, and stores stay in flight.
+  stage_barrier();
+  int8_t *mine = lds + wave * NT * 32 * S::kOutPitch;
+  constexpr int kVec = 16 / int(sizeof(E)), kPer = S::kOutRow / 16;  // 16-byte vectors of a token's row
+  const bool whole = a.y_vec && n_o == S::kO && n_t == S::kT;
+  float sx[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const float sx = s_t[wn * NT * 32 + j * 32 + lane % 32];
+  for (int j = 0; j < NT; ++j) sx[j] = s_t[wn * NT * 32 + j * 32 + lane % 32];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+  for (int m0 = 0; m0 < MT; m0 += S::kOutM) {
+    float4 sw[S::kOutM * 4], b[S::kOutM * 4];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int o = m * 32 + g * 8 + lane / 32 * 4;
-        const float4 sw = *reinterpret_cast<const float4 *>(s_o + wm * MT * 32 + o);
-        const float4 b = *reinterpret_cast<const float4 *>(b_o + wm * MT * 32 + o);
-        const float v0 = float(acc[m][j][g * 4]) * sx * sw.x + b.x, v1 = float(acc[m][j][g * 4 + 1]) * sx * sw.y + b.y;
-        const float v2 = float(acc[m][j][g * 4 + 2]) * sx * sw.z + b.z, v3 = float(acc[m][j][g * 4 + 3]) * sx * sw.w + b.w;
-        int8_t *p = mine + lane % 32 * kRow + o * int(sizeof(E));
+    for (int k = 0; k < S::kOutM * 4; ++k) {
+      const int o = wm * MT * 32 + m0 * 32 + k * 8 + lane / 32 * 4;
+      sw[k] = *reinterpret_cast<const float4 *>(s_o + o);
+      b[k] = *reinterpret_cast<const float4 *>(b_o + o);
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int k = 0; k < S::kOutM * 4; ++k) {
+        const i32x16 &c = acc[m0 + k / 4][j];
+        const int g = k % 4 * 4;
+        const float v0 = float(c[g]) * sx[j] * sw[k].x + b[k].x, v1 = float(c[g + 1]) * sx[j] * sw[k].y + b[k].y;
+        const float v2 = float(c[g + 2]) * sx[j] * sw[k].z + b[k].z, v3 = float(c[g + 3]) * sx[j] * sw[k].w + b[k].w;
+        int8_t *p = mine + (j * 32 + lane % 32) * S::kOutPitch + (k * 8 + lane / 32 * 4) * int(sizeof(E));
         if constexpr (sizeof(E) == 2)
           *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf2(v0, v1), pack_bf2(v2, v3));
         else
           *reinterpret_cast<float4 *>(p) = make_float4(v0, v1, v2, v3);
       }
-    __syncthreads();
-    for (int v = lane; v < 32 * kPer; v += 64) {
-      const int r = v / kPer, c = v % kPer * kVec;
-      const int tt = wn * NT * 32 + j * 32 + r, oo = wm * MT * 32 + c;
-      if (tt >= n_t || oo >= n_o) continue;
-      const int8_t *p = mine + r * kRow + c * int(sizeof(E));
-      E *y = static_cast<E *>(a.y) + (t0 + tt) * a.ldy + o0 + oo;
-      if (oo + kVec <= n_o && a.y_vec) {
-        gstore(y, *reinterpret_cast<const uint4 *>(p));
-      } else {
-        for (int e = 0; e < kVec; ++e)
-          if (oo + e < n_o) gstore(y + e, reinterpret_cast<const E *>(p)[e]);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    const int tt = wn * NT * 32, oo = wm * MT * 32 + m0 * 32;
+    E *y = static_cast<E *>(a.y) + (t0 + tt) * a.ldy + o0 + oo;
+    if (whole) {
+      constexpr int kBatch = 8;
+      static_assert(NT * 32 * kPer % (64 * kBatch) == 0, "");
+#pragma unroll 1
+      for (int v = lane; v < NT * 32 * kPer; v += 64 * kBatch) {
+        uint4 r[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          r[k] = *reinterpret_cast<const uint4 *>(mine + (v + k * 64) / kPer * S::kOutPitch + (v + k * 64) % kPer * 16);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) gstore(y + (v + k * 64) / kPer * a.ldy + (v + k * 64) % kPer * kVec, r[k]);
+      }
+    } else {
+      for (int v = lane; v < NT * 32 * kPer; v += 64) {
+        const int r = v / kPer, c = v % kPer * kVec;
+        if (tt + r >= n_t || oo + c >= n_o) continue;
+        const int8_t *p = mine + r * S::kOutPitch + c * int(sizeof(E));
+        if (oo + c + kVec <= n_o && a.y_vec) {
+          gstore(y + r * a.ldy + c, *reinterpret_cast<const uint4 *>(p));
+        } else {
+          for (int e = 0; e < kVec; ++e)
+            if (oo + c + e < n_o) gstore(y + r * a.ldy + c + e, reinterpret_cast<const E *>(p)[e]);
+        }
       }
     }
-    __syncthreads();
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
 template <typename E, int MT, int NT>
 hipError_t launch_tiles(const ProductArgs &a, hipStream_t stream) {
-  typedef TileShape<MT, NT> S;
+  typedef TileShape<E, MT, NT> S;
   static const bool ready = raise_lds_limit(reinterpret_cast<const void *>(product_tile_kernel<E, MT, NT>), S::kLds);
   (void)ready;
   const int tiles_o = (a.d_out + S::kO - 1) / S::kO;
