@@ -108,19 +108,24 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
 
 // ------------------------------------------------------------ large tiles --
 //
-// MT * 64 channels x NT * 64 tokens by four waves (2 x 2, each MT x NT blocks
-// of v_mfma_i32_32x32x32_i8).  The sum's axis goes in stages of 128 values,
+// MT * 32 channels x NT * 32 tokens by four waves (2 x 2, each MT x NT blocks
+// of v_mfma_i32_16x16x64_i8).  The sum's axis goes in stages of 128 values,
 // copied to LDS without passing registers, two stages in LDS: stage i + 2 is on
 // its way while stage i + 1 lies ready and i is multiplied.  Within a stage
-// the operands of one 32-value step are read from LDS while the step before
+// the operands of one 64-value step are read from LDS while the step before
 // is multiplied, across stages too, so the matrix unit waits for nothing but
 // the one barrier of a stage.
+//
+// What bounds it is power: four waves on every CU that only multiply random
+// 8-bit numbers run at 1.79 GHz (3.68 POP/s) with 16 x 16 blocks and at 1.44
+// GHz (2.97 POP/s) with 32 x 32 ones, which move twice the sums.  So 16 x 16
+// blocks, and the largest tile that fits the registers, 8 x 8 blocks a wave,
+// which reads the fewest operands from LDS for each product.
 //
 // A row of a stage is 128 bytes, eight 16-byte pieces; piece c of row r lies
 // at place c ^ (r & 7), so that eight lanes reading one piece of neighbouring
 // rows meet every bank once.  The copy writes LDS in lane order, so the lanes
 // take their global pieces in that order instead.
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 constexpr int kStage = 128;
 
 // 16 bytes a lane from base + off straight to LDS at `lds` (wave-uniform) + 16 lane.
@@ -128,17 +133,45 @@ __device__ __forceinline__ void copy_to_lds(const int8_t *base, uint32_t off, ui
   __builtin_amdgcn_global_load_lds((const LORA_GLOBAL void *)((const LORA_GLOBAL char *)base + off),
                                    (__attribute__((address_space(3))) void *)(uintptr_t)lds, 16, 0, 0);
 }
+// Waits as the compiler counts them: after one it adds none of its own for what came before.
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }  // lgkmcnt(0)
 // Every copy of this wave has landed and every LDS read has returned, for all waves.
-__device__ __forceinline__ void stage_barrier() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+__device__ __forceinline__ void stage_barrier() {
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  asm volatile("s_barrier" ::: "memory");
+}
+
+// c += a b^T on a 16 x 16 block, c kept where it is: given the choice, the
+// compiler writes the sums elsewhere and moves 200 registers back each stage.
+// It sees no matrix instruction here, so the waits that it would insert stand
+// at the places that need them (settle, settled).
+__device__ __forceinline__ void multiply(i32x4 &c, const i32x4 &a, const i32x4 &b) {
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+// Between vector instructions that write operands and the products that read them (2 wait states).
+__device__ __forceinline__ void settle() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 3");
+  __builtin_amdgcn_sched_barrier(0);
+}
+// Between the last products and reads of their sums (at most 19 wait states).
+template <int M, int N>
+__device__ __forceinline__ void settled(i32x4 (&c)[M][N]) {
+  asm volatile("s_nop 15\n\ts_nop 15");
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+#pragma unroll
+    for (int j = 0; j < N; ++j) asm volatile("" : "+a"(c[m][j]));
+}
 
 template <typename E, int MT, int NT>
 struct TileShape {
-  static constexpr int kO = MT * 64, kT = NT * 64;   // channels and tokens of a tile
+  static constexpr int kO = MT * 32, kT = NT * 32;   // channels and tokens of a tile
   static constexpr int kBytes = (kO + kT) * kStage;  // one stage
   // results on their way out: up to 256 bytes of channels of each of a wave's tokens
-  static constexpr int kOutM = MT * 32 * int(sizeof(E)) <= 256 ? MT : 256 / (32 * int(sizeof(E)));
-  static constexpr int kOutRow = kOutM * 32 * int(sizeof(E)), kOutPitch = kOutRow + 16;
-  static constexpr int kOut = 4 * NT * 32 * kOutPitch;
+  static constexpr int kOutM = MT * 16 * int(sizeof(E)) <= 256 ? MT : 256 / (16 * int(sizeof(E)));
+  static constexpr int kOutRow = kOutM * 16 * int(sizeof(E)), kOutPitch = kOutRow + 16;
+  static constexpr int kOut = 4 * NT * 16 * kOutPitch;
   static constexpr int kScales = 2 * kBytes > kOut ? 2 * kBytes : kOut;  // then the scales and biases
   static constexpr int kLds = kScales + (2 * kO + kT) * 4;
   static_assert(MT % kOutM == 0 && kLds <= kMaxLdsBytes, "");
@@ -153,45 +186,45 @@ __global__ __launch_bounds__(256, 1) void product_tile_kernel(ProductArgs a, int
   const int64_t t0 = int64_t(int(blockIdx.x) / tiles_o) * S::kT;
   const int n_o = min(S::kO, a.d_out - o0), n_t = int(min(int64_t(S::kT), a.T - t0));
 
-  // this lane's pieces: 2 MT rows of W and 2 NT of q a stage (rows past the end: the last row again)
+  // this lane's pieces: MT rows of W and NT of q a stage (rows past the end: the last row again)
   const int8_t *W = a.W + int64_t(o0) * a.ldw, *q = a.q + t0 * a.ldq;
   const int piece = (lane % 8) ^ (lane / 8);
-  uint32_t off[2 * (MT + NT)];
+  uint32_t off[MT + NT];
 #pragma unroll
-  for (int i = 0; i < 2 * MT; ++i)
-    off[i] = uint32_t(min((wave * 2 * MT + i) * 8 + lane / 8, n_o - 1)) * uint32_t(a.ldw) + piece * 16;
+  for (int i = 0; i < MT; ++i)
+    off[i] = uint32_t(min((wave * MT + i) * 8 + lane / 8, n_o - 1)) * uint32_t(a.ldw) + piece * 16;
 #pragma unroll
-  for (int i = 0; i < 2 * NT; ++i)
-    off[2 * MT + i] = uint32_t(min((wave * 2 * NT + i) * 8 + lane / 8, n_t - 1)) * uint32_t(a.ldq) + piece * 16;
+  for (int i = 0; i < NT; ++i)
+    off[MT + i] = uint32_t(min((wave * NT + i) * 8 + lane / 8, n_t - 1)) * uint32_t(a.ldq) + piece * 16;
   const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) int8_t *)lds));
 
   auto copy = [&](int i, int stage, uint32_t back) {
     const uint32_t at = lds0 + (stage & 1) * S::kBytes;
-    if (i < 2 * MT)
-      copy_to_lds(W + stage * kStage, off[i] - back, at + (wave * 2 * MT + i) * 1024);
+    if (i < MT)
+      copy_to_lds(W + stage * kStage, off[i] - back, at + (wave * MT + i) * 1024);
     else
-      copy_to_lds(q + stage * kStage, off[i] - back, at + S::kO * kStage + (wave * 2 * NT + i - 2 * MT) * 1024);
+      copy_to_lds(q + stage * kStage, off[i] - back, at + S::kO * kStage + (wave * NT + i - MT) * 1024);
   };
   // pieces past the end of the rows are not read: the stage's first piece stands in (and is masked below)
   auto back_of = [&](int stage) -> uint32_t { return stage * kStage + piece * 16 < a.d_in ? 0u : piece * 16u; };
 
   const int wm = wave / 2, wn = wave % 2;
-  const int8_t *lw = lds + (wm * MT * 32 + lane % 32) * kStage, *lx = lds + (S::kO + wn * NT * 32 + lane % 32) * kStage;
+  const int8_t *lw = lds + (wm * MT * 16 + lane % 16) * kStage, *lx = lds + (S::kO + wn * NT * 16 + lane % 16) * kStage;
   i32x4 fw[2][MT], fx[2][NT];
-  i32x16 acc[MT][NT] = {};
-  auto read = [&](int stage, int s, int set) {
-    const int p = (stage & 1) * S::kBytes + (((s * 2 + lane / 32) ^ (lane & 7)) * 16);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) fw[set][i] = *reinterpret_cast<const i32x4 *>(lw + p + i * 32 * kStage);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) fx[set][j] = *reinterpret_cast<const i32x4 *>(lx + p + j * 32 * kStage);
+  i32x4 acc[MT][NT] = {};
+  auto place = [&](int stage, int s) { return (stage & 1) * S::kBytes + (((s * 4 + lane / 16) ^ (lane & 7)) * 16); };
+  auto read = [&](int k, int p, int s) {
+    if (k < MT)
+      fw[s][k] = *reinterpret_cast<const i32x4 *>(lw + p + k * 16 * kStage);
+    else
+      fx[s][k - MT] = *reinterpret_cast<const i32x4 *>(lx + p + (k - MT) * 16 * kStage);
   };
 
   const int n = (a.d_in + kStage - 1) / kStage;
   for (int st = 0; st < min(n, 2); ++st) {
     const uint32_t back = back_of(st);
 #pragma unroll
-    for (int i = 0; i < 2 * (MT + NT); ++i) copy(i, st, back);
+    for (int i = 0; i < MT + NT; ++i) copy(i, st, back);
   }
   float *s_o = reinterpret_cast<float *>(lds + S::kScales), *b_o = s_o + S::kO, *s_t = b_o + S::kO;
   for (int i = tid; i < S::kO; i += 256) {
@@ -201,87 +234,77 @@ __global__ __launch_bounds__(256, 1) void product_tile_kernel(ProductArgs a, int
   }
   for (int i = tid; i < S::kT; i += 256) s_t[i] = gload<float>(a.q_scale + t0 + min(i, n_t - 1));
   stage_barrier();
-  read(0, 0, 0);
+#pragma unroll
+  for (int k = 0; k < MT + NT; ++k) read(k, place(0, 0), 0);
 
+  // The order of issue is the order written: LDS reads spread over half the
+  // products of a step, the copies over the other half.
+  constexpr int kReads = MT + NT, kEach = MT * NT / (2 * kReads);
+  static_assert(kEach >= 1, "a read or a copy goes with a product");
   auto stage = [&](int i, auto more, auto masked) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      uint32_t back = 0;
-      if (s == 3) {
-        stage_barrier();
-        if constexpr (more) back = back_of(i + 2);
-      }
-      read(s == 3 ? i + 1 : i, (s + 1) & 3, (s + 1) & 1);
+    for (int s = 0; s < 2; ++s) {
+      // the operands of this step were read half a step ago and more
+      if (s == 1) stage_barrier();
+      else wait_lds();
+      const int p = place(s ? i + 1 : i, s ^ 1);
+      const uint32_t back = more && s == 1 ? back_of(i + 2) : 0;
       if constexpr (masked) {
         // past the end of the sum's axis q counts as zero
-        const bool in = i * kStage + s * 32 + lane / 32 * 16 < a.d_in;
+        const bool in = i * kStage + s * 64 + lane / 16 * 16 < a.d_in;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) fx[s & 1][j][e] = in ? fx[s & 1][j][e] : 0;
+          for (int e = 0; e < 4; ++e) fx[s][j][e] = in ? fx[s][j][e] : 0;
+        settle();
       }
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if constexpr (more) {
-            constexpr int kCopies = 2 * (MT + NT), kMul = MT * NT;
-            if (s == 3)
-              for (int c = (m * NT + j) * kCopies / kMul; c < (m * NT + j + 1) * kCopies / kMul; ++c) copy(c, i + 2, back);
-          }
-          acc[m][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[s & 1][m], fx[s & 1][j], acc[m][j], 0, 0, 0);
+      for (int t = 0; t < MT * NT; ++t) {
+        if (t % kEach == 0) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (t / kEach < kReads)
+            read(t / kEach, p, s ^ 1);
+          else if (more && s == 1 && t / kEach - kReads < kReads)
+            copy(t / kEach - kReads, i + 2, back);
+          __builtin_amdgcn_sched_barrier(0);
         }
-      // the order of issue: LDS reads spread over the products, then the copies
-      constexpr int kReads = MT + NT, kMul = MT * NT, kCopies = 2 * kReads;
-      static_assert(kReads <= kMul, "a read goes with a product");
-#pragma unroll
-      for (int k = 0; k < kReads; ++k) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(8, 1, 0);
+        multiply(acc[t / NT][t % NT], fw[s][t / NT], fx[s][t % NT]);
       }
-      if (more && s == 3) {
-#pragma unroll
-        for (int k = 0; k < kMul - kReads; ++k) {
-          __builtin_amdgcn_sched_group_barrier(0x20, kCopies / (kMul - kReads), 0);
-          __builtin_amdgcn_sched_group_barrier(8, 1, 0);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
     }
   };
   int i = 0;
   for (; i < n - 2; ++i) stage(i, std::true_type{}, std::false_type{});
   for (; i < n - 1; ++i) stage(i, std::false_type{}, std::false_type{});
   stage(i, std::false_type{}, std::true_type{});
+  settled(acc);
 
   // Results through LDS, so that a token's channels leave in whole lines.  Each
   // wave has its own place there, which it writes and reads in order: no
   // barrier after the first, and stores stay in flight.
   stage_barrier();
-  int8_t *mine = lds + wave * NT * 32 * S::kOutPitch;
+  int8_t *mine = lds + wave * NT * 16 * S::kOutPitch;
   constexpr int kVec = 16 / int(sizeof(E)), kPer = S::kOutRow / 16;  // 16-byte vectors of a token's row
   const bool whole = a.y_vec && n_o == S::kO && n_t == S::kT;
   float sx[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) sx[j] = s_t[wn * NT * 32 + j * 32 + lane % 32];
+  for (int j = 0; j < NT; ++j) sx[j] = s_t[wn * NT * 16 + j * 16 + lane % 16];
 #pragma unroll
   for (int m0 = 0; m0 < MT; m0 += S::kOutM) {
-    float4 sw[S::kOutM * 4], b[S::kOutM * 4];
+    float4 sw[S::kOutM], b[S::kOutM];
 #pragma unroll
-    for (int k = 0; k < S::kOutM * 4; ++k) {
-      const int o = wm * MT * 32 + m0 * 32 + k * 8 + lane / 32 * 4;
+    for (int k = 0; k < S::kOutM; ++k) {
+      const int o = (wm * MT + m0 + k) * 16 + lane / 16 * 4;
       sw[k] = *reinterpret_cast<const float4 *>(s_o + o);
       b[k] = *reinterpret_cast<const float4 *>(b_o + o);
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int k = 0; k < S::kOutM * 4; ++k) {
-        const i32x16 &c = acc[m0 + k / 4][j];
-        const int g = k % 4 * 4;
-        const float v0 = float(c[g]) * sx[j] * sw[k].x + b[k].x, v1 = float(c[g + 1]) * sx[j] * sw[k].y + b[k].y;
-        const float v2 = float(c[g + 2]) * sx[j] * sw[k].z + b[k].z, v3 = float(c[g + 3]) * sx[j] * sw[k].w + b[k].w;
-        int8_t *p = mine + (j * 32 + lane % 32) * S::kOutPitch + (k * 8 + lane / 32 * 4) * int(sizeof(E));
+      for (int k = 0; k < S::kOutM; ++k) {
+        const i32x4 &c = acc[m0 + k][j];
+        const float v0 = float(c[0]) * sx[j] * sw[k].x + b[k].x, v1 = float(c[1]) * sx[j] * sw[k].y + b[k].y;
+        const float v2 = float(c[2]) * sx[j] * sw[k].z + b[k].z, v3 = float(c[3]) * sx[j] * sw[k].w + b[k].w;
+        int8_t *p = mine + (j * 16 + lane % 16) * S::kOutPitch + (k * 16 + lane / 16 * 4) * int(sizeof(E));
         if constexpr (sizeof(E) == 2)
           *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf2(v0, v1), pack_bf2(v2, v3));
         else
@@ -289,13 +312,13 @@ __global__ __launch_bounds__(256, 1) void product_tile_kernel(ProductArgs a, int
       }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
-    const int tt = wn * NT * 32, oo = wm * MT * 32 + m0 * 32;
+    const int tt = wn * NT * 16, oo = (wm * MT + m0) * 16;
     E *y = static_cast<E *>(a.y) + (t0 + tt) * a.ldy + o0 + oo;
     if (whole) {
       constexpr int kBatch = 8;
-      static_assert(NT * 32 * kPer % (64 * kBatch) == 0, "");
+      static_assert(NT * 16 * kPer % (64 * kBatch) == 0, "");
 #pragma unroll 1
-      for (int v = lane; v < NT * 32 * kPer; v += 64 * kBatch) {
+      for (int v = lane; v < NT * 16 * kPer; v += 64 * kBatch) {
         uint4 r[kBatch];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
@@ -304,7 +327,7 @@ __global__ __launch_bounds__(256, 1) void product_tile_kernel(ProductArgs a, int
         for (int k = 0; k < kBatch; ++k) gstore(y + (v + k * 64) / kPer * a.ldy + (v + k * 64) % kPer * kVec, r[k]);
       }
     } else {
-      for (int v = lane; v < NT * 32 * kPer; v += 64) {
+      for (int v = lane; v < NT * 16 * kPer; v += 64) {
         const int r = v / kPer, c = v % kPer * kVec;
         if (tt + r >= n_t || oo + c >= n_o) continue;
         const int8_t *p = mine + r * S::kOutPitch + c * int(sizeof(E));
@@ -337,7 +360,7 @@ hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
   a.y_vec = aligned16(a.y) && a.ldy * int64_t(sizeof(E)) % 16 == 0;
   const bool lines = aligned16(a.q) && aligned16(a.W) && a.ldq % 16 == 0 && a.ldw % 16 == 0 && a.d_in % 16 == 0 &&
                      a.ldq <= (1 << 22) && a.ldw <= (1 << 22);
-  if (lines && a.T > 128) return launch_tiles<E, 4, 4>(a, stream);
+  if (lines && a.T > 128) return launch_tiles<E, 8, 8>(a, stream);
   const dim3 grid((a.d_out + kAnyTile - 1) / kAnyTile, (a.T + kAnyTile - 1) / kAnyTile);
   product_any_kernel<E><<<grid, 256, 0, stream>>>(a);
   return hipGetLastError();
