@@ -164,51 +164,63 @@ __device__ __forceinline__ void settled(i32x4 (&c)[M][N]) {
     for (int j = 0; j < N; ++j) asm volatile("" : "+a"(c[m][j]));
 }
 
-template <typename E, int MT, int NT>
+template <typename E, int MT, int NT, int WM, int WN>
 struct TileShape {
-  static constexpr int kO = MT * 32, kT = NT * 32;   // channels and tokens of a tile
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int kO = MT * 16 * WM, kT = NT * 16 * WN;  // channels and tokens of a tile
+  static constexpr int kCopyO = kO / 8 / kWaves, kCopyT = kT / 8 / kWaves;  // copies of a wave a stage
   static constexpr int kBytes = (kO + kT) * kStage;  // one stage
   // results on their way out: up to 256 bytes of channels of each of a wave's tokens
   static constexpr int kOutM = MT * 16 * int(sizeof(E)) <= 256 ? MT : 256 / (16 * int(sizeof(E)));
   static constexpr int kOutRow = kOutM * 16 * int(sizeof(E)), kOutPitch = kOutRow + 16;
-  static constexpr int kOut = 4 * NT * 16 * kOutPitch;
+  static constexpr int kOut = kWaves * NT * 16 * kOutPitch;
   static constexpr int kScales = 2 * kBytes > kOut ? 2 * kBytes : kOut;  // then the scales and biases
   static constexpr int kLds = kScales + (2 * kO + kT) * 4;
   static_assert(MT % kOutM == 0 && kLds <= kMaxLdsBytes, "");
 };
 
-template <typename E, int MT, int NT>
-__global__ __launch_bounds__(256, 1) void product_tile_kernel(ProductArgs a, int tiles_o) {
-  typedef TileShape<E, MT, NT> S;
+template <typename E, int MT, int NT, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void product_tile_kernel(ProductArgs a, int tiles_o, int tiles_t) {
+  typedef TileShape<E, MT, NT, WM, WN> S;
   extern __shared__ __align__(16) int8_t lds[];
   const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64);
-  const int o0 = int(blockIdx.x) % tiles_o * S::kO;
-  const int64_t t0 = int64_t(int(blockIdx.x) / tiles_o) * S::kT;
+  // Workgroups go to the XCDs in turn.  Each XCD takes a contiguous eighth of
+  // the tiles, in blocks of four token tiles by all channel tiles, so that the
+  // 32 tiles it works on at a time are about 4 x 8 and share their operands
+  // in its L2.
+  const uint32_t tiles = gridDim.x, xcd = blockIdx.x % 8;
+  const uint32_t tile = xcd * (tiles / 8) + min(xcd, tiles % 8) + blockIdx.x / 8;
+  constexpr uint32_t kGroup = 4;
+  const uint32_t group = tile / (kGroup * tiles_o), in_group = tile % (kGroup * tiles_o);
+  const uint32_t high = min(kGroup, tiles_t - group * kGroup);
+  const int o0 = int(in_group / high) * S::kO;
+  const int64_t t0 = int64_t(group * kGroup + in_group % high) * S::kT;
   const int n_o = min(S::kO, a.d_out - o0), n_t = int(min(int64_t(S::kT), a.T - t0));
 
-  // this lane's pieces: MT rows of W and NT of q a stage (rows past the end: the last row again)
+  // this lane's pieces of W and of q (rows past the end: the last row again)
   const int8_t *W = a.W + int64_t(o0) * a.ldw, *q = a.q + t0 * a.ldq;
   const int piece = (lane % 8) ^ (lane / 8);
-  uint32_t off[MT + NT];
+  constexpr int kCopies = S::kCopyO + S::kCopyT;
+  uint32_t off[kCopies];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-    off[i] = uint32_t(min((wave * MT + i) * 8 + lane / 8, n_o - 1)) * uint32_t(a.ldw) + piece * 16;
+  for (int i = 0; i < S::kCopyO; ++i)
+    off[i] = uint32_t(min((wave * S::kCopyO + i) * 8 + lane / 8, n_o - 1)) * uint32_t(a.ldw) + piece * 16;
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
-    off[MT + i] = uint32_t(min((wave * NT + i) * 8 + lane / 8, n_t - 1)) * uint32_t(a.ldq) + piece * 16;
+  for (int i = 0; i < S::kCopyT; ++i)
+    off[S::kCopyO + i] = uint32_t(min((wave * S::kCopyT + i) * 8 + lane / 8, n_t - 1)) * uint32_t(a.ldq) + piece * 16;
   const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) int8_t *)lds));
 
   auto copy = [&](int i, int stage, uint32_t back) {
     const uint32_t at = lds0 + (stage & 1) * S::kBytes;
-    if (i < MT)
-      copy_to_lds(W + stage * kStage, off[i] - back, at + (wave * MT + i) * 1024);
+    if (i < S::kCopyO)
+      copy_to_lds(W + stage * kStage, off[i] - back, at + (wave * S::kCopyO + i) * 1024);
     else
-      copy_to_lds(q + stage * kStage, off[i] - back, at + S::kO * kStage + (wave * NT + i - MT) * 1024);
+      copy_to_lds(q + stage * kStage, off[i] - back, at + S::kO * kStage + (wave * S::kCopyT + i - S::kCopyO) * 1024);
   };
   // pieces past the end of the rows are not read: the stage's first piece stands in (and is masked below)
   auto back_of = [&](int stage) -> uint32_t { return stage * kStage + piece * 16 < a.d_in ? 0u : piece * 16u; };
 
-  const int wm = wave / 2, wn = wave % 2;
+  const int wm = wave / WN, wn = wave % WN;
   const int8_t *lw = lds + (wm * MT * 16 + lane % 16) * kStage, *lx = lds + (S::kO + wn * NT * 16 + lane % 16) * kStage;
   i32x4 fw[2][MT], fx[2][NT];
   i32x4 acc[MT][NT] = {};
@@ -224,23 +236,23 @@ __global__ __launch_bounds__(256, 1) void product_tile_kernel(ProductArgs a, int
   for (int st = 0; st < min(n, 2); ++st) {
     const uint32_t back = back_of(st);
 #pragma unroll
-    for (int i = 0; i < MT + NT; ++i) copy(i, st, back);
+    for (int i = 0; i < kCopies; ++i) copy(i, st, back);
   }
   float *s_o = reinterpret_cast<float *>(lds + S::kScales), *b_o = s_o + S::kO, *s_t = b_o + S::kO;
-  for (int i = tid; i < S::kO; i += 256) {
+  for (int i = tid; i < S::kO; i += S::kThreads) {
     const int o = o0 + min(i, n_o - 1);
     s_o[i] = gload<float>(a.w_scale + o);
     b_o[i] = bias_of(a, o);
   }
-  for (int i = tid; i < S::kT; i += 256) s_t[i] = gload<float>(a.q_scale + t0 + min(i, n_t - 1));
+  for (int i = tid; i < S::kT; i += S::kThreads) s_t[i] = gload<float>(a.q_scale + t0 + min(i, n_t - 1));
   stage_barrier();
 #pragma unroll
   for (int k = 0; k < MT + NT; ++k) read(k, place(0, 0), 0);
 
   // The order of issue is the order written: LDS reads spread over half the
   // products of a step, the copies over the other half.
-  constexpr int kReads = MT + NT, kEach = MT * NT / (2 * kReads);
-  static_assert(kEach >= 1, "a read or a copy goes with a product");
+  constexpr int kReads = MT + NT, kHalf = MT * NT / 2;
+  static_assert(kReads <= kHalf && kCopies <= kHalf, "a read or a copy goes with a product");
   auto stage = [&](int i, auto more, auto masked) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -260,12 +272,15 @@ __global__ __launch_bounds__(256, 1) void product_tile_kernel(ProductArgs a, int
       }
 #pragma unroll
       for (int t = 0; t < MT * NT; ++t) {
-        if (t % kEach == 0) {
+        const int half = t / kHalf, h = t % kHalf;
+        if (half == s && h % (kHalf / kReads) == 0 && h / (kHalf / kReads) < kReads) {
           __builtin_amdgcn_sched_barrier(0);
-          if (t / kEach < kReads)
-            read(t / kEach, p, s ^ 1);
-          else if (more && s == 1 && t / kEach - kReads < kReads)
-            copy(t / kEach - kReads, i + 2, back);
+          read(h / (kHalf / kReads), p, s ^ 1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (more && s == 1 && half == 0 && h % (kHalf / kCopies) == 0 && h / (kHalf / kCopies) < kCopies) {
+          __builtin_amdgcn_sched_barrier(0);
+          copy(h / (kHalf / kCopies), i + 2, back);
           __builtin_amdgcn_sched_barrier(0);
         }
         multiply(acc[t / NT][t % NT], fw[s][t / NT], fx[s][t % NT]);
@@ -343,14 +358,16 @@ __global__ __launch_bounds__(256, 1) void product_tile_kernel(ProductArgs a, int
   }
 }
 
-template <typename E, int MT, int NT>
+template <typename E, int MT, int NT, int WM, int WN>
 hipError_t launch_tiles(const ProductArgs &a, hipStream_t stream) {
-  typedef TileShape<E, MT, NT> S;
-  static const bool ready = raise_lds_limit(reinterpret_cast<const void *>(product_tile_kernel<E, MT, NT>), S::kLds);
+  typedef TileShape<E, MT, NT, WM, WN> S;
+  const auto kernel = product_tile_kernel<E, MT, NT, WM, WN>;
+  static const bool ready = raise_lds_limit(reinterpret_cast<const void *>(kernel), S::kLds);
   (void)ready;
   const int tiles_o = (a.d_out + S::kO - 1) / S::kO;
-  const int64_t tiles = int64_t(tiles_o) * ((a.T + S::kT - 1) / S::kT);
-  product_tile_kernel<E, MT, NT><<<dim3(uint32_t(tiles)), 256, S::kLds, stream>>>(a, tiles_o);
+  const int tiles_t = (a.T - 1) / S::kT + 1;
+  const int64_t tiles = int64_t(tiles_o) * tiles_t;
+  kernel<<<dim3(uint32_t(tiles)), S::kThreads, S::kLds, stream>>>(a, tiles_o, tiles_t);
   return hipGetLastError();
 }
 
@@ -360,7 +377,7 @@ hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
   a.y_vec = aligned16(a.y) && a.ldy * int64_t(sizeof(E)) % 16 == 0;
   const bool lines = aligned16(a.q) && aligned16(a.W) && a.ldq % 16 == 0 && a.ldw % 16 == 0 && a.d_in % 16 == 0 &&
                      a.ldq <= (1 << 22) && a.ldw <= (1 << 22);
-  if (lines && a.T > 128) return launch_tiles<E, 8, 8>(a, stream);
+  if (lines && a.T > 128) return launch_tiles<E, 8, 4, 2, 4>(a, stream);
   const dim3 grid((a.d_out + kAnyTile - 1) / kAnyTile, (a.T + kAnyTile - 1) / kAnyTile);
   product_any_kernel<E><<<grid, 256, 0, stream>>>(a);
   return hipGetLastError();
