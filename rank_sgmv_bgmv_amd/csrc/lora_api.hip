@@ -10,6 +10,17 @@
 
 using namespace lora;
 
+int lora::cu_count() {
+  static int cached[64] = {0};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  if (cached[dev] == 0) {
+    int n = 0;
+    cached[dev] = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && n > 0 ? n : 256;
+  }
+  return cached[dev];
+}
+
 namespace {
 
 // Tuning knobs (overridable through the environment for sweeps).
@@ -96,17 +107,6 @@ lora_status plan_for(const BatchDims &d, int n, const void *ws, size_t ws_bytes,
 
 int round_up(int x, int m) { return (x + m - 1) / m * m; }
 
-// Compute units of the current device (looked up once per device).
-int cu_count() {
-  static int cached[64] = {0};
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
-  if (cached[dev] == 0) {
-    int n = 0;
-    cached[dev] = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && n > 0 ? n : 256;
-  }
-  return cached[dev];
-}
 int pow2_floor(int x) {
   int p = 1;
   while (p * 2 <= x) p *= 2;

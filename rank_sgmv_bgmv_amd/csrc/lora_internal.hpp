@@ -77,6 +77,9 @@ inline size_t span_bytes(int rows, int64_t ld, int cols, int eb) {
   return (size_t(rows - 1) * size_t(ld) + size_t(cols)) * size_t(eb);
 }
 
+// Compute units of the current device (looked up once per device).
+int cu_count();
+
 inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 inline PlanLayout plan_layout(int S, int T, int n) {

@@ -133,13 +133,28 @@ __device__ __forceinline__ void copy_to_lds(const int8_t *base, uint32_t off, ui
   __builtin_amdgcn_global_load_lds((const LORA_GLOBAL void *)((const LORA_GLOBAL char *)base + off),
                                    (__attribute__((address_space(3))) void *)(uintptr_t)lds, 16, 0, 0);
 }
-// Waits as the compiler counts them: after one it adds none of its own for what came before.
-__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }  // lgkmcnt(0)
-// Every copy of this wave has landed and every LDS read has returned, for all waves.
-__device__ __forceinline__ void stage_barrier() {
-  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-  asm volatile("s_barrier" ::: "memory");
+// Waits as the compiler counts them (after one it adds none of its own for
+// what came before), and the workgroup's barrier, which no memory access of
+// the code around it crosses.
+template <int kCopies>  // of this wave's copies, all but the last kCopies have landed
+__device__ __forceinline__ void wait_copies() {
+  static_assert(kCopies < 64, "");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (kCopies & 15) | (kCopies >> 4) << 14);
 }
+// At most `stages` stages of kCopies copies still on their way (a wave-uniform number; kMost at most).
+template <int kCopies, int kMost>
+__device__ __forceinline__ void wait_stages(int stages) {
+  if constexpr (kMost == 0) {
+    wait_copies<0>();
+  } else {
+    if (stages >= kMost)
+      wait_copies<kCopies * kMost>();
+    else
+      wait_stages<kCopies, kMost - 1>(stages);
+  }
+}
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }  // lgkmcnt(0)
+__device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
 
 // c += a b^T on a 16 x 16 block, c kept where it is: given the choice, the
 // compiler writes the sums elsewhere and moves 200 registers back each stage.
@@ -164,24 +179,29 @@ __device__ __forceinline__ void settled(i32x4 (&c)[M][N]) {
     for (int j = 0; j < N; ++j) asm volatile("" : "+a"(c[m][j]));
 }
 
-template <typename E, int MT, int NT, int WM, int WN>
+template <typename E, int MT, int NT, int WM, int WN, int ST>
 struct TileShape {
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int kO = MT * 16 * WM, kT = NT * 16 * WN;  // channels and tokens of a tile
   static constexpr int kCopyO = kO / 8 / kWaves, kCopyT = kT / 8 / kWaves;  // copies of a wave a stage
   static constexpr int kBytes = (kO + kT) * kStage;  // one stage
   // results on their way out: up to 256 bytes of channels of each of a wave's tokens
-  static constexpr int kOutM = MT * 16 * int(sizeof(E)) <= 256 ? MT : 256 / (16 * int(sizeof(E)));
+  static constexpr int kOutM = MT * 16 * int(sizeof(E)) <= 256 ? MT : MT / 2;
   static constexpr int kOutRow = kOutM * 16 * int(sizeof(E)), kOutPitch = kOutRow + 16;
   static constexpr int kOut = kWaves * NT * 16 * kOutPitch;
-  static constexpr int kScales = 2 * kBytes > kOut ? 2 * kBytes : kOut;  // then the scales and biases
+  static constexpr int kScales = ST * kBytes > kOut ? ST * kBytes : kOut;  // then the scales and biases
   static constexpr int kLds = kScales + (2 * kO + kT) * 4;
-  static_assert(MT % kOutM == 0 && kLds <= kMaxLdsBytes, "");
+  // 16-byte vectors that a lane stores, and how many of them at a time
+  static constexpr int kStores = NT * 16 * (kOutRow / 16) / 64;
+  static constexpr int kBatch = kStores % 8 == 0 ? 8 : kStores % 6 == 0 ? 6 : kStores % 4 == 0 ? 4 : kStores % 3 == 0 ? 3 : 2;
+  static_assert(MT % kOutM == 0 && kOutRow <= 256 && kStores % kBatch == 0 && kLds <= kMaxLdsBytes, "");
+  static_assert(ST >= 2 && (ST & (ST - 1)) == 0, "stages are found by their number's low bits");
+  static_assert(kO % (8 * kWaves) == 0 && kT % (8 * kWaves) == 0, "every wave copies the same");
 };
 
-template <typename E, int MT, int NT, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void product_tile_kernel(ProductArgs a, int tiles_o, int tiles_t) {
-  typedef TileShape<E, MT, NT, WM, WN> S;
+template <typename E, int MT, int NT, int WM, int WN, int ST>
+__global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductArgs a, int tiles_o, int tiles_t) {
+  typedef TileShape<E, MT, NT, WM, WN, ST> S;
   extern __shared__ __align__(16) int8_t lds[];
   const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64);
   // Workgroups go to the XCDs in turn.  Each XCD takes a contiguous eighth of
@@ -211,7 +231,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void product_tile_kernel
   const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) int8_t *)lds));
 
   auto copy = [&](int i, int stage, uint32_t back) {
-    const uint32_t at = lds0 + (stage & 1) * S::kBytes;
+    const uint32_t at = lds0 + (stage & (ST - 1)) * S::kBytes;
     if (i < S::kCopyO)
       copy_to_lds(W + stage * kStage, off[i] - back, at + (wave * S::kCopyO + i) * 1024);
     else
@@ -224,7 +244,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void product_tile_kernel
   const int8_t *lw = lds + (wm * MT * 16 + lane % 16) * kStage, *lx = lds + (S::kO + wn * NT * 16 + lane % 16) * kStage;
   i32x4 fw[2][MT], fx[2][NT];
   i32x4 acc[MT][NT] = {};
-  auto place = [&](int stage, int s) { return (stage & 1) * S::kBytes + (((s * 4 + lane / 16) ^ (lane & 7)) * 16); };
+  auto place = [&](int stage, int s) { return (stage & (ST - 1)) * S::kBytes + (((s * 4 + lane / 16) ^ (lane & 7)) * 16); };
   auto read = [&](int k, int p, int s) {
     if (k < MT)
       fw[s][k] = *reinterpret_cast<const i32x4 *>(lw + p + k * 16 * kStage);
@@ -233,34 +253,57 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void product_tile_kernel
   };
 
   const int n = (a.d_in + kStage - 1) / kStage;
-  for (int st = 0; st < min(n, 2); ++st) {
+  float *s_o = reinterpret_cast<float *>(lds + S::kScales), *b_o = s_o + S::kO, *s_t = b_o + S::kO;
+  float scale_o[S::kO / S::kThreads + 1], scale_t[S::kT / S::kThreads + 1], bias[S::kO / S::kThreads + 1];
+#pragma unroll
+  for (int i = 0; i * S::kThreads < S::kO; ++i) {
+    const int o = o0 + min(tid + i * S::kThreads, n_o - 1);
+    scale_o[i] = gload<float>(a.w_scale + o);
+    bias[i] = bias_of(a, o);
+  }
+#pragma unroll
+  for (int i = 0; i * S::kThreads < S::kT; ++i)
+    scale_t[i] = gload<float>(a.q_scale + t0 + min(tid + i * S::kThreads, n_t - 1));
+  for (int st = 0; st < min(n, ST); ++st) {
     const uint32_t back = back_of(st);
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) copy(i, st, back);
   }
-  float *s_o = reinterpret_cast<float *>(lds + S::kScales), *b_o = s_o + S::kO, *s_t = b_o + S::kO;
-  for (int i = tid; i < S::kO; i += S::kThreads) {
-    const int o = o0 + min(i, n_o - 1);
-    s_o[i] = gload<float>(a.w_scale + o);
-    b_o[i] = bias_of(a, o);
-  }
-  for (int i = tid; i < S::kT; i += S::kThreads) s_t[i] = gload<float>(a.q_scale + t0 + min(i, n_t - 1));
-  stage_barrier();
+#pragma unroll
+  for (int i = 0; i * S::kThreads < S::kO; ++i)
+    if (tid + i * S::kThreads < S::kO) s_o[tid + i * S::kThreads] = scale_o[i], b_o[tid + i * S::kThreads] = bias[i];
+#pragma unroll
+  for (int i = 0; i * S::kThreads < S::kT; ++i)
+    if (tid + i * S::kThreads < S::kT) s_t[tid + i * S::kThreads] = scale_t[i];
+  wait_stages<kCopies, ST - 1>(n - 1);
+  wait_lds();
+  meet();
 #pragma unroll
   for (int k = 0; k < MT + NT; ++k) read(k, place(0, 0), 0);
 
-  // The order of issue is the order written: LDS reads spread over half the
-  // products of a step, the copies over the other half.
-  constexpr int kReads = MT + NT, kHalf = MT * NT / 2;
-  static_assert(kReads <= kHalf && kCopies <= kHalf, "a read or a copy goes with a product");
+  // A stage is two steps of 64 values.  The first step's products go with the
+  // reads of the second's operands.  Then all waves meet: the stage has been
+  // read by all, so the copies of stage i + ST may take its place, and stage i +
+  // 1 has landed for all, so the second step's products go with the reads of
+  // its first operands.  The order of issue is the order written.
+  constexpr int kReads = MT + NT, kMul = MT * NT;
+  constexpr int kCopyEach = kMul / 2 > kCopies ? kMul / 2 / kCopies : 1;
+  constexpr int kReadAt = kMul / 2 + kReads <= kMul ? kMul / 2 : kMul - kReads;
+  static_assert(kReads <= kMul && kCopies <= kMul, "a read or a copy goes with a product");
   auto stage = [&](int i, auto more, auto masked) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      // the operands of this step were read half a step ago and more
-      if (s == 1) stage_barrier();
-      else wait_lds();
+      wait_lds();
+      if (s == 1 && !masked) {
+        // what may still be on its way: the stages after the next one
+        if constexpr (more)
+          wait_copies<kCopies *(ST - 2)>();
+        else
+          wait_stages<kCopies, ST - 2>(n - 2 - i);
+        meet();
+      }
       const int p = place(s ? i + 1 : i, s ^ 1);
-      const uint32_t back = more && s == 1 ? back_of(i + 2) : 0;
+      const uint32_t back = more && s == 1 ? back_of(i + ST) : 0;
       if constexpr (masked) {
         // past the end of the sum's axis q counts as zero
         const bool in = i * kStage + s * 64 + lane / 16 * 16 < a.d_in;
@@ -271,24 +314,18 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void product_tile_kernel
         settle();
       }
 #pragma unroll
-      for (int t = 0; t < MT * NT; ++t) {
-        const int half = t / kHalf, h = t % kHalf;
-        if (half == s && h % (kHalf / kReads) == 0 && h / (kHalf / kReads) < kReads) {
-          __builtin_amdgcn_sched_barrier(0);
-          read(h / (kHalf / kReads), p, s ^ 1);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        if (more && s == 1 && half == 0 && h % (kHalf / kCopies) == 0 && h / (kHalf / kCopies) < kCopies) {
-          __builtin_amdgcn_sched_barrier(0);
-          copy(h / (kHalf / kCopies), i + 2, back);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+      for (int t = 0; t < kMul; ++t) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (more && s == 1 && t % kCopyEach == 0 && t / kCopyEach < kCopies) copy(t / kCopyEach, i + ST, back);
+        if (s == 0 && t < kReads) read(t, p, 1);
+        if (!masked && s == 1 && t >= kReadAt && t < kReadAt + kReads) read(t - kReadAt, p, 0);
+        __builtin_amdgcn_sched_barrier(0);
         multiply(acc[t / NT][t % NT], fw[s][t / NT], fx[s][t % NT]);
       }
     }
   };
   int i = 0;
-  for (; i < n - 2; ++i) stage(i, std::true_type{}, std::false_type{});
+  for (; i < n - ST; ++i) stage(i, std::true_type{}, std::false_type{});
   for (; i < n - 1; ++i) stage(i, std::false_type{}, std::false_type{});
   stage(i, std::false_type{}, std::true_type{});
   settled(acc);
@@ -296,7 +333,9 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void product_tile_kernel
   // Results through LDS, so that a token's channels leave in whole lines.  Each
   // wave has its own place there, which it writes and reads in order: no
   // barrier after the first, and stores stay in flight.
-  stage_barrier();
+  wait_copies<0>();
+  wait_lds();
+  meet();
   int8_t *mine = lds + wave * NT * 16 * S::kOutPitch;
   constexpr int kVec = 16 / int(sizeof(E)), kPer = S::kOutRow / 16;  // 16-byte vectors of a token's row
   const bool whole = a.y_vec && n_o == S::kO && n_t == S::kT;
@@ -330,8 +369,7 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void product_tile_kernel
     const int tt = wn * NT * 16, oo = (wm * MT + m0) * 16;
     E *y = static_cast<E *>(a.y) + (t0 + tt) * a.ldy + o0 + oo;
     if (whole) {
-      constexpr int kBatch = 8;
-      static_assert(NT * 16 * kPer % (64 * kBatch) == 0, "");
+      constexpr int kBatch = S::kBatch;
 #pragma unroll 1
       for (int v = lane; v < NT * 16 * kPer; v += 64 * kBatch) {
         uint4 r[kBatch];
@@ -358,10 +396,10 @@ __global__ __launch_bounds__(64 * WM * WN, WM * WN / 4) void product_tile_kernel
   }
 }
 
-template <typename E, int MT, int NT, int WM, int WN>
+template <typename E, int MT, int NT, int WM, int WN, int ST>
 hipError_t launch_tiles(const ProductArgs &a, hipStream_t stream) {
-  typedef TileShape<E, MT, NT, WM, WN> S;
-  const auto kernel = product_tile_kernel<E, MT, NT, WM, WN>;
+  typedef TileShape<E, MT, NT, WM, WN, ST> S;
+  const auto kernel = product_tile_kernel<E, MT, NT, WM, WN, ST>;
   static const bool ready = raise_lds_limit(reinterpret_cast<const void *>(kernel), S::kLds);
   (void)ready;
   const int tiles_o = (a.d_out + S::kO - 1) / S::kO;
@@ -371,13 +409,53 @@ hipError_t launch_tiles(const ProductArgs &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The tile shapes and what a tile of n stages costs, in microseconds: when its
+// CU has no other tile, and when the CU is full (so many tiles at once).  Large
+// tiles move the fewest bytes for each product, small ones fill more CUs.
+// Measured at 32 and 112 stages of 4096-wide and 14336-wide weights: 512 rows
+// through 4096 x 4096 take 40 us with the first shape, 22, 17.5, 13 and 15.6
+// with the last four; 2304 rows through 4096 x 14336 take 113 with the first,
+// 130 with the second and 133, 158, 196, 209 with the others.
+struct TileCost {
+  int o, t, at_once;
+  float alone, full, once;  // per stage, per stage with a full CU, per tile
+};
+constexpr TileCost kTileCosts[] = {
+    {256, 256, 1, 1.30f, 1.30f, 7.0f}, {192, 256, 1, 1.05f, 1.05f, 6.0f}, {128, 128, 2, 0.60f, 0.85f, 3.0f},
+    {128, 128, 1, 0.50f, 0.50f, 3.0f}, {128, 64, 1, 0.33f, 0.33f, 2.5f},  {64, 64, 2, 0.20f, 0.41f, 2.0f},
+};
+
+int choose_tile(const ProductArgs &a) {
+  const int64_t cus = cu_count(), n = (a.d_in + kStage - 1) / kStage;
+  int best = 0;
+  double least = 0;
+  for (int k = 0; k < int(sizeof(kTileCosts) / sizeof(kTileCosts[0])); ++k) {
+    const TileCost &c = kTileCosts[k];
+    const int64_t tiles = int64_t((a.d_out - 1) / c.o + 1) * ((a.T - 1) / c.t + 1);
+    const int64_t rounds = tiles / (cus * c.at_once), rest = tiles % (cus * c.at_once);
+    double us = rounds * double(n * c.full + c.once);
+    if (rest) us += n * (rest <= cus ? c.alone : c.full) + c.once;
+    if (k == 0 || us < least) best = k, least = us;
+  }
+  return best;
+}
+
 template <typename E>
 hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
   ProductArgs a = args;
   a.y_vec = aligned16(a.y) && a.ldy * int64_t(sizeof(E)) % 16 == 0;
   const bool lines = aligned16(a.q) && aligned16(a.W) && a.ldq % 16 == 0 && a.ldw % 16 == 0 && a.d_in % 16 == 0 &&
                      a.ldq <= (1 << 22) && a.ldw <= (1 << 22);
-  if (lines && a.T > 128) return launch_tiles<E, 8, 4, 2, 4>(a, stream);
+  if (lines) {
+    switch (choose_tile(a)) {
+      case 0: return launch_tiles<E, 8, 4, 2, 4, 2>(a, stream);
+      case 1: return launch_tiles<E, 6, 4, 2, 4, 2>(a, stream);
+      case 2: return launch_tiles<E, 4, 4, 2, 2, 2>(a, stream);
+      case 3: return launch_tiles<E, 4, 4, 2, 2, 4>(a, stream);
+      case 4: return launch_tiles<E, 4, 2, 2, 2, 4>(a, stream);
+      default: return launch_tiles<E, 2, 2, 2, 2, 4>(a, stream);
+    }
+  }
   const dim3 grid((a.d_out + kAnyTile - 1) / kAnyTile, (a.T + kAnyTile - 1) / kAnyTile);
   product_any_kernel<E><<<grid, 256, 0, stream>>>(a);
   return hipGetLastError();
