@@ -22,7 +22,6 @@ x [T][ldx], y [T][ldy] with unit column stride (ld = stride(0)); idx int32
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -127,8 +126,14 @@ def lib() -> ctypes.CDLL:
 
 # ------------------------------------------------------------- marshalling --
 def _torch():
-    import torch
-    return torch
+    global _torch_module, _REAL
+    if _torch_module is None:
+        import torch
+        _torch_module, _REAL = torch, {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32}
+    return _torch_module
+
+
+_torch_module, _REAL = None, {}
 
 
 def _dtype_code(t) -> int:
@@ -396,11 +401,32 @@ def lora_pool_load(pool: Pool, slot: int, A_host, B_host, stream=None):
 
 
 # ------------------------------------------- around a LoRA layer (lora_base.h) --
-def _device_guard(dev):
-    """The tensors' device as the current one: a launch goes to the current device."""
-    if dev.index == _torch().cuda.current_device():
-        return contextlib.nullcontext()
-    return _torch().cuda.device(dev)
+# A decode step's kernels take a few microseconds, as does a call's way through
+# Python: these bindings look first for tensors that are plainly right (_row,
+# _line), and where one is not go through the checks that name what is wrong.
+def _launch(index: int, what: str, f, *args):
+    """f(*args, stream) on the current stream of device `index`, as the current device: launches go to that one."""
+    torch = _torch()
+    if index == torch.cuda.current_device():
+        st = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            st = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st != 0:
+        raise LoraError(st, what)
+
+
+def _row(t, dtype, index: int) -> int:
+    """The row stride of a 2-D tensor of this type and device with unit column stride; 0 if t is not plainly one."""
+    if t.dtype is not dtype or t.get_device() != index or t.dim() != 2:
+        return 0
+    s = t.stride()
+    return s[0] if s[1] == 1 else 0
+
+
+def _line(t, dtype, index: int, n: int) -> bool:
+    """Whether t is plainly a contiguous 1-D tensor of n elements or more, of this type and device."""
+    return t.dtype is dtype and t.get_device() == index and t.dim() == 1 and t.shape[0] >= n and t.is_contiguous()
 
 
 def _rows_2d(what: str, name: str, t, dtypes, dev, cols: int, rows: Optional[int] = None) -> int:
@@ -443,38 +469,46 @@ class BaseWeight:
                     raise LoraError(-2, f"BaseWeight: {name} must be [{self.d_out}]")
         self.W, self.scale, self.bias, self.device = W, scale, bias, W.device
         self.c = lora_base_weight(_ptr(W), _ptr(scale), _ptr(bias), self.ld, self.d_in, self.d_out)
-        self.ref = ctypes.addressof(self.c)
+        self.ref, self.index = ctypes.addressof(self.c), W.get_device()
 
 
 def lora_quantize_rows(x, q, scale):
     """q[t] = rint(127 x[t] / max|x[t]|) and scale[t] = max|x[t]| / 127 for every row of x [T][d]
     (bfloat16 or float32) into q int8 [T][d] and scale float32 [T]."""
     torch = _torch()
-    what, dev = "lora_quantize_rows", x.device
-    if x.dim() != 2 or q.dim() != 2 or x.shape != q.shape:
-        raise LoraError(-2, f"{what}: x and q must be of one shape [T][d]")
-    ldx = _rows_2d(what, "x", x, (torch.bfloat16, torch.float32), dev, 1)
-    ldq = _rows_2d(what, "q", q, (torch.int8,), dev, 1)
-    _vector(what, "scale", scale, torch.float32, dev, x.shape[0])
-    with _device_guard(dev):
-        _check(lib().lora_quantize_rows(_ptr(x), ldx, _dtype_code(x), x.shape[0], x.shape[1], _ptr(q), ldq, _ptr(scale),
-                                        _stream(x)), what)
+    what, index = "lora_quantize_rows", x.get_device()
+    code = _REAL.get(x.dtype, -1)
+    ldx, ldq = _row(x, x.dtype, index), _row(q, torch.int8, index)
+    if index < 0 or code < 0 or ldx == 0 or ldq == 0 or x.shape != q.shape or not _line(scale, torch.float32, index, x.shape[0]):
+        dev = x.device
+        if x.dim() != 2 or q.dim() != 2 or x.shape != q.shape:
+            raise LoraError(-2, f"{what}: x and q must be of one shape [T][d]")
+        ldx = _rows_2d(what, "x", x, _REAL, dev, 1)
+        ldq = _rows_2d(what, "q", q, (torch.int8,), dev, 1)
+        _vector(what, "scale", scale, torch.float32, dev, x.shape[0])
+    T, d = x.shape
+    _launch(index, what, lib().lora_quantize_rows, x.data_ptr(), ldx, code, T, d, q.data_ptr(), ldq, scale.data_ptr())
 
 
 def lora_base_product(weight: BaseWeight, q, q_scale, y):
     """y[t][o] = q_scale[t] scale[o] sum_c q[t][c] W[o][c] (+ bias[o]) for every row of q int8 [T][d_in] into
     y [T][>= d_out] (bfloat16 or float32; further rows and columns are left as they are)."""
     torch = _torch()
-    what, dev = "lora_base_product", weight.device
-    ldq = _rows_2d(what, "q", q, (torch.int8,), dev, weight.d_in)
-    T = q.shape[0]
-    if q.shape[1] != weight.d_in:
-        raise LoraError(-2, f"{what}: q must be [T][{weight.d_in}]")
-    ldy = _rows_2d(what, "y", y, (torch.bfloat16, torch.float32), dev, weight.d_out, T)
-    _vector(what, "q_scale", q_scale, torch.float32, dev, T)
-    with _device_guard(dev):
-        _check(lib().lora_base_product(weight.ref, _ptr(q), ldq, _ptr(q_scale), T, _ptr(y), ldy, _dtype_code(y),
-                                       _stream(y)), what)
+    what, index, d_in = "lora_base_product", weight.index, weight.d_in
+    code = _REAL.get(y.dtype, -1)
+    ldq, ldy = _row(q, torch.int8, index), _row(y, y.dtype, index)
+    T = q.shape[0] if ldq else 0
+    if (code < 0 or ldq == 0 or ldy == 0 or q.shape[1] != d_in or y.shape[0] < T or y.shape[1] < weight.d_out
+            or not _line(q_scale, torch.float32, index, T)):
+        dev = weight.device
+        ldq = _rows_2d(what, "q", q, (torch.int8,), dev, d_in)
+        T = q.shape[0]
+        if q.shape[1] != d_in:
+            raise LoraError(-2, f"{what}: q must be [T][{d_in}]")
+        ldy = _rows_2d(what, "y", y, _REAL, dev, weight.d_out, T)
+        _vector(what, "q_scale", q_scale, torch.float32, dev, T)
+    _launch(index, what, lib().lora_base_product, weight.ref, q.data_ptr(), ldq, q_scale.data_ptr(), T, y.data_ptr(), ldy,
+            code)
 
 
 def lora_base_workspace_size(weight: BaseWeight, n_tokens: int) -> int:
@@ -490,16 +524,21 @@ def lora_base_apply(weight: BaseWeight, x, y, ws):
     """lora_quantize_rows and lora_base_product in one call: y [T][>= d_out] from x [T][d_in] of the same type, the
     quantised rows in the uint8 workspace ws (new_base_workspace)."""
     torch = _torch()
-    what, dev = "lora_base_apply", weight.device
-    ldx = _rows_2d(what, "x", x, (torch.bfloat16, torch.float32), dev, weight.d_in)
-    T = x.shape[0]
-    if x.shape[1] != weight.d_in:
-        raise LoraError(-2, f"{what}: x must be [T][{weight.d_in}]")
-    ldy = _rows_2d(what, "y", y, (x.dtype,), dev, weight.d_out, T)
-    _vector(what, "ws", ws, torch.uint8, dev, 0)
-    with _device_guard(dev):
-        _check(lib().lora_base_apply(weight.ref, _ptr(x), ldx, T, _ptr(y), ldy, _dtype_code(x), _ptr(ws), ws.numel(),
-                                     _stream(y)), what)
+    what, index, d_in = "lora_base_apply", weight.index, weight.d_in
+    code = _REAL.get(x.dtype, -1)
+    ldx, ldy = _row(x, x.dtype, index), _row(y, x.dtype, index)
+    T = x.shape[0] if ldx else 0
+    if (code < 0 or ldx == 0 or ldy == 0 or x.shape[1] != d_in or y.shape[0] < T or y.shape[1] < weight.d_out
+            or not _line(ws, torch.uint8, index, 0)):
+        dev = weight.device
+        ldx = _rows_2d(what, "x", x, _REAL, dev, d_in)
+        T = x.shape[0]
+        if x.shape[1] != d_in:
+            raise LoraError(-2, f"{what}: x must be [T][{d_in}]")
+        ldy = _rows_2d(what, "y", y, (x.dtype,), dev, weight.d_out, T)
+        _vector(what, "ws", ws, torch.uint8, dev, 0)
+    _launch(index, what, lib().lora_base_apply, weight.ref, x.data_ptr(), ldx, T, y.data_ptr(), ldy, code, ws.data_ptr(),
+            ws.shape[0])
 
 
 class Rotary:
@@ -514,37 +553,41 @@ class Rotary:
         _vector("Rotary", "freq", freq, _torch().float64, freq.device, freq.numel())
         self.freq, self.device, self.head_dim = freq, freq.device, int(head_dim)
         self.c = lora_rotary(_ptr(freq), self.head_dim, 2 * freq.numel(), int(bool(interleaved)), float(mscale))
-        self.ref = ctypes.addressof(self.c)
+        self.ref, self.index = ctypes.addressof(self.c), freq.get_device()
 
 
 def lora_rotary_apply(rotary: Rotary, positions, src: Sequence, dst: Optional[Sequence] = None, inverse: bool = False):
     """Rotates the heads of src, up to 8 tensors [T][heads][head_dim] of the same tokens (any token and head
     strides), into dst (in place by default).  positions int32 [T]; tokens of a negative position are skipped."""
     torch = _torch()
-    what, dev = "lora_rotary_apply", rotary.device
-    dst = src if dst is None else dst
+    what, index, D = "lora_rotary_apply", rotary.index, rotary.head_dim
     n, T = len(src), positions.shape[0] if positions.dim() else 0
-    if not 1 <= n <= LORA_MAX_SLICES or len(dst) != n:
+    if not 1 <= n <= LORA_MAX_SLICES or (dst is not None and len(dst) != n):
         raise LoraError(-2, f"{what}: 1 to {LORA_MAX_SLICES} tensors, as many in dst as in src")
-    _vector(what, "positions", positions, torch.int32, dev, T)
-    t0 = src[0].dtype
-    if t0 not in (torch.bfloat16, torch.float32):
-        raise LoraError(-2, f"{what}: heads must be bfloat16 or float32 (got {t0})")
+    if not _line(positions, torch.int32, index, T):
+        _vector(what, "positions", positions, torch.int32, rotary.device, T)
+    dtype = src[0].dtype
+    code = _REAL.get(dtype, -1)
+    if code < 0:
+        raise LoraError(-2, f"{what}: heads must be bfloat16 or float32 (got {dtype})")
     slices = (lora_rotary_slice * n)()
     for i in range(n):
-        a, b = src[i], dst[i]
-        for t in (a, b) if b is not a else (a,):
-            if t.dim() != 3 or t.shape[0] != T or t.shape[2] != rotary.head_dim or t.shape != a.shape:
-                raise LoraError(-2, f"{what}: heads must be [{T}][heads][{rotary.head_dim}] (got {tuple(t.shape)})")
-            if t.dtype != t0 or t.device != dev:
-                raise LoraError(-2, f"{what}: heads must all be {t0} on {dev} (found {t.dtype} on {t.device})")
-            if t.stride(2) != 1 and t.shape[2] > 1:
-                raise LoraError(-2, f"{what}: heads must have unit stride within a head")
-        sa, sb = a.stride(), b.stride()
-        slices[i] = lora_rotary_slice(a.data_ptr(), b.data_ptr(), sa[0], sa[1], sb[0], sb[1], a.shape[1])
-    with _device_guard(dev):
-        _check(lib().lora_rotary_apply(rotary.ref, _ptr(positions), T, n, ctypes.addressof(slices), _dtype_code(src[0]),
-                                       int(bool(inverse)), _stream(positions)), what)
+        a = src[i]
+        shape, sa, pa = a.shape, a.stride(), a.data_ptr()
+        if a.dtype is not dtype or a.get_device() != index or len(shape) != 3 or shape[0] != T or shape[2] != D or (
+                sa[2] != 1 and D > 1):
+            raise LoraError(-2, f"{what}: heads must be {dtype} [{T}][heads][{D}] on {rotary.device}, a head's values "
+                                f"side by side (got {a.dtype} {tuple(shape)} on {a.device}, strides {sa})")
+        sb, pb = sa, pa
+        if dst is not None:
+            b = dst[i]
+            sb, pb = b.stride(), b.data_ptr()
+            if b.dtype is not dtype or b.get_device() != index or b.shape != shape or (sb[2] != 1 and D > 1):
+                raise LoraError(-2, f"{what}: dst must be like src (got {b.dtype} {tuple(b.shape)} on {b.device}, "
+                                    f"strides {sb})")
+        slices[i] = (pa, pb, sa[0], sa[1], sb[0], sb[1], shape[1])
+    _launch(index, what, lib().lora_rotary_apply, rotary.ref, positions.data_ptr(), T, n, ctypes.addressof(slices), code,
+            1 if inverse else 0)
 
 
 def lora_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = LORA_ROTARY_PLAIN, factor: float = 1.0,
