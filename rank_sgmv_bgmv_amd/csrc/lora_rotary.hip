@@ -1,9 +1,14 @@
 // Rotary positions: the pairs of each head turned by position * frequency.
 //
 // Angles are float64 products, reduced to a fraction of a turn there, so that
-// a position of millions keeps an error of 2^-26 turns; sine and cosine of the
+// a position of millions keeps an error of 2^-27 turns; sine and cosine of the
 // fraction are float32.  One table of rot_dim / 2 of them serves all heads of a
 // token, in LDS.
+//
+// Bound by memory: every value is read and written once, 16 bytes a lane.  A
+// workgroup takes kTokens tokens (one when there are few: then the heads are
+// split over workgroups too) and a lane one 16-byte column of a head, for every
+// slots-th head of each of them.
 
 #include "lora_base.hpp"
 #include "lora_device.hpp"
@@ -13,11 +18,12 @@ namespace {
 
 constexpr int kRotaryThreads = 256;
 
-template <typename E> __device__ __forceinline__ float load_f(const E *p);
-template <> __device__ __forceinline__ float load_f<uint16_t>(const uint16_t *p) { return bf_to_f(gload<uint16_t>(p)); }
-template <> __device__ __forceinline__ float load_f<float>(const float *p) { return gload<float>(p); }
-__device__ __forceinline__ void store_f(uint16_t *p, float v) { gstore(p, f_to_bf(v)); }
-__device__ __forceinline__ void store_f(float *p, float v) { gstore(p, v); }
+// Where a value's partner in its pair lies.
+enum {
+  ROT_HALVES = 0,  // half a rotation further on, in whole vectors: a lane takes both vectors
+  ROT_NEXT = 1,    // beside it, in the same vector
+  ROT_ANY = 2      // half a rotation away, inside other vectors: found in LDS
+};
 
 // (m cos, m sin) of position * frequency, the sine with the direction's sign.
 __device__ __forceinline__ float2 turn(int pos, double freq, float m, float sign) {
@@ -28,44 +34,237 @@ __device__ __forceinline__ float2 turn(int pos, double freq, float m, float sign
   return make_float2(m * cs, m * sign * sn);
 }
 
-template <typename E>
-__global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(RotaryArgs a) {
-  __shared__ float2 cs[LORA_MAX_HEAD_DIM / 2];
-  const int64_t t = blockIdx.x;
-  const int pos = gload<int>(a.positions + t);
-  if (pos < 0) return;
-  const int half = a.rot_dim / 2, rest = a.head_dim - a.rot_dim;
-  for (int j = threadIdx.x; j < half; j += kRotaryThreads) cs[j] = turn(pos, gload<double>(a.freq + j), a.mscale, a.sign);
-  __syncthreads();
-  for (int s = 0; s < a.n_slices; ++s) {
-    const lora_rotary_slice &v = a.s[s];
-    const E *src = static_cast<const E *>(v.src) + t * v.src_token;
-    E *dst = static_cast<E *>(v.dst) + t * v.dst_token;
-    for (int i = threadIdx.x; i < v.n_heads * half; i += kRotaryThreads) {
-      const int h = i / half, j = i % half;
-      const int p0 = a.interleaved ? 2 * j : j, p1 = a.interleaved ? 2 * j + 1 : j + half;
-      const E *x = src + h * v.src_head;
-      E *y = dst + h * v.dst_head;
-      const float x0 = load_f(x + p0), x1 = load_f(x + p1);
-      store_f(y + p0, x0 * cs[j].x - x1 * cs[j].y);
-      store_f(y + p1, x1 * cs[j].x + x0 * cs[j].y);
+// 16 bytes of a head, at any alignment of its elements.
+template <typename E> struct HeadVec {
+  static constexpr int kN = 16 / int(sizeof(E));
+  uint32_t w[4];
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (sizeof(E) == 4) return __uint_as_float(w[i]);
+    else return i % 2 ? bf_hi(w[i / 2]) : bf_lo(w[i / 2]);
+  }
+  // v[i] in the place of every element for which turned(i) holds
+  template <typename F>
+  __device__ __forceinline__ void put(const float *v, F turned) {
+#pragma unroll
+    for (int i = 0; i < kN; i += 4 / int(sizeof(E))) {
+      if constexpr (sizeof(E) == 4) {
+        w[i] = turned(i) ? __float_as_uint(v[i]) : w[i];
+      } else {
+        const uint32_t u = pack_bf2(v[i], v[i + 1]);
+        const uint32_t keep = (turned(i) ? 0u : 0xffffu) | (turned(i + 1) ? 0u : 0xffff0000u);
+        w[i / 2] = (w[i / 2] & keep) | (u & ~keep);
+      }
     }
-    if (v.src != v.dst)
-      for (int i = threadIdx.x; i < v.n_heads * rest; i += kRotaryThreads) {
-        const int h = i / rest, j = a.rot_dim + i % rest;
-        gstore(dst + h * v.dst_head + j, gload<E>(src + h * v.src_head + j));
+  }
+};
+template <typename E> struct Unaligned;
+template <> struct Unaligned<uint16_t> { typedef uint32_t U __attribute__((ext_vector_type(4), aligned(2))); };
+template <> struct Unaligned<float> { typedef uint32_t U __attribute__((ext_vector_type(4), aligned(4))); };
+
+// The vector at p, of which n elements are there.
+template <typename E>
+__device__ __forceinline__ HeadVec<E> load_head(const E *p, int n) {
+  HeadVec<E> v = {{0u, 0u, 0u, 0u}};
+  if (n >= HeadVec<E>::kN) {
+    const typename Unaligned<E>::U u = *(const LORA_GLOBAL typename Unaligned<E>::U *)p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.w[i] = u[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < HeadVec<E>::kN; ++i)
+      if (i < n) {
+        if constexpr (sizeof(E) == 4) v.w[i] = gload<uint32_t>(p + i);
+        else v.w[i / 2] |= uint32_t(gload<uint16_t>(p + i)) << (i % 2 * 16);
+      }
+  }
+  return v;
+}
+template <typename E>
+__device__ __forceinline__ void store_head(E *p, const HeadVec<E> &v, int n) {
+  if (n >= HeadVec<E>::kN) {
+    const typename Unaligned<E>::U u = {v.w[0], v.w[1], v.w[2], v.w[3]};
+    *(LORA_GLOBAL typename Unaligned<E>::U *)p = u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < HeadVec<E>::kN; ++i)
+      if (i < n) {
+        if constexpr (sizeof(E) == 4) gstore(p + i, v.w[i]);
+        else gstore(p + i, uint16_t(v.w[i / 2] >> (i % 2 * 16)));
       }
   }
 }
 
+// Dynamic LDS: the table [kTokens][rot_dim / 2], and for ROT_ANY a head for
+// each slot, cols * 16 bytes.
+template <typename E, int MODE, int kTokens>
+__global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(RotaryArgs a, int cols, int head_groups) {
+  constexpr int kN = HeadVec<E>::kN;
+  extern __shared__ __align__(16) char lds[];
+  float2 *table = reinterpret_cast<float2 *>(lds);
+  const int half = a.rot_dim / 2, D = a.head_dim;
+  char *rows = lds + (kTokens * half * int(sizeof(float2)) + 15) / 16 * 16;
+  const int slots = kRotaryThreads / cols, slot = threadIdx.x / cols, col = threadIdx.x % cols;
+  const int64_t t0 = int64_t(blockIdx.x / head_groups) * kTokens;
+  const int first = int(blockIdx.x % head_groups) * slots + slot, step = head_groups * slots;
+
+  int pos[kTokens];
+#pragma unroll
+  for (int t = 0; t < kTokens; ++t) pos[t] = t0 + t < a.T ? gload<int>(a.positions + t0 + t) : -1;
+
+  // where this lane's vectors lie in a head, and how much of them is there
+  const bool pair = MODE == ROT_HALVES && col < half / kN;
+  const int i0 = MODE == ROT_HALVES && !pair ? a.rot_dim + (col - half / kN) * kN : col * kN;
+  const int n0 = D - i0;
+
+  HeadVec<E> x0[kTokens], x1[kTokens];
+  E *dst = nullptr;
+  int64_t dst_token = 0;
+  auto load = [&](int g) {
+    // the slice of head g (few slices: a walk over all of them)
+    const E *src = nullptr;
+    int64_t src_token = 0;
+    int start = 0;
+    for (int s = 0; s < a.n_slices; ++s) {
+      const lora_rotary_slice &v = a.s[s];
+      if (g >= start) {
+        src = static_cast<const E *>(v.src) + (g - start) * v.src_head;
+        dst = static_cast<E *>(v.dst) + (g - start) * v.dst_head;
+        src_token = v.src_token;
+        dst_token = v.dst_token;
+      }
+      start += v.n_heads;
+    }
+#pragma unroll
+    for (int t = 0; t < kTokens; ++t)
+      if (pos[t] >= 0) {
+        const E *p = src + (t0 + t) * src_token + i0;
+        x0[t] = load_head(p, n0);
+        if (pair) x1[t] = load_head(p + half, kN);
+      }
+  };
+  const bool mine = slot < slots;
+  // the first heads are on their way while the table is made
+  if (mine && first < a.n_heads) load(first);
+  for (int k = threadIdx.x; k < kTokens * half; k += kRotaryThreads) {
+    const int t = kTokens == 1 ? 0 : k / half;
+    int p = pos[0];
+#pragma unroll
+    for (int u = 1; u < kTokens; ++u) p = t == u ? pos[u] : p;
+    table[k] = turn(max(p, 0), gload<double>(a.freq + (k - t * half)), a.mscale, a.sign);
+  }
+  lds_barrier();
+
+  // all lanes of a workgroup go round as often as its first, which has the most heads
+  for (int g = first; g - slot < a.n_heads; g += step) {
+    const bool live = mine && g < a.n_heads;
+    if (live && g != first) load(g);
+#pragma unroll
+    for (int t = 0; t < kTokens; ++t) {
+      const float2 *cs = table + t * half;
+      if constexpr (MODE == ROT_ANY) {
+        // the barriers are all lanes'
+        if (t > 0 || g != first) lds_barrier();
+        if (live) *reinterpret_cast<uint4 *>(rows + (slot * cols + col) * 16) = make_uint4(x0[t].w[0], x0[t].w[1], x0[t].w[2], x0[t].w[3]);
+        lds_barrier();
+      }
+      if (!live || pos[t] < 0) continue;
+      E *p = dst + (t0 + t) * dst_token + i0;
+      if (MODE == ROT_HALVES && pair) {
+        float y0[kN], y1[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const float2 r = cs[i0 + i];
+          const float u = x0[t].get(i), v = x1[t].get(i);
+          y0[i] = u * r.x - v * r.y;
+          y1[i] = v * r.x + u * r.y;
+        }
+        const auto all = [](int) { return true; };
+        x0[t].put(y0, all);
+        x1[t].put(y1, all);
+        store_head(p + half, x1[t], kN);
+      } else if (MODE == ROT_NEXT) {
+        float y[kN];
+#pragma unroll
+        for (int i = 0; i < kN; i += 2) {
+          const float2 r = cs[min((i0 + i) / 2, half - 1)];
+          const float u = x0[t].get(i), v = x0[t].get(i + 1);
+          y[i] = u * r.x - v * r.y;
+          y[i + 1] = v * r.x + u * r.y;
+        }
+        x0[t].put(y, [&](int i) { return i0 + i < a.rot_dim; });
+      } else if (MODE == ROT_ANY) {
+        const E *row = reinterpret_cast<const E *>(rows + slot * cols * 16);
+        float y[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int at = min(i0 + i, a.rot_dim - 1);
+          const bool low = at < half;
+          const float2 r = cs[low ? at : at - half];
+          const E other = row[low ? at + half : at - half];
+          float v;
+          if constexpr (sizeof(E) == 4) v = other;
+          else v = bf_to_f(other);
+          y[i] = x0[t].get(i) * r.x + v * (low ? -r.y : r.y);
+        }
+        x0[t].put(y, [&](int i) { return i0 + i < a.rot_dim; });
+      }
+      store_head(p, x0[t], n0);
+    }
+  }
+}
+
+template <typename E, int MODE>
+hipError_t launch_mode(const RotaryArgs &a, bool copy_rest, hipStream_t stream) {
+  constexpr int kN = HeadVec<E>::kN;
+  const int half = a.rot_dim / 2, rest = a.head_dim - a.rot_dim;
+  // columns of a head that the call has to visit; in place those of the pairs
+  int cols;
+  if (MODE == ROT_HALVES) cols = half / kN + (copy_rest ? (rest + kN - 1) / kN : 0);
+  else cols = ((copy_rest ? a.head_dim : a.rot_dim) + kN - 1) / kN;
+  const int slots = kRotaryThreads / cols;
+  const size_t rows = MODE == ROT_ANY ? size_t(slots) * cols * 16 : 0;
+  // Few tokens: one a workgroup, and as many workgroups a token as its heads
+  // fill.  Many: four, which share the table's work and have four times the
+  // loads in flight.
+  constexpr int kMany = 4;
+  if (a.T >= 4096) {
+    const size_t smem = (size_t(kMany) * half * sizeof(float2) + 15) / 16 * 16 + rows;
+    rotary_kernel<E, MODE, kMany><<<dim3(uint32_t((a.T - 1) / kMany + 1)), kRotaryThreads, smem, stream>>>(a, cols, 1);
+  } else {
+    const size_t smem = (size_t(half) * sizeof(float2) + 15) / 16 * 16 + rows;
+    const int groups = min((a.n_heads - 1) / slots + 1, 256);
+    rotary_kernel<E, MODE, 1><<<dim3(uint32_t(a.T) * uint32_t(groups)), kRotaryThreads, smem, stream>>>(a, cols, groups);
+  }
+  return hipGetLastError();
+}
+
+template <typename E>
+hipError_t launch_typed(const RotaryArgs &a, hipStream_t stream) {
+  bool copy_rest = false;
+  for (int s = 0; s < a.n_slices; ++s) copy_rest = copy_rest || a.s[s].src != a.s[s].dst;
+  if (a.interleaved) return launch_mode<E, ROT_NEXT>(a, copy_rest, stream);
+  if (a.rot_dim / 2 % HeadVec<E>::kN == 0) return launch_mode<E, ROT_HALVES>(a, copy_rest, stream);
+  return launch_mode<E, ROT_ANY>(a, copy_rest, stream);
+}
+
 }  // namespace
 
-hipError_t launch_rotary(const RotaryArgs &a, int dtype, hipStream_t stream) {
-  if (dtype == LORA_BF16)
-    rotary_kernel<uint16_t><<<a.T, kRotaryThreads, 0, stream>>>(a);
-  else
-    rotary_kernel<float><<<a.T, kRotaryThreads, 0, stream>>>(a);
-  return hipGetLastError();
+hipError_t launch_rotary(const RotaryArgs &args, int dtype, hipStream_t stream) {
+  // a grid holds so many tokens; the rest in further launches
+  constexpr int kMost = 1 << 24;
+  const int64_t eb = dtype == LORA_BF16 ? 2 : 4;
+  for (int64_t t = 0; t < args.T; t += kMost) {
+    RotaryArgs a = args;
+    a.positions += t;
+    a.T = int(args.T - t < kMost ? args.T - t : kMost);
+    for (int s = 0; s < a.n_slices; ++s) {
+      a.s[s].src = static_cast<const char *>(a.s[s].src) + t * a.s[s].src_token * eb;
+      a.s[s].dst = static_cast<char *>(a.s[s].dst) + t * a.s[s].dst_token * eb;
+    }
+    const hipError_t e = dtype == LORA_BF16 ? launch_typed<uint16_t>(a, stream) : launch_typed<float>(a, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace lora
