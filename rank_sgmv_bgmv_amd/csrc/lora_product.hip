@@ -38,10 +38,14 @@ __device__ __forceinline__ void store_y(const ProductArgs &a, float *y, int o, c
   }
 }
 
+// 16 bytes from p, at any alignment.
+__device__ __forceinline__ i32x4 load16(const int8_t *p) {
+  typedef int i32x4u __attribute__((ext_vector_type(4), aligned(1)));
+  return *(const LORA_GLOBAL i32x4u *)p;
+}
 // 16 bytes from p, of which the first n (any whole number) are there: the rest are zeros.
 __device__ __forceinline__ i32x4 load16(const int8_t *p, int n) {
-  typedef int i32x4u __attribute__((ext_vector_type(4), aligned(1)));
-  if (n >= 16) return *(const LORA_GLOBAL i32x4u *)p;
+  if (n >= 16) return load16(p);
   union {
     i32x4 v;
     int8_t b[16];
@@ -106,26 +110,12 @@ __global__ __launch_bounds__(256) void product_any_kernel(ProductArgs a) {
   }
 }
 
-// ------------------------------------------------------------ large tiles --
-//
-// MT * 32 channels x NT * 32 tokens by four waves (2 x 2, each MT x NT blocks
-// of v_mfma_i32_16x16x64_i8).  The sum's axis goes in stages of 128 values,
-// copied to LDS without passing registers, two stages in LDS: stage i + 2 is on
-// its way while stage i + 1 lies ready and i is multiplied.  Within a stage
-// the operands of one 64-value step are read from LDS while the step before
-// is multiplied, across stages too, so the matrix unit waits for nothing but
-// the one barrier of a stage.
-//
-// What bounds it is power: four waves on every CU that only multiply random
-// 8-bit numbers run at 1.79 GHz (3.68 POP/s) with 16 x 16 blocks and at 1.44
-// GHz (2.97 POP/s) with 32 x 32 ones, which move twice the sums.  So 16 x 16
-// blocks, and the largest tile that fits the registers, 8 x 8 blocks a wave,
-// which reads the fewest operands from LDS for each product.
-//
-// A row of a stage is 128 bytes, eight 16-byte pieces; piece c of row r lies
-// at place c ^ (r & 7), so that eight lanes reading one piece of neighbouring
-// rows meet every bank once.  The copy writes LDS in lane order, so the lanes
-// take their global pieces in that order instead.
+// ------------------------------------------------- copies to LDS and waits --
+// The sum's axis goes through LDS in stages of 128 values.  A row of a stage is
+// 128 bytes, eight 16-byte pieces; piece c of row r lies at place c ^ (r & 7),
+// so that eight lanes reading one piece of neighbouring rows meet every bank
+// once.  A copy (eight rows) writes LDS in lane order, so the lanes take their
+// global pieces in that order instead.
 constexpr int kStage = 128;
 
 // 16 bytes a lane from base + off straight to LDS at `lds` (wave-uniform) + 16 lane.
@@ -155,6 +145,237 @@ __device__ __forceinline__ void wait_stages(int stages) {
 }
 __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xc07f); }  // lgkmcnt(0)
 __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory"); }
+
+// --------------------------------------------------------------- few rows --
+//
+// Up to NT * 16 tokens: bound by reading the weights once.  A workgroup takes
+// MT * 16 channels and all tokens, its eight waves an eighth of the sum's axis
+// each, so that a weight of 4096 channels fills the chip and a CU has 16 waves
+// of loads on their way.  Operands go straight to registers, four 64-value
+// steps at a time while the four before are multiplied; any alignment and any
+// length (only the last steps look where the rows end).  The waves' sums meet
+// in LDS.
+constexpr int kFewWaves = 8, kFewSteps = 4;
+template <typename E, int MT, int NT>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void product_few_kernel(ProductArgs a) {
+  __shared__ i32x4 part[kFewWaves][MT * NT][64];
+  const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64);
+  const int steps = (a.d_in + 63) / 64, each = (steps + kFewWaves - 1) / kFewWaves;
+  const int begin = wave * each, end = min(begin + each, steps), whole = min(end, a.d_in / 64);
+  for (int o0 = blockIdx.x * MT * 16; o0 < a.d_out; o0 += gridDim.x * MT * 16) {
+    // rows past the end: the last row again
+    const int8_t *pw[MT], *px[NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) pw[m] = a.W + int64_t(min(o0 + m * 16 + lane % 16, a.d_out - 1)) * a.ldw + lane / 16 * 16;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) px[j] = a.q + int64_t(min(j * 16 + lane % 16, a.T - 1)) * a.ldq + lane / 16 * 16;
+    i32x4 acc[MT][NT] = {};
+    i32x4 w[2][kFewSteps][MT], x[2][kFewSteps][NT];
+    auto load = [&](int step, int set) {
+#pragma unroll
+      for (int u = 0; u < kFewSteps; ++u) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) w[set][u][m] = load16(pw[m] + (step + u) * 64);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) x[set][u][j] = load16(px[j] + (step + u) * 64);
+      }
+    };
+    auto multiply_set = [&](int set) {
+#pragma unroll
+      for (int u = 0; u < kFewSteps; ++u)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            acc[m][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[set][u][m], x[set][u][j], acc[m][j], 0, 0, 0);
+    };
+    int k = begin;
+    if (k + kFewSteps <= whole) {
+      load(k, 0);
+      for (; k + 3 * kFewSteps <= whole; k += 2 * kFewSteps) {
+        load(k + kFewSteps, 1);
+        multiply_set(0);
+        load(k + 2 * kFewSteps, 0);
+        multiply_set(1);
+      }
+      if (k + 2 * kFewSteps <= whole) {
+        load(k + kFewSteps, 1);
+        multiply_set(0);
+        multiply_set(1);
+        k += 2 * kFewSteps;
+      } else {
+        multiply_set(0);
+        k += kFewSteps;
+      }
+    }
+    for (; k < end; ++k) {
+      // q counts as zero past the end; what W holds there is not read either
+      const int n = a.d_in - k * 64 - lane / 16 * 16;
+      i32x4 wt[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) wt[m] = load16(pw[m] + k * 64, n);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const i32x4 xt = load16(px[j] + k * 64, n);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[m][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wt[m], xt, acc[m][j], 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) part[wave][m * NT + j][lane] = acc[m][j];
+    lds_barrier();
+    for (int b = wave; b < MT * NT; b += kFewWaves) {
+      const int m = b / NT, j = b % NT, t = j * 16 + lane % 16, o = o0 + m * 16 + lane / 16 * 4;
+      i32x4 sum = part[0][b][lane];
+#pragma unroll
+      for (int v = 1; v < kFewWaves; ++v) sum += part[v][b][lane];
+      if (t < a.T && o < a.d_out) {
+        const float sx = gload<float>(a.q_scale + t);
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = min(o + e, a.d_out - 1);
+          v[e] = float(sum[e]) * sx * gload<float>(a.w_scale + c) + bias_of(a, c);
+        }
+        store_y(a, static_cast<E *>(a.y) + t * a.ldy, o, v);
+      }
+    }
+    lds_barrier();
+  }
+}
+
+template <typename E, int MT, int NT>
+hipError_t launch_few(const ProductArgs &a, hipStream_t stream) {
+  const int groups = (a.d_out - 1) / (MT * 16) + 1;
+  product_few_kernel<E, MT, NT><<<dim3(uint32_t(groups < (1 << 20) ? groups : 1 << 20)), 64 * kFewWaves, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+// The same for rows of whole 16-byte pieces and more tokens, whose operands
+// would come 16 bytes a row and clock that way (a lane's neighbours hold other
+// rows): each wave copies its stages to its own part of LDS in whole lines,
+// one stage ahead, and needs no barrier before the sums meet.
+template <int NT>
+struct FewShape {
+  static constexpr int kRows = 16 + NT * 16, kCopies = kRows / 8, kBytes = kRows * kStage;  // of a wave's stage
+  static constexpr int kLds = kFewWaves * 2 * kBytes;  // the sums take the same place afterwards
+  static_assert(kLds <= kMaxLdsBytes && kFewWaves * NT * 1024 <= kLds, "");
+};
+template <typename E, int NT>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void product_few_lines_kernel(ProductArgs a) {
+  typedef FewShape<NT> S;
+  extern __shared__ __align__(16) int8_t lds[];
+  const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64);
+  const int stages = (a.d_in + kStage - 1) / kStage, each = (stages + kFewWaves - 1) / kFewWaves;
+  const int begin = wave * each, end = min(begin + each, stages);
+  const int piece = (lane % 8) ^ (lane / 8);
+  int8_t *mine = lds + wave * 2 * S::kBytes;
+  const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) int8_t *)mine));
+  uint32_t off_x[2 * NT];
+#pragma unroll
+  for (int i = 0; i < 2 * NT; ++i) off_x[i] = uint32_t(min(i * 8 + lane / 8, a.T - 1)) * uint32_t(a.ldq) + piece * 16;
+  for (int o0 = blockIdx.x * 16; o0 < a.d_out; o0 += gridDim.x * 16) {
+    const int8_t *W = a.W + int64_t(o0) * a.ldw;
+    uint32_t off_w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) off_w[i] = uint32_t(min(i * 8 + lane / 8, a.d_out - 1 - o0)) * uint32_t(a.ldw) + piece * 16;
+    auto copy = [&](int stage) {
+      // pieces past the end of the rows are not read: the stage's first piece stands in (and is masked below)
+      const uint32_t back = stage * kStage + piece * 16 < a.d_in ? 0u : piece * 16u;
+      const uint32_t at = lds0 + (stage & 1) * S::kBytes;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) copy_to_lds(W + stage * kStage, off_w[i] - back, at + i * 1024);
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) copy_to_lds(a.q + stage * kStage, off_x[i] - back, at + (2 + i) * 1024);
+    };
+    i32x4 acc[NT] = {};
+    if (begin < end) copy(begin);
+    if (begin + 1 < end) copy(begin + 1);
+    for (int i = begin; i < end; ++i) {
+      if (i + 1 < end)
+        wait_copies<S::kCopies>();
+      else
+        wait_copies<0>();
+      __builtin_amdgcn_sched_barrier(0);
+      const int8_t *p = mine + (i & 1) * S::kBytes + lane % 16 * kStage;
+      i32x4 w[2], x[2][NT];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int at = ((s * 4 + lane / 16) ^ (lane & 7)) * 16;
+        w[s] = *reinterpret_cast<const i32x4 *>(p + at);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) x[s][j] = *reinterpret_cast<const i32x4 *>(p + (16 + j * 16) * kStage + at);
+      }
+      wait_lds();
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + 2 < end) copy(i + 2);
+      if (i == stages - 1) {
+        // past the end of the sum's axis the weights count as zero
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const bool in = i * kStage + s * 64 + lane / 16 * 16 < a.d_in;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[s][e] = in ? w[s][e] : 0;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s], x[s][j], acc[j], 0, 0, 0);
+    }
+    i32x4 *part = reinterpret_cast<i32x4 *>(lds);
+    lds_barrier();  // every wave is done with its stages
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[(wave * NT + j) * 64 + lane] = acc[j];
+    lds_barrier();
+    if (wave < NT) {
+      const int t = wave * 16 + lane % 16, o = o0 + lane / 16 * 4;
+      i32x4 sum = part[wave * 64 + lane];
+#pragma unroll
+      for (int v = 1; v < kFewWaves; ++v) sum += part[(v * NT + wave) * 64 + lane];
+      if (t < a.T && o < a.d_out) {
+        const float sx = gload<float>(a.q_scale + t);
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = min(o + e, a.d_out - 1);
+          v[e] = float(sum[e]) * sx * gload<float>(a.w_scale + c) + bias_of(a, c);
+        }
+        store_y(a, static_cast<E *>(a.y) + t * a.ldy, o, v);
+      }
+    }
+    lds_barrier();
+  }
+}
+
+template <typename E, int NT>
+hipError_t launch_few_lines(const ProductArgs &a, hipStream_t stream) {
+  typedef FewShape<NT> S;
+  const auto kernel = product_few_lines_kernel<E, NT>;
+  static const bool ready = raise_lds_limit(reinterpret_cast<const void *>(kernel), S::kLds);
+  (void)ready;
+  const int groups = (a.d_out - 1) / 16 + 1;
+  kernel<<<dim3(uint32_t(groups < (1 << 20) ? groups : 1 << 20)), 64 * kFewWaves, S::kLds, stream>>>(a);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------ large tiles --
+//
+// MT * 32 channels x NT * 32 tokens by four waves (2 x 2, each MT x NT blocks
+// of v_mfma_i32_16x16x64_i8).  The sum's axis goes in stages of 128 values,
+// copied to LDS without passing registers, two stages in LDS: stage i + 2 is on
+// its way while stage i + 1 lies ready and i is multiplied.  Within a stage
+// the operands of one 64-value step are read from LDS while the step before
+// is multiplied, across stages too, so the matrix unit waits for nothing but
+// the one barrier of a stage.
+//
+// What bounds it is power: four waves on every CU that only multiply random
+// 8-bit numbers run at 1.79 GHz (3.68 POP/s) with 16 x 16 blocks and at 1.44
+// GHz (2.97 POP/s) with 32 x 32 ones, which move twice the sums.  So 16 x 16
+// blocks, and the largest tile that fits the registers, 8 x 8 blocks a wave,
+// which reads the fewest operands from LDS for each product.
 
 // c += a b^T on a 16 x 16 block, c kept where it is: given the choice, the
 // compiler writes the sums elsewhere and moves 200 registers back each stage.
@@ -446,6 +667,13 @@ hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
   a.y_vec = aligned16(a.y) && a.ldy * int64_t(sizeof(E)) % 16 == 0;
   const bool lines = aligned16(a.q) && aligned16(a.W) && a.ldq % 16 == 0 && a.ldw % 16 == 0 && a.d_in % 16 == 0 &&
                      a.ldq <= (1 << 22) && a.ldw <= (1 << 22);
+  if (a.T <= 64) {
+    const bool wide = false;
+    if (lines) return a.T <= 16 ? launch_few_lines<E, 1>(a, stream) : a.T <= 32 ? launch_few_lines<E, 2>(a, stream) : launch_few_lines<E, 4>(a, stream);
+    if (a.T <= 16) return wide ? launch_few<E, 2, 1>(a, stream) : launch_few<E, 1, 1>(a, stream);
+    if (a.T <= 32) return wide ? launch_few<E, 2, 2>(a, stream) : launch_few<E, 1, 2>(a, stream);
+    return wide ? launch_few<E, 2, 4>(a, stream) : launch_few<E, 1, 4>(a, stream);
+  }
   if (lines) {
     switch (choose_tile(a)) {
       case 0: return launch_tiles<E, 8, 4, 2, 4, 2>(a, stream);
