@@ -6,6 +6,7 @@
 // which is the order in which v_mfma_i32_16x16x64_i8 takes them: a lane holds
 // 16 consecutive values of one row.
 
+#include <algorithm>
 #include <type_traits>
 
 #include "lora_base.hpp"
@@ -42,6 +43,17 @@ __device__ __forceinline__ void store_y(const ProductArgs &a, float *y, int o, c
 __device__ __forceinline__ i32x4 load16(const int8_t *p) {
   typedef int i32x4u __attribute__((ext_vector_type(4), aligned(1)));
   return *(const LORA_GLOBAL i32x4u *)p;
+}
+// The 16 bytes at k of a row of d_in (16 or more) bytes, zeros past its end:
+// read from further ahead where they would pass it, and moved down.
+__device__ __forceinline__ i32x4 load16_end(const int8_t *row, int k, int d_in) {
+  const int start = min(k, d_in - 16), bits = min(k - start, 16) * 8;
+  const i32x4 v = load16(row + start);
+  const uint64_t lo = uint32_t(v[0]) | uint64_t(uint32_t(v[1])) << 32, hi = uint32_t(v[2]) | uint64_t(uint32_t(v[3])) << 32;
+  const int b = bits & 63;
+  const uint64_t down = b ? hi << (64 - b) : 0;
+  const uint64_t l = bits < 64 ? lo >> b | down : bits < 128 ? hi >> b : 0, h = bits < 64 ? hi >> b : 0;
+  return i32x4{int(uint32_t(l)), int(uint32_t(l >> 32)), int(uint32_t(h)), int(uint32_t(h >> 32))};
 }
 // 16 bytes from p, of which the first n (any whole number) are there: the rest are zeros.
 __device__ __forceinline__ i32x4 load16(const int8_t *p, int n) {
@@ -162,7 +174,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void product_few_kernel(ProductA
   const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64);
   const int steps = (a.d_in + 63) / 64, each = (steps + kFewWaves - 1) / kFewWaves;
   const int begin = wave * each, end = min(begin + each, steps), whole = min(end, a.d_in / 64);
-  for (int o0 = blockIdx.x * MT * 16; o0 < a.d_out; o0 += gridDim.x * MT * 16) {
+  {
+    const int o0 = blockIdx.x * MT * 16;
     // rows past the end: the last row again
     const int8_t *pw[MT], *px[NT];
 #pragma unroll
@@ -209,14 +222,13 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void product_few_kernel(ProductA
       }
     }
     for (; k < end; ++k) {
-      // q counts as zero past the end; what W holds there is not read either
-      const int n = a.d_in - k * 64 - lane / 16 * 16;
+      const int piece = lane / 16 * 16;  // already in the pointers
       i32x4 wt[MT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) wt[m] = load16(pw[m] + k * 64, n);
+      for (int m = 0; m < MT; ++m) wt[m] = load16_end(pw[m] - piece, k * 64 + piece, a.d_in);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const i32x4 xt = load16(px[j] + k * 64, n);
+        const i32x4 xt = load16_end(px[j] - piece, k * 64 + piece, a.d_in);
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[m][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wt[m], xt, acc[m][j], 0, 0, 0);
       }
@@ -249,7 +261,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void product_few_kernel(ProductA
 template <typename E, int MT, int NT>
 hipError_t launch_few(const ProductArgs &a, hipStream_t stream) {
   const int groups = (a.d_out - 1) / (MT * 16) + 1;
-  product_few_kernel<E, MT, NT><<<dim3(uint32_t(groups < (1 << 20) ? groups : 1 << 20)), 64 * kFewWaves, 0, stream>>>(a);
+  product_few_kernel<E, MT, NT><<<dim3(uint32_t(groups)), 64 * kFewWaves, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -276,7 +288,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void product_few_lines_kernel(Pr
   uint32_t off_x[2 * NT];
 #pragma unroll
   for (int i = 0; i < 2 * NT; ++i) off_x[i] = uint32_t(min(i * 8 + lane / 8, a.T - 1)) * uint32_t(a.ldq) + piece * 16;
-  for (int o0 = blockIdx.x * 16; o0 < a.d_out; o0 += gridDim.x * 16) {
+  {
+    const int o0 = blockIdx.x * 16;
     const int8_t *W = a.W + int64_t(o0) * a.ldw;
     uint32_t off_w[2];
 #pragma unroll
@@ -357,7 +370,7 @@ hipError_t launch_few_lines(const ProductArgs &a, hipStream_t stream) {
   static const bool ready = raise_lds_limit(reinterpret_cast<const void *>(kernel), S::kLds);
   (void)ready;
   const int groups = (a.d_out - 1) / 16 + 1;
-  kernel<<<dim3(uint32_t(groups < (1 << 20) ? groups : 1 << 20)), 64 * kFewWaves, S::kLds, stream>>>(a);
+  kernel<<<dim3(uint32_t(groups)), 64 * kFewWaves, S::kLds, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -420,7 +433,7 @@ struct TileShape {
   static_assert(kO % (8 * kWaves) == 0 && kT % (8 * kWaves) == 0, "every wave copies the same");
 };
 
-template <typename E, int MT, int NT, int WM, int WN, int ST>
+template <typename E, int MT, int NT, int WM, int WN, int ST, bool LINES>
 __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductArgs a, int tiles_o, int tiles_t) {
   typedef TileShape<E, MT, NT, WM, WN, ST> S;
   extern __shared__ __align__(16) int8_t lds[];
@@ -460,6 +473,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   };
   // pieces past the end of the rows are not read: the stage's first piece stands in (and is masked below)
   auto back_of = [&](int stage) -> uint32_t { return stage * kStage + piece * 16 < a.d_in ? 0u : piece * 16u; };
+  // Rows of any alignment go through registers: a stage's pieces are read a
+  // stage before they are written to LDS.
+  i32x4 held[LINES ? 1 : kCopies];
+  auto fetch = [&](int i, int stage, bool whole) {
+    const int8_t *row = (i < S::kCopyO ? W : q) + (off[i] - piece * 16);
+    held[i] = whole ? load16(row + stage * kStage + piece * 16) : load16_end(row, stage * kStage + piece * 16, a.d_in);
+  };
+  auto put = [&](int i, int stage) {
+    const int at = (stage & (ST - 1)) * S::kBytes +
+                   (i < S::kCopyO ? (wave * S::kCopyO + i) * 1024 : S::kO * kStage + (wave * S::kCopyT + i - S::kCopyO) * 1024);
+    *reinterpret_cast<i32x4 *>(lds + at + lane * 16) = held[i];
+  };
 
   const int wm = wave / WN, wn = wave % WN;
   const int8_t *lw = lds + (wm * MT * 16 + lane % 16) * kStage, *lx = lds + (S::kO + wn * NT * 16 + lane % 16) * kStage;
@@ -485,10 +510,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
 #pragma unroll
   for (int i = 0; i * S::kThreads < S::kT; ++i)
     scale_t[i] = gload<float>(a.q_scale + t0 + min(tid + i * S::kThreads, n_t - 1));
-  for (int st = 0; st < min(n, ST); ++st) {
-    const uint32_t back = back_of(st);
+  if constexpr (LINES) {
+    for (int st = 0; st < min(n, ST); ++st) {
+      const uint32_t back = back_of(st);
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) copy(i, st, back);
+      for (int i = 0; i < kCopies; ++i) copy(i, st, back);
+    }
+  } else {
+    static_assert(LINES || ST == 2, "a third stage is in registers");
+    for (int st = 0; st < 3; ++st) {
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) fetch(i, min(st, n - 1), false);
+      if (st == 2) break;
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) put(i, st);
+    }
   }
 #pragma unroll
   for (int i = 0; i * S::kThreads < S::kO; ++i)
@@ -496,7 +532,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
 #pragma unroll
   for (int i = 0; i * S::kThreads < S::kT; ++i)
     if (tid + i * S::kThreads < S::kT) s_t[tid + i * S::kThreads] = scale_t[i];
-  wait_stages<kCopies, ST - 1>(n - 1);
+  if constexpr (LINES) wait_stages<kCopies, ST - 1>(n - 1);
   wait_lds();
   meet();
 #pragma unroll
@@ -517,15 +553,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
       wait_lds();
       if (s == 1 && !masked) {
         // what may still be on its way: the stages after the next one
-        if constexpr (more)
+        if constexpr (LINES && more)
           wait_copies<kCopies *(ST - 2)>();
-        else
+        else if constexpr (LINES)
           wait_stages<kCopies, ST - 2>(n - 2 - i);
         meet();
       }
       const int p = place(s ? i + 1 : i, s ^ 1);
-      const uint32_t back = more && s == 1 ? back_of(i + ST) : 0;
-      if constexpr (masked) {
+      const uint32_t back = LINES && more && s == 1 ? back_of(i + ST) : 0;
+      if constexpr (LINES && masked) {
         // past the end of the sum's axis q counts as zero
         const bool in = i * kStage + s * 64 + lane / 16 * 16 < a.d_in;
 #pragma unroll
@@ -537,7 +573,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
 #pragma unroll
       for (int t = 0; t < kMul; ++t) {
         __builtin_amdgcn_sched_barrier(0);
-        if (more && s == 1 && t % kCopyEach == 0 && t / kCopyEach < kCopies) copy(t / kCopyEach, i + ST, back);
+        if constexpr (LINES) {
+          if (more && s == 1 && t % kCopyEach == 0 && t / kCopyEach < kCopies) copy(t / kCopyEach, i + ST, back);
+        } else if (!masked && s == 1 && t % kCopyEach == 0 && t / kCopyEach < kCopies) {
+          put(t / kCopyEach, i + ST);
+          fetch(t / kCopyEach, more ? i + ST + 1 : min(i + ST + 1, n - 1), more);
+        }
         if (s == 0 && t < kReads) read(t, p, 1);
         if (!masked && s == 1 && t >= kReadAt && t < kReadAt + kReads) read(t - kReadAt, p, 0);
         __builtin_amdgcn_sched_barrier(0);
@@ -546,7 +587,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     }
   };
   int i = 0;
-  for (; i < n - ST; ++i) stage(i, std::true_type{}, std::false_type{});
+  // (in registers: `more` as long as the stage to be read is a whole one)
+  for (; i < (LINES ? n - ST : n - ST - 2); ++i) stage(i, std::true_type{}, std::false_type{});
   for (; i < n - 1; ++i) stage(i, std::false_type{}, std::false_type{});
   stage(i, std::false_type{}, std::true_type{});
   settled(acc);
@@ -617,10 +659,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   }
 }
 
-template <typename E, int MT, int NT, int WM, int WN, int ST>
+template <typename E, int MT, int NT, int WM, int WN, int ST, bool LINES = true>
 hipError_t launch_tiles(const ProductArgs &a, hipStream_t stream) {
   typedef TileShape<E, MT, NT, WM, WN, ST> S;
-  const auto kernel = product_tile_kernel<E, MT, NT, WM, WN, ST>;
+  const auto kernel = product_tile_kernel<E, MT, NT, WM, WN, ST, LINES>;
   static const bool ready = raise_lds_limit(reinterpret_cast<const void *>(kernel), S::kLds);
   (void)ready;
   const int tiles_o = (a.d_out + S::kO - 1) / S::kO;
@@ -643,39 +685,49 @@ struct TileCost {
 };
 constexpr TileCost kTileCosts[] = {
     {256, 256, 1, 1.30f, 1.30f, 7.0f}, {192, 256, 1, 1.05f, 1.05f, 6.0f}, {128, 128, 2, 0.60f, 0.85f, 3.0f},
-    {128, 128, 1, 0.50f, 0.50f, 3.0f}, {128, 64, 1, 0.33f, 0.33f, 2.5f},  {64, 64, 2, 0.20f, 0.41f, 2.0f},
+    {128, 128, 1, 0.50f, 0.50f, 3.0f}, {128, 64, 1, 0.33f, 0.33f, 2.5f},  {64, 64, 2, 0.20f, 0.41f, 3.0f},
 };
 
-int choose_tile(const ProductArgs &a) {
+// The shape of the least cost, among those whose bit is set in `among`.
+int choose_tile(const ProductArgs &a, unsigned among, double &least) {
   const int64_t cus = cu_count(), n = (a.d_in + kStage - 1) / kStage;
-  int best = 0;
-  double least = 0;
+  int best = -1;
   for (int k = 0; k < int(sizeof(kTileCosts) / sizeof(kTileCosts[0])); ++k) {
+    if (!(among >> k & 1)) continue;
     const TileCost &c = kTileCosts[k];
     const int64_t tiles = int64_t((a.d_out - 1) / c.o + 1) * ((a.T - 1) / c.t + 1);
     const int64_t rounds = tiles / (cus * c.at_once), rest = tiles % (cus * c.at_once);
     double us = rounds * double(n * c.full + c.once);
     if (rest) us += n * (rest <= cus ? c.alone : c.full) + c.once;
-    if (k == 0 || us < least) best = k, least = us;
+    if (best < 0 || us < least) best = k, least = us;
   }
   return best;
+}
+
+// What the kernel for few rows costs, likewise: a wave's stages, in as many
+// rounds as its workgroups fill the chip (two on a CU up to 16 rows).  64 rows
+// through 4096 x 4096 take 7.9 us with it and 9.3 with 64 x 64 tiles, through
+// 4096 x 14336, whose channels make it read the rows 896 times, 29.5 and 16.8.
+double cost_of_few(const ProductArgs &a) {
+  const int each = ((a.d_in + kStage - 1) / kStage + kFewWaves - 1) / kFewWaves, nt = (a.T + 15) / 16;
+  const double stage = nt <= 1 ? 0.75 : nt <= 2 ? 0.9 : 1.3, at_once = nt <= 1 ? 2 : 1;
+  return std::max(1.0, ((a.d_out - 1) / 16 + 1) / (at_once * cu_count())) * (2.2 + stage * each);
 }
 
 template <typename E>
 hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
   ProductArgs a = args;
   a.y_vec = aligned16(a.y) && a.ldy * int64_t(sizeof(E)) % 16 == 0;
-  const bool lines = aligned16(a.q) && aligned16(a.W) && a.ldq % 16 == 0 && a.ldw % 16 == 0 && a.d_in % 16 == 0 &&
-                     a.ldq <= (1 << 22) && a.ldw <= (1 << 22);
-  if (a.T <= 64) {
-    const bool wide = false;
-    if (lines) return a.T <= 16 ? launch_few_lines<E, 1>(a, stream) : a.T <= 32 ? launch_few_lines<E, 2>(a, stream) : launch_few_lines<E, 4>(a, stream);
-    if (a.T <= 16) return wide ? launch_few<E, 2, 1>(a, stream) : launch_few<E, 1, 1>(a, stream);
-    if (a.T <= 32) return wide ? launch_few<E, 2, 2>(a, stream) : launch_few<E, 1, 2>(a, stream);
-    return wide ? launch_few<E, 2, 4>(a, stream) : launch_few<E, 1, 4>(a, stream);
-  }
-  if (lines) {
-    switch (choose_tile(a)) {
+  const bool lines = aligned16(a.q) && aligned16(a.W) && a.ldq % 16 == 0 && a.ldw % 16 == 0 && a.d_in % 16 == 0;
+  const bool near = a.ldq <= (1 << 22) && a.ldw <= (1 << 22);  // a tile's rows within 32-bit offsets
+  double us = 0;
+  if (near && lines) {
+    const int tile = choose_tile(a, ~0u, us);
+    if (a.T <= 64 && cost_of_few(a) < us)
+      return a.T <= 16   ? launch_few_lines<E, 1>(a, stream)
+             : a.T <= 32 ? launch_few_lines<E, 2>(a, stream)
+                         : launch_few_lines<E, 4>(a, stream);
+    switch (tile) {
       case 0: return launch_tiles<E, 8, 4, 2, 4, 2>(a, stream);
       case 1: return launch_tiles<E, 6, 4, 2, 4, 2>(a, stream);
       case 2: return launch_tiles<E, 4, 4, 2, 2, 2>(a, stream);
@@ -684,6 +736,11 @@ hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
       default: return launch_tiles<E, 2, 2, 2, 2, 4>(a, stream);
     }
   }
+  if (a.d_in >= 16 && a.T <= 16) return launch_few<E, 1, 1>(a, stream);
+  if (a.d_in >= 16 && near) {
+    if (choose_tile(a, 1u << 2 | 1u << 5, us) == 2) return launch_tiles<E, 4, 4, 2, 2, 2, false>(a, stream);
+    return launch_tiles<E, 2, 2, 2, 2, 2, false>(a, stream);
+  }
   const dim3 grid((a.d_out + kAnyTile - 1) / kAnyTile, (a.T + kAnyTile - 1) / kAnyTile);
   product_any_kernel<E><<<grid, 256, 0, stream>>>(a);
   return hipGetLastError();
@@ -691,8 +748,25 @@ hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_product(const ProductArgs &a, int dtype, hipStream_t stream) {
-  return dtype == LORA_BF16 ? launch_typed<uint16_t>(a, stream) : launch_typed<float>(a, stream);
+hipError_t launch_product(const ProductArgs &args, int dtype, hipStream_t stream) {
+  // what a launch may hold, at one thread for every 16 results at least
+  constexpr int kMostT = 1 << 18, kMostO = 1 << 17;
+  const int64_t eb = dtype == LORA_BF16 ? 2 : 4;
+  for (int64_t t = 0; t < args.T; t += kMostT)
+    for (int64_t o = 0; o < args.d_out; o += kMostO) {
+      ProductArgs a = args;
+      a.q += t * a.ldq;
+      a.q_scale += t;
+      a.W += o * a.ldw;
+      a.w_scale += o;
+      if (a.bias) a.bias += o;
+      a.y = static_cast<char *>(a.y) + (t * a.ldy + o) * eb;
+      a.T = int(std::min<int64_t>(kMostT, args.T - t));
+      a.d_out = int(std::min<int64_t>(kMostO, args.d_out - o));
+      const hipError_t e = dtype == LORA_BF16 ? launch_typed<uint16_t>(a, stream) : launch_typed<float>(a, stream);
+      if (e != hipSuccess) return e;
+    }
+  return hipSuccess;
 }
 
 }  // namespace lora
