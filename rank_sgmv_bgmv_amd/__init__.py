@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 from . import accounting  # noqa: F401  (pure Python byte/FLOP accounting)
@@ -74,6 +75,8 @@ class lora_rotary_slice(ctypes.Structure):
                 ("src_head", ctypes.c_int64), ("dst_token", ctypes.c_int64), ("dst_head", ctypes.c_int64),
                 ("n_heads", ctypes.c_int32)]
 
+
+_pack_slice = struct.Struct("@PPqqqqi4x").pack  # a lora_rotary_slice's bytes
 
 LORA_ROTARY_PLAIN, LORA_ROTARY_LINEAR, LORA_ROTARY_BASE, LORA_ROTARY_PARTS = 0, 1, 2, 3
 LORA_MAX_SLICES = 8
@@ -570,7 +573,7 @@ def lora_rotary_apply(rotary: Rotary, positions, src: Sequence, dst: Optional[Se
     code = _REAL.get(dtype, -1)
     if code < 0:
         raise LoraError(-2, f"{what}: heads must be bfloat16 or float32 (got {dtype})")
-    slices = (lora_rotary_slice * n)()
+    slices = b""
     for i in range(n):
         a = src[i]
         shape, sa, pa = a.shape, a.stride(), a.data_ptr()
@@ -585,9 +588,8 @@ def lora_rotary_apply(rotary: Rotary, positions, src: Sequence, dst: Optional[Se
             if b.dtype is not dtype or b.get_device() != index or b.shape != shape or (sb[2] != 1 and D > 1):
                 raise LoraError(-2, f"{what}: dst must be like src (got {b.dtype} {tuple(b.shape)} on {b.device}, "
                                     f"strides {sb})")
-        slices[i] = (pa, pb, sa[0], sa[1], sb[0], sb[1], shape[1])
-    _launch(index, what, lib().lora_rotary_apply, rotary.ref, positions.data_ptr(), T, n, ctypes.addressof(slices), code,
-            1 if inverse else 0)
+        slices += _pack_slice(pa, pb, sa[0], sa[1], sb[0], sb[1], shape[1])
+    _launch(index, what, lib().lora_rotary_apply, rotary.ref, positions.data_ptr(), T, n, slices, code, 1 if inverse else 0)
 
 
 def lora_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = LORA_ROTARY_PLAIN, factor: float = 1.0,
