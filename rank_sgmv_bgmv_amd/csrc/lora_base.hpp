@@ -22,7 +22,6 @@ struct ProductArgs {
   void *y;
   int64_t ldq, ldw, ldy;
   int T, d_in, d_out;
-  int y_vec;  // rows of y allow 16-byte stores
 };
 hipError_t launch_product(const ProductArgs &a, int dtype, hipStream_t stream);
 

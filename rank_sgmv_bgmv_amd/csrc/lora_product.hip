@@ -44,6 +44,27 @@ __device__ __forceinline__ i32x4 load16(const int8_t *p) {
   typedef int i32x4u __attribute__((ext_vector_type(4), aligned(1)));
   return *(const LORA_GLOBAL i32x4u *)p;
 }
+// The first n elements of a vector to y, at any alignment of theirs.
+template <typename E>
+__device__ __forceinline__ void store_vec(E *y, const uint4 &v, int n) {
+  typedef uint32_t U2 __attribute__((ext_vector_type(4), aligned(2)));
+  typedef uint32_t U4 __attribute__((ext_vector_type(4), aligned(4)));
+  typedef typename std::conditional<sizeof(E) == 2, U2, U4>::type U;
+  constexpr int kN = 16 / int(sizeof(E));
+  if (n >= kN) {
+    const U u = {v.x, v.y, v.z, v.w};
+    *(LORA_GLOBAL U *)y = u;
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      if (i < n) {
+        if constexpr (sizeof(E) == 2) gstore(y + i, uint16_t(w[i / 2] >> (i % 2 * 16)));
+        else gstore(y + i, __uint_as_float(w[i]));
+      }
+  }
+}
+
 // The 16 bytes at k of a row of d_in (16 or more) bytes, zeros past its end:
 // read from further ahead where they would pass it, and moved down.
 __device__ __forceinline__ i32x4 load16_end(const int8_t *row, int k, int d_in) {
@@ -419,16 +440,9 @@ struct TileShape {
   static constexpr int kO = MT * 16 * WM, kT = NT * 16 * WN;  // channels and tokens of a tile
   static constexpr int kCopyO = kO / 8 / kWaves, kCopyT = kT / 8 / kWaves;  // copies of a wave a stage
   static constexpr int kBytes = (kO + kT) * kStage;  // one stage
-  // results on their way out: up to 256 bytes of channels of each of a wave's tokens
-  static constexpr int kOutM = MT * 16 * int(sizeof(E)) <= 256 ? MT : MT / 2;
-  static constexpr int kOutRow = kOutM * 16 * int(sizeof(E)), kOutPitch = kOutRow + 16;
-  static constexpr int kOut = kWaves * NT * 16 * kOutPitch;
-  static constexpr int kScales = ST * kBytes > kOut ? ST * kBytes : kOut;  // then the scales and biases
+  static constexpr int kScales = ST * kBytes;  // then the scales and biases
   static constexpr int kLds = kScales + (2 * kO + kT) * 4;
-  // 16-byte vectors that a lane stores, and how many of them at a time
-  static constexpr int kStores = NT * 16 * (kOutRow / 16) / 64;
-  static constexpr int kBatch = kStores % 8 == 0 ? 8 : kStores % 6 == 0 ? 6 : kStores % 4 == 0 ? 4 : kStores % 3 == 0 ? 3 : 2;
-  static_assert(MT % kOutM == 0 && kOutRow <= 256 && kStores % kBatch == 0 && kLds <= kMaxLdsBytes, "");
+  static_assert(MT % 2 == 0 && kLds <= kMaxLdsBytes, "");
   static_assert(ST >= 2 && (ST & (ST - 1)) == 0, "stages are found by their number's low bits");
   static_assert(kO % (8 * kWaves) == 0 && kT % (8 * kWaves) == 0, "every wave copies the same");
 };
@@ -593,69 +607,50 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   stage(i, std::false_type{}, std::true_type{});
   settled(acc);
 
-  // Results through LDS, so that a token's channels leave in whole lines.  Each
-  // wave has its own place there, which it writes and reads in order: no
-  // barrier after the first, and stores stay in flight.
-  wait_copies<0>();
-  wait_lds();
-  meet();
-  int8_t *mine = lds + wave * NT * 16 * S::kOutPitch;
-  constexpr int kVec = 16 / int(sizeof(E)), kPer = S::kOutRow / 16;  // 16-byte vectors of a token's row
-  const bool whole = a.y_vec && n_o == S::kO && n_t == S::kT;
+  // Results leave from registers.  A lane has four channels of a token in each
+  // block, its neighbours 16 lanes on the next four: in bf16 two blocks change
+  // places between such neighbours, so that each has eight of one block, and
+  // every store is 16 bytes a lane and 64 a token.
+  constexpr int kVec = 16 / int(sizeof(E));
+  const bool whole = n_o == S::kO && n_t == S::kT;
   float sx[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) sx[j] = s_t[wn * NT * 16 + j * 16 + lane % 16];
+  const int tt = wn * NT * 16 + lane % 16;
 #pragma unroll
-  for (int m0 = 0; m0 < MT; m0 += S::kOutM) {
-    float4 sw[S::kOutM], b[S::kOutM];
+  for (int m = 0; m < MT; m += kVec / 4) {
+    float4 sw[kVec / 4], b[kVec / 4];
 #pragma unroll
-    for (int k = 0; k < S::kOutM; ++k) {
-      const int o = (wm * MT + m0 + k) * 16 + lane / 16 * 4;
+    for (int k = 0; k < kVec / 4; ++k) {
+      const int o = (wm * MT + m + k) * 16 + lane / 16 * 4;
       sw[k] = *reinterpret_cast<const float4 *>(s_o + o);
       b[k] = *reinterpret_cast<const float4 *>(b_o + o);
     }
+    const int oo = (wm * MT + m) * 16 + (kVec == 8 ? lane / 16 % 2 * 16 + lane / 32 * 8 : lane / 16 * 4);
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
+      uint4 out;
+      float v[kVec];
 #pragma unroll
-      for (int k = 0; k < S::kOutM; ++k) {
-        const i32x4 &c = acc[m0 + k][j];
-        const float v0 = float(c[0]) * sx[j] * sw[k].x + b[k].x, v1 = float(c[1]) * sx[j] * sw[k].y + b[k].y;
-        const float v2 = float(c[2]) * sx[j] * sw[k].z + b[k].z, v3 = float(c[3]) * sx[j] * sw[k].w + b[k].w;
-        int8_t *p = mine + (j * 16 + lane % 16) * S::kOutPitch + (k * 16 + lane / 16 * 4) * int(sizeof(E));
-        if constexpr (sizeof(E) == 2)
-          *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf2(v0, v1), pack_bf2(v2, v3));
-        else
-          *reinterpret_cast<float4 *>(p) = make_float4(v0, v1, v2, v3);
+      for (int k = 0; k < kVec / 4; ++k) {
+        const i32x4 &c = acc[m + k][j];
+        v[k * 4] = float(c[0]) * sx[j] * sw[k].x + b[k].x;
+        v[k * 4 + 1] = float(c[1]) * sx[j] * sw[k].y + b[k].y;
+        v[k * 4 + 2] = float(c[2]) * sx[j] * sw[k].z + b[k].z;
+        v[k * 4 + 3] = float(c[3]) * sx[j] * sw[k].w + b[k].w;
       }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-    __builtin_amdgcn_wave_barrier();
-    const int tt = wn * NT * 16, oo = (wm * MT + m0) * 16;
-    E *y = static_cast<E *>(a.y) + (t0 + tt) * a.ldy + o0 + oo;
-    if (whole) {
-      constexpr int kBatch = S::kBatch;
-#pragma unroll 1
-      for (int v = lane; v < NT * 16 * kPer; v += 64 * kBatch) {
-        uint4 r[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          r[k] = *reinterpret_cast<const uint4 *>(mine + (v + k * 64) / kPer * S::kOutPitch + (v + k * 64) % kPer * 16);
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) gstore(y + (v + k * 64) / kPer * a.ldy + (v + k * 64) % kPer * kVec, r[k]);
+      if constexpr (kVec == 8) {
+        const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf2(v[0], v[1]), pack_bf2(v[4], v[5]), false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf2(v[2], v[3]), pack_bf2(v[6], v[7]), false, false);
+        out = make_uint4(lo[0], hi[0], lo[1], hi[1]);
+      } else {
+        out = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
       }
-    } else {
-      for (int v = lane; v < NT * 16 * kPer; v += 64) {
-        const int r = v / kPer, c = v % kPer * kVec;
-        if (tt + r >= n_t || oo + c >= n_o) continue;
-        const int8_t *p = mine + r * S::kOutPitch + c * int(sizeof(E));
-        if (oo + c + kVec <= n_o && a.y_vec) {
-          gstore(y + r * a.ldy + c, *reinterpret_cast<const uint4 *>(p));
-        } else {
-          for (int e = 0; e < kVec; ++e)
-            if (oo + c + e < n_o) gstore(y + r * a.ldy + c + e, reinterpret_cast<const E *>(p)[e]);
-        }
+      if (whole || (tt + j * 16 < n_t && oo < n_o)) {
+        E *y = static_cast<E *>(a.y) + (t0 + tt + j * 16) * a.ldy + o0 + oo;
+        store_vec(y, out, whole ? kVec : n_o - oo);
       }
     }
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -717,7 +712,6 @@ double cost_of_few(const ProductArgs &a) {
 template <typename E>
 hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
   ProductArgs a = args;
-  a.y_vec = aligned16(a.y) && a.ldy * int64_t(sizeof(E)) % 16 == 0;
   const bool lines = aligned16(a.q) && aligned16(a.W) && a.ldq % 16 == 0 && a.ldw % 16 == 0 && a.d_in % 16 == 0;
   const bool near = a.ldq <= (1 << 22) && a.ldw <= (1 << 22);  // a tile's rows within 32-bit offsets
   double us = 0;
