@@ -416,7 +416,7 @@ hipError_t launch_few_lines(const ProductArgs &a, hipStream_t stream) {
 // It sees no matrix instruction here, so the waits that it would insert stand
 // at the places that need them (settle, settled).
 __device__ __forceinline__ void multiply(i32x4 &c, const i32x4 &a, const i32x4 &b) {
-  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
 }
 // Between vector instructions that write operands and the products that read them (2 wait states).
 __device__ __forceinline__ void settle() {
@@ -431,7 +431,7 @@ __device__ __forceinline__ void settled(i32x4 (&c)[M][N]) {
 #pragma unroll
   for (int m = 0; m < M; ++m)
 #pragma unroll
-    for (int j = 0; j < N; ++j) asm volatile("" : "+a"(c[m][j]));
+    for (int j = 0; j < N; ++j) asm volatile("" : "+v"(c[m][j]));
 }
 
 template <typename E, int MT, int NT, int WM, int WN, int ST>
@@ -681,6 +681,7 @@ struct TileCost {
 constexpr TileCost kTileCosts[] = {
     {256, 256, 1, 1.30f, 1.30f, 7.0f}, {192, 256, 1, 1.05f, 1.05f, 6.0f}, {128, 128, 2, 0.60f, 0.85f, 3.0f},
     {128, 128, 1, 0.50f, 0.50f, 3.0f}, {128, 64, 1, 0.33f, 0.33f, 2.5f},  {64, 64, 2, 0.20f, 0.41f, 3.0f},
+    {128, 160, 2, 0.70f, 1.07f, 3.5f},
 };
 
 // The shape of the least cost, among those whose bit is set in `among`.
@@ -727,6 +728,7 @@ hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
       case 2: return launch_tiles<E, 4, 4, 2, 2, 2>(a, stream);
       case 3: return launch_tiles<E, 4, 4, 2, 2, 4>(a, stream);
       case 4: return launch_tiles<E, 4, 2, 2, 2, 4>(a, stream);
+      case 6: return launch_tiles<E, 4, 5, 2, 2, 2>(a, stream);
       default: return launch_tiles<E, 2, 2, 2, 2, 4>(a, stream);
     }
   }
