@@ -181,207 +181,164 @@ __device__ __forceinline__ void meet() { asm volatile("s_barrier" ::: "memory");
 
 // --------------------------------------------------------------- few rows --
 //
-// Up to NT * 16 tokens: bound by reading the weights once.  A workgroup takes
-// MT * 16 channels and all tokens, its eight waves an eighth of the sum's axis
-// each, so that a weight of 4096 channels fills the chip and a CU has 16 waves
-// of loads on their way.  Operands go straight to registers, four 64-value
-// steps at a time while the four before are multiplied; any alignment and any
-// length (only the last steps look where the rows end).  The waves' sums meet
-// in LDS.
+// Up to 16 tokens and rows of any alignment: bound by reading the weights once.
+// A workgroup takes 16 channels and all tokens, its eight waves an eighth of the
+// sum's axis each, so that a weight of 4096 channels fills the chip and a CU has
+// 16 waves of loads on their way.  Operands go straight to registers, four
+// 64-value steps at a time while the four before are multiplied; only the last
+// steps look where the rows end.  The waves' sums meet in LDS.  One row through
+// 4096 x 4096 takes 5.4 us when rows are a multiple of 16 bytes, 11.1 when they
+// are of 4095.
 constexpr int kFewWaves = 8, kFewSteps = 4;
-template <typename E, int MT, int NT>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void product_few_kernel(ProductArgs a) {
-  __shared__ i32x4 part[kFewWaves][MT * NT][64];
-  const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64);
-  const int steps = (a.d_in + 63) / 64, each = (steps + kFewWaves - 1) / kFewWaves;
-  const int begin = wave * each, end = min(begin + each, steps), whole = min(end, a.d_in / 64);
-  {
-    const int o0 = blockIdx.x * MT * 16;
-    // rows past the end: the last row again
-    const int8_t *pw[MT], *px[NT];
+
+// The sums of 16 channels and 16 tokens, added over the waves, to y.
+template <typename E>
+__device__ __forceinline__ void store_few(const ProductArgs &a, const i32x4 *part, int stride, int o0, int t0) {
+  const int lane = threadIdx.x % 64, t = t0 + lane % 16, o = o0 + lane / 16 * 4;
+  i32x4 sum = part[lane];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) pw[m] = a.W + int64_t(min(o0 + m * 16 + lane % 16, a.d_out - 1)) * a.ldw + lane / 16 * 16;
+  for (int w = 1; w < kFewWaves; ++w) sum += part[w * stride + lane];
+  if (t >= a.T || o >= a.d_out) return;
+  const float sx = gload<float>(a.q_scale + t);
+  float v[4];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) px[j] = a.q + int64_t(min(j * 16 + lane % 16, a.T - 1)) * a.ldq + lane / 16 * 16;
-    i32x4 acc[MT][NT] = {};
-    i32x4 w[2][kFewSteps][MT], x[2][kFewSteps][NT];
-    auto load = [&](int step, int set) {
-#pragma unroll
-      for (int u = 0; u < kFewSteps; ++u) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) w[set][u][m] = load16(pw[m] + (step + u) * 64);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) x[set][u][j] = load16(px[j] + (step + u) * 64);
-      }
-    };
-    auto multiply_set = [&](int set) {
-#pragma unroll
-      for (int u = 0; u < kFewSteps; ++u)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            acc[m][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[set][u][m], x[set][u][j], acc[m][j], 0, 0, 0);
-    };
-    int k = begin;
-    if (k + kFewSteps <= whole) {
-      load(k, 0);
-      for (; k + 3 * kFewSteps <= whole; k += 2 * kFewSteps) {
-        load(k + kFewSteps, 1);
-        multiply_set(0);
-        load(k + 2 * kFewSteps, 0);
-        multiply_set(1);
-      }
-      if (k + 2 * kFewSteps <= whole) {
-        load(k + kFewSteps, 1);
-        multiply_set(0);
-        multiply_set(1);
-        k += 2 * kFewSteps;
-      } else {
-        multiply_set(0);
-        k += kFewSteps;
-      }
-    }
-    for (; k < end; ++k) {
-      const int piece = lane / 16 * 16;  // already in the pointers
-      i32x4 wt[MT];
-#pragma unroll
-      for (int m = 0; m < MT; ++m) wt[m] = load16_end(pw[m] - piece, k * 64 + piece, a.d_in);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const i32x4 xt = load16_end(px[j] - piece, k * 64 + piece, a.d_in);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) acc[m][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wt[m], xt, acc[m][j], 0, 0, 0);
-      }
-    }
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) part[wave][m * NT + j][lane] = acc[m][j];
-    lds_barrier();
-    for (int b = wave; b < MT * NT; b += kFewWaves) {
-      const int m = b / NT, j = b % NT, t = j * 16 + lane % 16, o = o0 + m * 16 + lane / 16 * 4;
-      i32x4 sum = part[0][b][lane];
-#pragma unroll
-      for (int v = 1; v < kFewWaves; ++v) sum += part[v][b][lane];
-      if (t < a.T && o < a.d_out) {
-        const float sx = gload<float>(a.q_scale + t);
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = min(o + e, a.d_out - 1);
-          v[e] = float(sum[e]) * sx * gload<float>(a.w_scale + c) + bias_of(a, c);
-        }
-        store_y(a, static_cast<E *>(a.y) + t * a.ldy, o, v);
-      }
-    }
-    lds_barrier();
+  for (int e = 0; e < 4; ++e) {
+    const int c = min(o + e, a.d_out - 1);
+    v[e] = float(sum[e]) * sx * gload<float>(a.w_scale + c) + bias_of(a, c);
   }
+  store_y(a, static_cast<E *>(a.y) + t * a.ldy, o, v);
 }
 
-template <typename E, int MT, int NT>
+template <typename E>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void product_few_kernel(ProductArgs a) {
+  __shared__ i32x4 part[kFewWaves * 64];
+  const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
+  const int steps = (a.d_in + 63) / 64, each = (steps + kFewWaves - 1) / kFewWaves;
+  const int begin = wave * each, end = min(begin + each, steps), whole = min(end, a.d_in / 64);
+  const int o0 = blockIdx.x * 16, piece = lane / 16 * 16;
+  // rows past the end: the last row again
+  const int8_t *pw = a.W + int64_t(min(o0 + lane % 16, a.d_out - 1)) * a.ldw;
+  const int8_t *px = a.q + int64_t(min(lane % 16, a.T - 1)) * a.ldq;
+  i32x4 acc = {};
+  i32x4 w[2][kFewSteps], x[2][kFewSteps];
+  auto load = [&](int step, int set) {
+#pragma unroll
+    for (int u = 0; u < kFewSteps; ++u) {
+      w[set][u] = load16(pw + piece + (step + u) * 64);
+      x[set][u] = load16(px + piece + (step + u) * 64);
+    }
+  };
+  auto multiply_set = [&](int set) {
+#pragma unroll
+    for (int u = 0; u < kFewSteps; ++u) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[set][u], x[set][u], acc, 0, 0, 0);
+  };
+  int k = begin;
+  if (k + kFewSteps <= whole) {
+    load(k, 0);
+    for (; k + 3 * kFewSteps <= whole; k += 2 * kFewSteps) {
+      load(k + kFewSteps, 1);
+      multiply_set(0);
+      load(k + 2 * kFewSteps, 0);
+      multiply_set(1);
+    }
+    const bool two = k + 2 * kFewSteps <= whole;
+    if (two) load(k + kFewSteps, 1);
+    multiply_set(0);
+    if (two) multiply_set(1);
+    k += two ? 2 * kFewSteps : kFewSteps;
+  }
+  for (; k < end; ++k)
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(load16_end(pw, k * 64 + piece, a.d_in), load16_end(px, k * 64 + piece, a.d_in),
+                                                acc, 0, 0, 0);
+  part[wave * 64 + lane] = acc;
+  lds_barrier();
+  if (wave == 0) store_few<E>(a, part, 64, o0, 0);
+}
+
+template <typename E>
 hipError_t launch_few(const ProductArgs &a, hipStream_t stream) {
-  const int groups = (a.d_out - 1) / (MT * 16) + 1;
-  product_few_kernel<E, MT, NT><<<dim3(uint32_t(groups)), 64 * kFewWaves, 0, stream>>>(a);
+  product_few_kernel<E><<<dim3(uint32_t((a.d_out - 1) / 16 + 1)), 64 * kFewWaves, 0, stream>>>(a);
   return hipGetLastError();
 }
 
-// The same for rows of whole 16-byte pieces and more tokens, whose operands
-// would come 16 bytes a row and clock that way (a lane's neighbours hold other
-// rows): each wave copies its stages to its own part of LDS in whole lines,
-// one stage ahead, and needs no barrier before the sums meet.
+// Up to NT * 16 tokens and rows of whole 16-byte pieces.  Read as above, 64
+// lanes would take 16 bytes of each of 16 rows, neighbours never side by side,
+// at a quarter of the cache's rate: that is fine for the weights, read once, but
+// with 64 rows q is four times their bytes (64 rows through 4096 x 4096: 11.9
+// us).  Here each wave copies its stages to its own part of LDS in whole
+// lines, one stage ahead, and needs no barrier before the sums meet: 7.9 us; 1
+// row through 4096 x 1024 3.9 us instead of 4.8.
 template <int NT>
 struct FewShape {
   static constexpr int kRows = 16 + NT * 16, kCopies = kRows / 8, kBytes = kRows * kStage;  // of a wave's stage
   static constexpr int kLds = kFewWaves * 2 * kBytes;  // the sums take the same place afterwards
-  static_assert(kLds <= kMaxLdsBytes && kFewWaves * NT * 1024 <= kLds, "");
+  static_assert(kLds <= kMaxLdsBytes && kFewWaves * NT * 1024 <= kLds && NT <= kFewWaves, "");
 };
 template <typename E, int NT>
 __global__ __launch_bounds__(64 * kFewWaves, 2) void product_few_lines_kernel(ProductArgs a) {
   typedef FewShape<NT> S;
   extern __shared__ __align__(16) int8_t lds[];
-  const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64);
+  const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64);
   const int stages = (a.d_in + kStage - 1) / kStage, each = (stages + kFewWaves - 1) / kFewWaves;
   const int begin = wave * each, end = min(begin + each, stages);
-  const int piece = (lane % 8) ^ (lane / 8);
+  const int piece = (lane % 8) ^ (lane / 8), o0 = blockIdx.x * 16;
   int8_t *mine = lds + wave * 2 * S::kBytes;
   const uint32_t lds0 = uint32_t(uintptr_t((__attribute__((address_space(3))) int8_t *)mine));
-  uint32_t off_x[2 * NT];
+  const int8_t *W = a.W + int64_t(o0) * a.ldw;
+  uint32_t off[S::kCopies];  // two of W, then q's; rows past the end: the last row again
 #pragma unroll
-  for (int i = 0; i < 2 * NT; ++i) off_x[i] = uint32_t(min(i * 8 + lane / 8, a.T - 1)) * uint32_t(a.ldq) + piece * 16;
-  {
-    const int o0 = blockIdx.x * 16;
-    const int8_t *W = a.W + int64_t(o0) * a.ldw;
-    uint32_t off_w[2];
+  for (int i = 0; i < S::kCopies; ++i)
+    off[i] = (i < 2 ? uint32_t(min(i * 8 + lane / 8, a.d_out - 1 - o0)) * uint32_t(a.ldw)
+                    : uint32_t(min((i - 2) * 8 + lane / 8, a.T - 1)) * uint32_t(a.ldq)) +
+             piece * 16;
+  auto copy = [&](int stage) {
+    // pieces past the end of the rows are not read: the stage's first piece stands in (and is masked below)
+    const uint32_t back = stage * kStage + piece * 16 < a.d_in ? 0u : piece * 16u;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) off_w[i] = uint32_t(min(i * 8 + lane / 8, a.d_out - 1 - o0)) * uint32_t(a.ldw) + piece * 16;
-    auto copy = [&](int stage) {
-      // pieces past the end of the rows are not read: the stage's first piece stands in (and is masked below)
-      const uint32_t back = stage * kStage + piece * 16 < a.d_in ? 0u : piece * 16u;
-      const uint32_t at = lds0 + (stage & 1) * S::kBytes;
+    for (int i = 0; i < S::kCopies; ++i)
+      copy_to_lds((i < 2 ? W : a.q) + stage * kStage, off[i] - back, lds0 + (stage & 1) * S::kBytes + i * 1024);
+  };
+  i32x4 acc[NT] = {};
+  if (begin < end) copy(begin);
+  if (begin + 1 < end) copy(begin + 1);
+  for (int i = begin; i < end; ++i) {
+    if (i + 1 < end)
+      wait_copies<S::kCopies>();
+    else
+      wait_copies<0>();
+    __builtin_amdgcn_sched_barrier(0);
+    const int8_t *p = mine + (i & 1) * S::kBytes + lane % 16 * kStage;
+    i32x4 w[2], x[2][NT];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) copy_to_lds(W + stage * kStage, off_w[i] - back, at + i * 1024);
+    for (int s = 0; s < 2; ++s) {
+      const int at = ((s * 4 + lane / 16) ^ (lane & 7)) * 16;
+      w[s] = *reinterpret_cast<const i32x4 *>(p + at);
 #pragma unroll
-      for (int i = 0; i < 2 * NT; ++i) copy_to_lds(a.q + stage * kStage, off_x[i] - back, at + (2 + i) * 1024);
-    };
-    i32x4 acc[NT] = {};
-    if (begin < end) copy(begin);
-    if (begin + 1 < end) copy(begin + 1);
-    for (int i = begin; i < end; ++i) {
-      if (i + 1 < end)
-        wait_copies<S::kCopies>();
-      else
-        wait_copies<0>();
-      __builtin_amdgcn_sched_barrier(0);
-      const int8_t *p = mine + (i & 1) * S::kBytes + lane % 16 * kStage;
-      i32x4 w[2], x[2][NT];
+      for (int j = 0; j < NT; ++j) x[s][j] = *reinterpret_cast<const i32x4 *>(p + (16 + j * 16) * kStage + at);
+    }
+    wait_lds();  // the stage is read: its place may be written
+    __builtin_amdgcn_sched_barrier(0);
+    if (i + 2 < end) copy(i + 2);
+    if (i == stages - 1) {
+      // past the end of the sum's axis the weights count as zero
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        const int at = ((s * 4 + lane / 16) ^ (lane & 7)) * 16;
-        w[s] = *reinterpret_cast<const i32x4 *>(p + at);
+        const bool in = i * kStage + s * 64 + lane / 16 * 16 < a.d_in;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) x[s][j] = *reinterpret_cast<const i32x4 *>(p + (16 + j * 16) * kStage + at);
-      }
-      wait_lds();
-      __builtin_amdgcn_sched_barrier(0);
-      if (i + 2 < end) copy(i + 2);
-      if (i == stages - 1) {
-        // past the end of the sum's axis the weights count as zero
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const bool in = i * kStage + s * 64 + lane / 16 * 16 < a.d_in;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[s][e] = in ? w[s][e] : 0;
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s], x[s][j], acc[j], 0, 0, 0);
-    }
-    i32x4 *part = reinterpret_cast<i32x4 *>(lds);
-    lds_barrier();  // every wave is done with its stages
-#pragma unroll
-    for (int j = 0; j < NT; ++j) part[(wave * NT + j) * 64 + lane] = acc[j];
-    lds_barrier();
-    if (wave < NT) {
-      const int t = wave * 16 + lane % 16, o = o0 + lane / 16 * 4;
-      i32x4 sum = part[wave * 64 + lane];
-#pragma unroll
-      for (int v = 1; v < kFewWaves; ++v) sum += part[(v * NT + wave) * 64 + lane];
-      if (t < a.T && o < a.d_out) {
-        const float sx = gload<float>(a.q_scale + t);
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int c = min(o + e, a.d_out - 1);
-          v[e] = float(sum[e]) * sx * gload<float>(a.w_scale + c) + bias_of(a, c);
-        }
-        store_y(a, static_cast<E *>(a.y) + t * a.ldy, o, v);
+        for (int e = 0; e < 4; ++e) w[s][e] = in ? w[s][e] : 0;
       }
     }
-    lds_barrier();
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s], x[s][j], acc[j], 0, 0, 0);
   }
+  i32x4 *part = reinterpret_cast<i32x4 *>(lds);
+  lds_barrier();  // every wave is done with its stages
+#pragma unroll
+  for (int j = 0; j < NT; ++j) part[(wave * NT + j) * 64 + lane] = acc[j];
+  lds_barrier();
+  if (wave < NT) store_few<E>(a, part + wave * 64, NT * 64, o0, wave * 16);
 }
 
 template <typename E, int NT>
@@ -390,27 +347,29 @@ hipError_t launch_few_lines(const ProductArgs &a, hipStream_t stream) {
   const auto kernel = product_few_lines_kernel<E, NT>;
   static const bool ready = raise_lds_limit(reinterpret_cast<const void *>(kernel), S::kLds);
   (void)ready;
-  const int groups = (a.d_out - 1) / 16 + 1;
-  kernel<<<dim3(uint32_t(groups)), 64 * kFewWaves, S::kLds, stream>>>(a);
+  kernel<<<dim3(uint32_t((a.d_out - 1) / 16 + 1)), 64 * kFewWaves, S::kLds, stream>>>(a);
   return hipGetLastError();
 }
 
 // ------------------------------------------------------------ large tiles --
 //
-// MT * 32 channels x NT * 32 tokens by four waves (2 x 2, each MT x NT blocks
-// of v_mfma_i32_16x16x64_i8).  The sum's axis goes in stages of 128 values,
-// copied to LDS without passing registers, two stages in LDS: stage i + 2 is on
-// its way while stage i + 1 lies ready and i is multiplied.  Within a stage
-// the operands of one 64-value step are read from LDS while the step before
-// is multiplied, across stages too, so the matrix unit waits for nothing but
-// the one barrier of a stage.
+// WM x WN waves of MT x NT blocks of v_mfma_i32_16x16x64_i8: MT * WM * 16
+// channels x NT * WN * 16 tokens, with ST stages in LDS: stage i + ST is on its
+// way while stages i + 1 .. lie ready or arrive and i is multiplied.  Within a
+// stage the operands of one 64-value step are read from LDS while the step
+// before is multiplied, across stages too, so the matrix unit waits for nothing
+// but the one barrier of a stage.
 //
-// What bounds it is power: four waves on every CU that only multiply random
-// 8-bit numbers run at 1.79 GHz (3.68 POP/s) with 16 x 16 blocks and at 1.44
-// GHz (2.97 POP/s) with 32 x 32 ones, which move twice the sums.  So 16 x 16
-// blocks, and the largest tile that fits the registers, 8 x 8 blocks a wave,
-// which reads the fewest operands from LDS for each product.
-
+// What bounds large tiles is power: four waves on every CU that only multiply
+// random 8-bit numbers run at 1.79 GHz (3.68 POP/s) with 16 x 16 blocks and at
+// 1.44 GHz (2.97 POP/s) with 32 x 32 ones, which move twice the sums.  So 16 x 16
+// blocks, and the largest tile that fits the registers, which reads the fewest
+// operands from LDS for each product: 256 x 256 by eight waves (2 x 4, 128 x 64
+// each).  A stage of it is 2048 clocks of products; it takes 2444 when all
+// operands are in L2 (four waves of 128 x 128, which read a third less from LDS
+// but cannot fill each other's gaps: 2655) and about 2750 from memory, at 1.85
+// GHz.  8192^3: 413 us, 2.66 POP/s; 16384 rows through 4096 x 4096: 228 us, 2.4
+// POP/s, the rest being the tiles' first stages and stores (8 of 57 us a tile).
 // c += a b^T on a 16 x 16 block, c kept where it is: given the choice, the
 // compiler writes the sums elsewhere and moves 200 registers back each stage.
 // It sees no matrix instruction here, so the waits that it would insert stand
@@ -670,10 +629,14 @@ hipError_t launch_tiles(const ProductArgs &a, hipStream_t stream) {
 // The tile shapes and what a tile of n stages costs, in microseconds: when its
 // CU has no other tile, and when the CU is full (so many tiles at once).  Large
 // tiles move the fewest bytes for each product, small ones fill more CUs.
-// Measured at 32 and 112 stages of 4096-wide and 14336-wide weights: 512 rows
-// through 4096 x 4096 take 40 us with the first shape, 22, 17.5, 13 and 15.6
-// with the last four; 2304 rows through 4096 x 14336 take 113 with the first,
-// 130 with the second and 133, 158, 196, 209 with the others.
+// Measured, with the shapes in their order here:
+//                              256x256 192x256 128x128 128x128 128x64 64x64 128x160
+//   512 rows,  4096 -> 4096       40.3    34.1    22.7    18.0   13.8  18.0    24.6
+//   512 rows,  4096 -> 14336      55.3    50.1    41.8    46.8   62.4  58.7    43.0
+//   2304 rows, 4096 -> 4096       46.8    40.3    51.5    55.3   58.4  61.4    40.4
+//   2304 rows, 14336 -> 4096       165     145     178     173    188   209     129
+//   2304 rows, 4096 -> 14336       117     132     136     156    189   210     145
+//   16997 rows, 4096 -> 4096       260     265     283     331    411   436     271
 struct TileCost {
   int o, t, at_once;
   float alone, full, once;  // per stage, per stage with a full CU, per tile
@@ -703,7 +666,8 @@ int choose_tile(const ProductArgs &a, unsigned among, double &least) {
 // What the kernel for few rows costs, likewise: a wave's stages, in as many
 // rounds as its workgroups fill the chip (two on a CU up to 16 rows).  64 rows
 // through 4096 x 4096 take 7.9 us with it and 9.3 with 64 x 64 tiles, through
-// 4096 x 14336, whose channels make it read the rows 896 times, 29.5 and 16.8.
+// 14336 x 4096 22.7 and 36.8, through 4096 x 14336, whose channels make it read
+// the rows 896 times, 29.5 and 17.5.
 double cost_of_few(const ProductArgs &a) {
   const int each = ((a.d_in + kStage - 1) / kStage + kFewWaves - 1) / kFewWaves, nt = (a.T + 15) / 16;
   const double stage = nt <= 1 ? 0.75 : nt <= 2 ? 0.9 : 1.3, at_once = nt <= 1 ? 2 : 1;
@@ -732,7 +696,7 @@ hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
       default: return launch_tiles<E, 2, 2, 2, 2, 4>(a, stream);
     }
   }
-  if (a.d_in >= 16 && a.T <= 16) return launch_few<E, 1, 1>(a, stream);
+  if (a.d_in >= 16 && a.T <= 16) return launch_few<E>(a, stream);
   if (a.d_in >= 16 && near) {
     if (choose_tile(a, 1u << 2 | 1u << 5, us) == 2) return launch_tiles<E, 4, 4, 2, 2, 2, false>(a, stream);
     return launch_tiles<E, 2, 2, 2, 2, 2, false>(a, stream);

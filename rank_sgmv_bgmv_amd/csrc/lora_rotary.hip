@@ -166,7 +166,9 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(RotaryArgs a, in
       if constexpr (MODE == ROT_ANY) {
         // the barriers are all lanes'
         if (t > 0 || g != first) lds_barrier();
-        if (live) *reinterpret_cast<uint4 *>(rows + (slot * cols + col) * 16) = make_uint4(x0[t].w[0], x0[t].w[1], x0[t].w[2], x0[t].w[3]);
+        if (live && pos[t] >= 0)
+          *reinterpret_cast<uint4 *>(rows + (slot * cols + col) * 16) = 
+              make_uint4(x0[t].w[0], x0[t].w[1], x0[t].w[2], x0[t].w[3]);
         lds_barrier();
       }
       if (!live || pos[t] < 0) continue;
