@@ -409,27 +409,27 @@ def lora_pool_load(pool: Pool, slot: int, A_host, B_host, stream=None):
 # _line), and where one is not go through the checks that name what is wrong.
 def _launch(index: int, what: str, f, *args):
     """f(*args, stream) on the current stream of device `index`, as the current device: launches go to that one."""
-    torch = _torch()
-    if index == torch.cuda.current_device():
-        st = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    C = _torch()._C
+    if index == C._cuda_getDevice():
+        st = f(*args, C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(index):
-            st = f(*args, torch._C._cuda_getCurrentRawStream(index))
+        with _torch().cuda.device(index):
+            st = f(*args, C._cuda_getCurrentRawStream(index))
     if st != 0:
         raise LoraError(st, what)
 
 
 def _row(t, dtype, index: int) -> int:
     """The row stride of a 2-D tensor of this type and device with unit column stride; 0 if t is not plainly one."""
-    if t.dtype is not dtype or t.get_device() != index or t.dim() != 2:
+    if t.dtype is not dtype or t.get_device() != index:
         return 0
     s = t.stride()
-    return s[0] if s[1] == 1 else 0
+    return s[0] if len(s) == 2 and s[1] == 1 else 0
 
 
 def _line(t, dtype, index: int, n: int) -> bool:
     """Whether t is plainly a contiguous 1-D tensor of n elements or more, of this type and device."""
-    return t.dtype is dtype and t.get_device() == index and t.dim() == 1 and t.shape[0] >= n and t.is_contiguous()
+    return t.dtype is dtype and t.get_device() == index and t.stride() == (1,) and t.shape[0] >= n
 
 
 def _rows_2d(what: str, name: str, t, dtypes, dev, cols: int, rows: Optional[int] = None) -> int:
