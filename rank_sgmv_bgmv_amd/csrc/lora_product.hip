@@ -679,9 +679,9 @@ struct TileCost {
   float alone, full, once;  // per stage, per stage with a full CU, per tile
 };
 constexpr TileCost kTileCosts[] = {
-    {256, 256, 1, 1.30f, 1.30f, 7.0f}, {192, 256, 1, 1.05f, 1.05f, 6.0f}, {128, 128, 2, 0.60f, 0.85f, 3.0f},
-    {128, 128, 1, 0.50f, 0.50f, 3.0f}, {128, 64, 1, 0.33f, 0.33f, 2.5f},  {64, 64, 2, 0.20f, 0.41f, 3.0f},
-    {128, 160, 2, 0.70f, 1.07f, 3.5f},
+    {256, 256, 1, 1.10f, 1.45f, 8.0f}, {192, 256, 1, 0.88f, 1.20f, 6.0f}, {128, 128, 2, 0.60f, 0.82f, 4.0f},
+    {128, 128, 1, 0.48f, 0.48f, 3.0f}, {128, 64, 1, 0.33f, 0.33f, 2.5f},  {64, 64, 2, 0.19f, 0.45f, 3.0f},
+    {128, 160, 2, 0.75f, 1.13f, 4.0f},
 };
 
 // The shape of the least cost, among those whose bit is set in `among`.
@@ -694,7 +694,9 @@ int choose_tile(const ProductArgs &a, unsigned among, double &least) {
     const int64_t tiles = int64_t((a.d_out - 1) / c.o + 1) * ((a.T - 1) / c.t + 1);
     const int64_t rounds = tiles / (cus * c.at_once), rest = tiles % (cus * c.at_once);
     double us = rounds * double(n * c.full + c.once);
-    if (rest) us += n * (rest <= cus ? c.alone : c.full) + c.once;
+    // one to a CU, tiles slow down with the number of CUs at work (power)
+    const double busy = c.at_once == 1 ? double(rest) / cus : rest > cus;
+    if (rest) us += n * (c.alone + (c.full - c.alone) * busy) + c.once;
     if (best < 0 || us < least) best = k, least = us;
   }
   return best;
