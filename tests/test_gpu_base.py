@@ -215,6 +215,27 @@ def test_product_largest_sums(T, d_in):
     check_product(T, d_in, 33, torch.float32, bias=False, q=q, W=W)
 
 
+TILES = [(16797, 656, 579), (16806, 656, 513), (13627, 656, 266), (16511, 656, 65), (9355, 656, 65), (117, 704, 63),
+         (16877, 672, 130), (17045, 656, 1411), (301, 655, 130), (5001, 655, 1283)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("T, d_in, d_out", TILES)
+def test_product_large(T, d_in, d_out, dtype):
+    """Sizes that take each of the tile shapes, with ends in both directions and in the sum's axis, and one that is
+    split into whole rounds and a rest; against the float64 product on the GPU (sums below 2^53: exact)."""
+    g = gen(T)
+    q, W = i8((T, d_in), g).to(DEV), i8((d_out, d_in), g, -128, 127).to(DEV)
+    qs, ws, b = (torch.rand(n, generator=g).to(DEV) * 0.02 for n in (T, d_out, d_out))
+    yb = torch.full((T + 1, d_out + 8), 7.0, dtype=dtype, device=DEV)
+    L.lora_base_product(L.BaseWeight(W, ws, b), q, qs, yb[:T, :d_out])
+    p = (q.double() @ W.double().T) * qs.double()[:, None] * ws.double()
+    ref = p + b.double()
+    bad = (yb[:T, :d_out].double() - ref).abs() > half(dtype) * ref.abs() + 4 * V * (p.abs() + b.double().abs())
+    assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[:4].tolist())
+    assert bool((yb[T] == 7).all()) and bool((yb[:, d_out:] == 7).all())
+
+
 def test_product_nan_scale_stays_in_its_row():
     g = gen(3)
     q, W = i8((20, 64), g).to(DEV), i8((48, 64), g).to(DEV)
