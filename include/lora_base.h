@@ -14,11 +14,13 @@
  * Memory, streams and errors as in lora.h: every pointer is a DEVICE pointer
  * unless its comment says host; all buffers are the caller's; the library
  * allocates nothing, keeps nothing between calls but the device's
- * compute-unit count, and every call is asynchronous on `stream` (which must
- * belong to the current device) and can be captured in a graph.  What the
- * host can see to be wrong returns a status and launches nothing.  Rows and
- * columns outside the sizes of a call are never written, nor read.
- * Results do not depend on the launch: the same inputs give the same bits.
+ * compute-unit count and the kernels' LDS limit, and every call is
+ * asynchronous on `stream` (which must belong to the current device) and can
+ * be captured in a graph.  What the host can see to be wrong returns a status
+ * and launches nothing.  Rows and columns outside the sizes of a call are
+ * never written, and no result depends on what they hold.  Results do not
+ * depend on the launch either: the same inputs give the same bits, and a row
+ * the same ones whatever rows it is in a batch with.
  */
 #ifndef RANK_SGMV_BGMV_LORA_BASE_H
 #define RANK_SGMV_BGMV_LORA_BASE_H

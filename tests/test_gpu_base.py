@@ -128,6 +128,18 @@ def test_quantize_extremes(dtype):
     check_quantize(x.to(dtype))
 
 
+@pytest.mark.parametrize("T, d, dtype", [(270001, 8, torch.bfloat16), (66001, 1032, torch.float32)])
+def test_quantize_more_rows_than_workgroups(T, d, dtype):
+    x = torch.randn(T, d, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).to(dtype)
+    q, s = torch.empty(T, d, dtype=torch.int8, device=DEV), torch.empty(T, device=DEV)
+    L.lora_quantize_rows(x, q, s)
+    a = x.abs().amax(1).double()
+    assert torch.equal(s, (a / 127).float())
+    for lo in range(0, T, 20000):
+        v = x[lo:lo + 20000].double()
+        assert torch.equal(q[lo:lo + 20000].double(), torch.round(127 * v / a[lo:lo + 20000, None])), lo
+
+
 def test_quantize_no_rows():
     x, q, s = torch.empty(0, 64, device=DEV), torch.empty(0, 64, dtype=torch.int8, device=DEV), torch.empty(0, device=DEV)
     L.lora_quantize_rows(x, q, s)
@@ -274,6 +286,36 @@ def test_product_many_rows():
     assert torch.equal(y, (q[:, :1].float() * d).expand(T, 2))
 
 
+def test_product_of_a_row_does_not_depend_on_the_others():
+    """A row's results have the same bits in a batch of any size: one kernel or another, the sum is exact and what
+    follows it is the same."""
+    g = gen(11)
+    q, W = i8((700, 1040), g).to(DEV), i8((333, 1040), g).to(DEV)
+    qs, ws, b = torch.rand(700, generator=g).to(DEV), torch.rand(333, generator=g).to(DEV), torch.randn(333, generator=g).to(DEV)
+    w = L.BaseWeight(W, ws, b)
+    whole = torch.empty(700, 333, device=DEV)
+    L.lora_base_product(w, q, qs, whole)
+    for lo, n in ((0, 1), (5, 16), (30, 31), (64, 64), (100, 100), (300, 400)):
+        y = torch.empty(n, 333, device=DEV)
+        L.lora_base_product(w, q[lo:lo + n], qs[lo:lo + n], y)
+        assert torch.equal(y, whole[lo:lo + n]), (lo, n)
+        odd = torch.zeros(n, 1041, dtype=torch.int8, device=DEV)[:, 1:]  # the same rows, at odd addresses
+        odd.copy_(q[lo:lo + n])
+        L.lora_base_product(w, odd, qs[lo:lo + n], y)
+        assert torch.equal(y, whole[lo:lo + n]), (lo, n)
+
+
+def test_product_many_channels():
+    """More channels than a launch takes: the last ones are right."""
+    n, d = (1 << 17) + 33, 16
+    W = (torch.arange(n, device=DEV).view(-1, 1) % 251 - 125).to(torch.int8).expand(n, d).contiguous()
+    q = torch.ones(3, d, dtype=torch.int8, device=DEV)
+    b = torch.arange(n, device=DEV, dtype=torch.float32)
+    y = torch.zeros(3, n, device=DEV)
+    L.lora_base_product(L.BaseWeight(W, torch.ones(n, device=DEV), b), q, torch.ones(3, device=DEV), y)
+    assert torch.equal(y, (W[:, 0].float() * d + b).expand(3, n))
+
+
 # --------------------------------------------------------------------- apply --
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("T, d_in, d_out", [(1, 64, 48), (1, 4096, 256), (4, 1001, 77), (16, 512, 512), (64, 4096, 320),
@@ -293,6 +335,37 @@ def test_apply(T, d_in, d_out, dtype):
     ref, mag = ref_product(q, s, W, ws, b)
     assert bool(((y[:T].cpu().double() - ref).abs() <= half(dtype) * ref.abs() + 4 * V * mag).all())
     assert bool((y[T] == 5).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("T", [1, 2, 40, 200])
+def test_apply_on_columns_of_wider_buffers(T, dtype):
+    """x and y as column ranges: their neighbours are not read (NaN) and not written."""
+    g = gen(T)
+    d_in, d_out = 200, 72
+    xb = torch.full((T, d_in + 30), float("nan"), dtype=dtype, device=DEV)
+    x = xb[:, 16:16 + d_in]
+    x.copy_(torch.randn(T, d_in, generator=g).to(dtype))
+    W, ws = i8((d_out, d_in), g), torch.rand(d_out, generator=g) * 0.01
+    w = L.BaseWeight(W.to(DEV), ws.to(DEV))
+    yb = torch.full((T, d_out + 9), 7.0, dtype=dtype, device=DEV)
+    L.lora_base_apply(w, x, yb[:, 5:5 + d_out], L.new_base_workspace(w, T))
+    q, s = ref_quantize(x.cpu())
+    ref, mag = ref_product(q, s, W, ws, None)
+    assert bool(((yb[:, 5:5 + d_out].cpu().double() - ref).abs() <= half(dtype) * ref.abs() + 4 * V * mag).all())
+    assert bool((yb[:, :5] == 7).all()) and bool((yb[:, 5 + d_out:] == 7).all())
+
+
+def test_nothing_to_do():
+    """No rows, no tokens: nothing is launched or written."""
+    w = L.BaseWeight(torch.ones(8, 16, dtype=torch.int8, device=DEV), torch.ones(8, device=DEV))
+    y = torch.full((3, 8), 7.0, device=DEV)
+    e = torch.empty(0, device=DEV)
+    L.lora_base_product(w, torch.empty(0, 16, dtype=torch.int8, device=DEV), e, y)
+    L.lora_base_apply(w, torch.empty(0, 16, device=DEV), y, L.new_base_workspace(w, 0))
+    r = L.Rotary(L.lora_rotary_frequencies(8).to(DEV), 8)
+    L.lora_rotary_apply(r, torch.empty(0, dtype=torch.int32, device=DEV), [torch.empty(0, 2, 8, device=DEV)])
+    assert bool((y == 7).all())
 
 
 def test_apply_nan_row_stays_in_its_row():
@@ -444,6 +517,36 @@ def test_rotary_rows_far_apart():
     L.lora_rotary_apply(L.Rotary(freq.to(DEV), D), pos.to(DEV), [v])
     y, mag, _ = ref_rotary(x, pos, freq, D, False, False, 1.0)
     assert bool(((v.cpu().double() - y).abs() <= V * y.abs() + 6 * V * mag).all())
+
+
+def test_rotary_more_tokens_than_a_launch_takes():
+    T = (1 << 24) + 5
+    x = torch.ones(T, 1, 2, device=DEV)
+    pos = (torch.arange(T, device=DEV) % 1000).int()
+    freq = torch.tensor([0.5], dtype=torch.float64, device=DEV)
+    L.lora_rotary_apply(L.Rotary(freq, 2), pos, [x])
+    for lo in (0, (1 << 24) - 1000):
+        w = pos[lo:].double()[:2000] * 0.5
+        ref = torch.stack([torch.cos(w) - torch.sin(w), torch.cos(w) + torch.sin(w)], -1)
+        assert bool(((x[lo:, 0][:2000].double() - ref).abs() <= V * ref.abs() + 12 * V).all())
+
+
+@pytest.mark.parametrize("interleaved, rot", [(False, 64), (False, 36), (True, 36)])
+def test_rotary_one_slice_in_place_one_not_one_broadcast(interleaved, rot):
+    """In one launch: a tensor in place, one into another tensor, and one head spread to several."""
+    g = gen(8)
+    T, D = 50, 64
+    freq = L.lora_rotary_frequencies(rot)
+    pos = torch.randint(0, 900, (T,), generator=g, dtype=torch.int32)
+    xs = [torch.randn(T, h, D, generator=g) for h in (3, 2, 1)]
+    dev = [x.to(DEV) for x in xs]
+    out = [dev[0], torch.empty(T, 2, D, device=DEV), torch.empty(T, 4, D, device=DEV)]
+    L.lora_rotary_apply(L.Rotary(freq.to(DEV), D, interleaved=interleaved), pos.to(DEV),
+                        [dev[0], dev[1], dev[2].expand(T, 4, D)], out)
+    for x, o in zip([xs[0], xs[1], xs[2].expand(T, 4, D)], out):
+        y, mag, _ = ref_rotary(x, pos, freq, rot, interleaved, False, 1.0)
+        assert bool(((o.cpu().double() - y).abs() <= V * y.abs() + 6 * V * mag).all())
+        assert torch.equal(o.cpu()[..., rot:], x[..., rot:])
 
 
 def test_rotary_refusals_of_the_binding():
