@@ -606,48 +606,51 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   // Results leave from registers.  A lane has four channels of a token in each
   // block, its neighbours 16 lanes on the next four: in bf16 two blocks change
   // places between such neighbours, so that each has eight of one block, and
-  // every store is 16 bytes a lane and 64 a token.
+  // every store is 16 bytes a lane and 64 a token.  A token's stores follow one
+  // another, so that its lines fill up in L2: 65536 rows through
+  // 1280 x 1280 134 us block by block, 130 token by token.
   constexpr int kVec = 16 / int(sizeof(E));
-  const bool whole = n_o == S::kO && n_t == S::kT;
-  float sx[NT];
+  float4 sw[MT], b[MT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) sx[j] = s_t[wn * NT * 16 + j * 16 + lane % 16];
-  const int tt = wn * NT * 16 + lane % 16;
-#pragma unroll
-  for (int m = 0; m < MT; m += kVec / 4) {
-    float4 sw[kVec / 4], b[kVec / 4];
-#pragma unroll
-    for (int k = 0; k < kVec / 4; ++k) {
-      const int o = (wm * MT + m + k) * 16 + lane / 16 * 4;
-      sw[k] = *reinterpret_cast<const float4 *>(s_o + o);
-      b[k] = *reinterpret_cast<const float4 *>(b_o + o);
-    }
-    const int oo = (wm * MT + m) * 16 + (kVec == 8 ? lane / 16 % 2 * 16 + lane / 32 * 8 : lane / 16 * 4);
+  for (int m = 0; m < MT; ++m) {
+    const int o = (wm * MT + m) * 16 + lane / 16 * 4;
+    sw[m] = *reinterpret_cast<const float4 *>(s_o + o);
+    b[m] = *reinterpret_cast<const float4 *>(b_o + o);
+  }
+  auto store = [&](auto whole) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      uint4 out;
-      float v[kVec];
+      const int tt = (wn * NT + j) * 16 + lane % 16;
+      const float sx = s_t[tt];
+      E *y = static_cast<E *>(a.y) + (t0 + tt) * a.ldy + o0;
 #pragma unroll
-      for (int k = 0; k < kVec / 4; ++k) {
-        const i32x4 &c = acc[m + k][j];
-        v[k * 4] = float(c[0]) * sx[j] * sw[k].x + b[k].x;
-        v[k * 4 + 1] = float(c[1]) * sx[j] * sw[k].y + b[k].y;
-        v[k * 4 + 2] = float(c[2]) * sx[j] * sw[k].z + b[k].z;
-        v[k * 4 + 3] = float(c[3]) * sx[j] * sw[k].w + b[k].w;
-      }
-      if constexpr (kVec == 8) {
-        const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf2(v[0], v[1]), pack_bf2(v[4], v[5]), false, false);
-        const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf2(v[2], v[3]), pack_bf2(v[6], v[7]), false, false);
-        out = make_uint4(lo[0], hi[0], lo[1], hi[1]);
-      } else {
-        out = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-      }
-      if (whole || (tt + j * 16 < n_t && oo < n_o)) {
-        E *y = static_cast<E *>(a.y) + (t0 + tt + j * 16) * a.ldy + o0 + oo;
-        store_vec(y, out, whole ? kVec : n_o - oo);
+      for (int m = 0; m < MT; m += kVec / 4) {
+        const int oo = (wm * MT + m) * 16 + (kVec == 8 ? lane / 16 % 2 * 16 + lane / 32 * 8 : lane / 16 * 4);
+        float v[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec / 4; ++k) {
+          const i32x4 &c = acc[m + k][j];
+          v[k * 4] = float(c[0]) * sx * sw[m + k].x + b[m + k].x;
+          v[k * 4 + 1] = float(c[1]) * sx * sw[m + k].y + b[m + k].y;
+          v[k * 4 + 2] = float(c[2]) * sx * sw[m + k].z + b[m + k].z;
+          v[k * 4 + 3] = float(c[3]) * sx * sw[m + k].w + b[m + k].w;
+        }
+        uint4 out;
+        if constexpr (kVec == 8) {
+          const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf2(v[0], v[1]), pack_bf2(v[4], v[5]), false, false);
+          const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf2(v[2], v[3]), pack_bf2(v[6], v[7]), false, false);
+          out = make_uint4(lo[0], hi[0], lo[1], hi[1]);
+        } else {
+          out = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+        }
+        if (whole || (tt < n_t && oo < n_o)) store_vec(y + oo, out, whole ? kVec : n_o - oo);
       }
     }
-  }
+  };
+  if (n_o == S::kO && n_t == S::kT)
+    store(std::true_type{});
+  else
+    store(std::false_type{});
 }
 
 template <typename E, int MT, int NT, int WM, int WN, int ST, bool LINES = true>
