@@ -22,6 +22,7 @@ struct ProductArgs {
   void *y;
   int64_t ldq, ldw, ldy;
   int T, d_in, d_out;
+  int y_by;  // results pass the caches by (set at the launch)
 };
 hipError_t launch_product(const ProductArgs &a, int dtype, hipStream_t stream);
 
@@ -31,6 +32,7 @@ struct RotaryArgs {
   int T, head_dim, rot_dim, interleaved;
   float mscale, sign;  // sign of the angle: 1, or -1 for the inverse
   int n_slices, n_heads;  // heads of all slices
+  int by;                 // results pass the caches by (set at the launch)
   lora_rotary_slice s[LORA_MAX_SLICES];
 };
 hipError_t launch_rotary(const RotaryArgs &a, int dtype, hipStream_t stream);

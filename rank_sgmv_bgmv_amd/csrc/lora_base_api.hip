@@ -118,7 +118,7 @@ lora_status lora_base_product(const lora_base_weight *weight, const int8_t *q, i
   if (overlap(y, ys, q, span_bytes(n_tokens, ldq, weight->d_in, 1)) || overlap(y, ys, q_scale, size_t(n_tokens) * 4))
     return LORA_EINVAL;
   const ProductArgs a{q,   weight->W,   q_scale, weight->scale, weight->bias, y,
-                      ldq, weight->ldw, ldy,     n_tokens,      weight->d_in, weight->d_out};
+                      ldq, weight->ldw, ldy,     n_tokens,      weight->d_in, weight->d_out, 0};
   return launch_product(a, dtype, stream) == hipSuccess ? LORA_OK : LORA_EHIP;
 }
 
@@ -148,7 +148,7 @@ lora_status lora_base_apply(const lora_base_weight *weight, const void *x, int64
   const QuantArgs qa{x, q, scale, ldx, L.pitch, n_tokens, weight->d_in};
   if (launch_quantize(qa, dtype, stream) != hipSuccess) return LORA_EHIP;
   const ProductArgs a{q,       weight->W,   scale, weight->scale, weight->bias, y,
-                      L.pitch, weight->ldw, ldy,   n_tokens,      weight->d_in, weight->d_out};
+                      L.pitch, weight->ldw, ldy,   n_tokens,      weight->d_in, weight->d_out, 0};
   return launch_product(a, dtype, stream) == hipSuccess ? LORA_OK : LORA_EHIP;
 }
 

@@ -80,16 +80,23 @@ __device__ __forceinline__ i32x4 load16_end(const int8_t *row, int k, int d_in) 
   return move_down(load16(row + start), k - start);
 }
 
-// The first n elements of a vector to y, at any alignment of theirs.
-template <typename E>
+// 16 bytes of results, as aligned as one of them.
+template <typename E> struct ResultVec;
+template <> struct ResultVec<uint16_t> { typedef uint32_t U __attribute__((ext_vector_type(4), aligned(2))); };
+template <> struct ResultVec<float> { typedef uint32_t U __attribute__((ext_vector_type(4), aligned(4))); };
+
+// The first n elements of a vector to y; with BY, past the caches.
+template <bool BY, typename E>
 __device__ __forceinline__ void store_vec(E *y, const uint4 &v, int n) {
-  typedef uint32_t U2 __attribute__((ext_vector_type(4), aligned(2)));
-  typedef uint32_t U4 __attribute__((ext_vector_type(4), aligned(4)));
-  typedef typename std::conditional<sizeof(E) == 2, U2, U4>::type U;
+  typedef typename ResultVec<E>::U U;
   constexpr int kN = 16 / int(sizeof(E));
   if (n >= kN) {
     const U u = {v.x, v.y, v.z, v.w};
-    *(LORA_GLOBAL U *)y = u;
+    LORA_GLOBAL U *p = (LORA_GLOBAL U *)y;
+    if constexpr (BY)
+      __builtin_nontemporal_store(u, p);
+    else
+      *p = u;
   } else {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -393,7 +400,7 @@ hipError_t launch_few_lines(const ProductArgs &a, hipStream_t stream) {
 // each).  A stage of it is 2048 clocks of products; it takes 2444 when all
 // operands are in L2 (four waves of 128 x 128, which read a third less from LDS
 // but cannot fill each other's gaps: 2655) and about 2750 from memory, at 1.85
-// GHz.  8192^3: 413 us, 2.66 POP/s; 16384 rows through 4096 x 4096: 228 us, 2.4
+// GHz.  8192^3: 411 us, 2.67 POP/s; 16384 rows through 4096 x 4096: 221 us, 2.5
 // POP/s, the rest being the tiles' first stages and stores (8 of 57 us a tile).
 // c += a b^T on a 16 x 16 block, c kept where it is: given the choice, the
 // compiler writes the sums elsewhere and moves 200 registers back each stage.
@@ -617,7 +624,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     sw[m] = *reinterpret_cast<const float4 *>(s_o + o);
     b[m] = *reinterpret_cast<const float4 *>(b_o + o);
   }
-  auto store = [&](auto whole) {
+  auto store = [&](auto whole, auto by) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int tt = (wn * NT + j) * 16 + lane % 16;
@@ -643,14 +650,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
         } else {
           out = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
         }
-        if (whole || (tt < n_t && oo < n_o)) store_vec(y + oo, out, whole ? kVec : n_o - oo);
+        if (whole || (tt < n_t && oo < n_o)) store_vec<decltype(by)::value>(y + oo, out, whole ? kVec : n_o - oo);
       }
     }
   };
-  if (n_o == S::kO && n_t == S::kT)
-    store(std::true_type{});
-  else
-    store(std::false_type{});
+  if (n_o < S::kO || n_t < S::kT) {
+    store(std::false_type{}, std::false_type{});
+  } else if (a.y_by) {
+    asm volatile("");
+    store(std::true_type{}, std::true_type{});
+    asm volatile("");  // the compiler would make one of this and what follows, with ordinary stores
+  } else {
+    store(std::true_type{}, std::false_type{});
+  }
 }
 
 template <typename E, int MT, int NT, int WM, int WN, int ST, bool LINES = true>
@@ -793,9 +805,20 @@ hipError_t launch_product(const ProductArgs &args, int dtype, hipStream_t stream
   // what a launch may hold, at one thread for every 16 results at least
   constexpr int kMostT = 1 << 18, kMostO = 1 << 17;
   const int64_t eb = dtype == LORA_BF16 ? 2 : 4;
+  // Results beyond what the L2s hold (4 MiB on each of 8 XCDs) pass them by, and
+  // the operands that other tiles share stay in: 65536 rows through 1280 x 1280
+  // 127 -> 115 us, through 640 x 640 51 -> 42, 16997 rows through 4096 x 4096
+  // 245 -> 232.  Not where rows begin inside a line, which would go out in parts
+  // (65536 x 1280 through 1283 channels 168 -> 202), and not with few products
+  // for a byte of results, when the writing is most of the work (17000 rows
+  // through 4096 x 256 46 -> 48, x 512 64 -> 58; fp32 x 512 84 -> 87, x 1024
+  // 121 -> 114).  Smaller results stay near for what reads them next.
+  const int y_by = args.d_in >= 256 * eb && reinterpret_cast<uintptr_t>(args.y) % 128 == 0 &&
+                   args.ldy * eb % 128 == 0 && int64_t(args.T) * args.d_out * eb > (int64_t(32) << 20);
   for (int64_t t = 0; t < args.T; t += kMostT)
     for (int64_t o = 0; o < args.d_out; o += kMostO) {
       ProductArgs a = args;
+      a.y_by = y_by;
       a.q += t * a.ldq;
       a.q_scale += t;
       a.W += o * a.ldw;

@@ -8,9 +8,9 @@
 // Bound by memory: every value is read and written once, 16 bytes a lane.  A
 // workgroup takes kTokens tokens (one when there are few: then the heads are
 // split over workgroups too) and a lane one 16-byte column of a head, for every
-// slots-th head of each of them.  17k tokens of 40 bf16 heads of 128 take 67 us
-// (5.2 TB/s, as a large copy), with 70 of the 128 turned, whose partners come
-// through LDS, 72; 64 tokens 3.2 us, a launch.
+// slots-th head of each of them.  17k tokens of 40 bf16 heads of 128 take 64.5
+// us (5.4 TB/s, as a large copy), with 70 of the 128 turned, whose partners come
+// through LDS, 69; 64 tokens 3.2 us, a launch.
 
 #include "lora_base.hpp"
 #include "lora_device.hpp"
@@ -82,10 +82,18 @@ __device__ __forceinline__ HeadVec<E> load_head(const E *p, int n) {
   return v;
 }
 template <typename E>
-__device__ __forceinline__ void store_head(E *p, const HeadVec<E> &v, int n) {
+__device__ __forceinline__ void store_head(E *p, const HeadVec<E> &v, int n, int by) {
   if (n >= HeadVec<E>::kN) {
     const typename Unaligned<E>::U u = {v.w[0], v.w[1], v.w[2], v.w[3]};
-    *(LORA_GLOBAL typename Unaligned<E>::U *)p = u;
+    LORA_GLOBAL typename Unaligned<E>::U *to = (LORA_GLOBAL typename Unaligned<E>::U *)p;
+    if (by) {
+      // (the compiler would make one of the two stores, and that an ordinary one)
+      asm volatile("");
+      __builtin_nontemporal_store(u, to);
+      asm volatile("");
+    } else {
+      *to = u;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < HeadVec<E>::kN; ++i)
@@ -185,7 +193,7 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(RotaryArgs a, in
         const auto all = [](int) { return true; };
         x0[t].put(y0, all);
         x1[t].put(y1, all);
-        store_head(p + half, x1[t], kN);
+        store_head(p + half, x1[t], kN, a.by);
       } else if (MODE == ROT_NEXT) {
         float y[kN];
 #pragma unroll
@@ -212,7 +220,7 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(RotaryArgs a, in
         }
         x0[t].put(y, [&](int i) { return i0 + i < a.rot_dim; });
       }
-      store_head(p, x0[t], n0);
+      store_head(p, x0[t], n0, a.by);
     }
   }
 }
@@ -244,9 +252,21 @@ hipError_t launch_mode(const RotaryArgs &a, bool copy_rest, hipStream_t stream) 
 }
 
 template <typename E>
-hipError_t launch_typed(const RotaryArgs &a, hipStream_t stream) {
-  bool copy_rest = false;
-  for (int s = 0; s < a.n_slices; ++s) copy_rest = copy_rest || a.s[s].src != a.s[s].dst;
+hipError_t launch_typed(const RotaryArgs &args, hipStream_t stream) {
+  RotaryArgs a = args;
+  // Heads beyond what the L2s hold (4 MiB on each of 8 XCDs) pass them by where
+  // a lane's neighbours write whole lines: 17k tokens of 40 bf16 heads of 128
+  // 67 -> 64.5 us, of 10 fp32 ones 35.7 -> 28.9; heads of 80, halves of 80
+  // bytes, would go from 28.7 to 39.3, and heads that begin inside a line alike.
+  const int piece = (a.interleaved || a.rot_dim / 2 % HeadVec<E>::kN ? a.head_dim : a.rot_dim / 2) * int(sizeof(E));
+  bool copy_rest = false, whole = piece % 128 == 0;
+  for (int s = 0; s < a.n_slices; ++s) {
+    const lora_rotary_slice &v = a.s[s];
+    copy_rest = copy_rest || v.src != v.dst;
+    whole = whole && reinterpret_cast<uintptr_t>(v.dst) % 128 == 0 && v.dst_token * int(sizeof(E)) % 128 == 0 &&
+            v.dst_head * int(sizeof(E)) % 128 == 0;
+  }
+  a.by = whole && int64_t(a.T) * a.n_heads * a.head_dim * int(sizeof(E)) > (int64_t(32) << 20);
   if (a.interleaved) return launch_mode<E, ROT_NEXT>(a, copy_rest, stream);
   if (a.rot_dim / 2 % HeadVec<E>::kN == 0) return launch_mode<E, ROT_HALVES>(a, copy_rest, stream);
   return launch_mode<E, ROT_ANY>(a, copy_rest, stream);

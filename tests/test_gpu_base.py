@@ -731,3 +731,41 @@ def test_same_bits_again(T):
         dl.y.fill_(9)
         dl.run()
         assert torch.equal(dl.y, y)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("d_out, pad", [(2112, 0), (2048, 64), (2048, 3)])
+def test_product_result_larger_than_the_caches(d_out, pad, dtype):
+    """More than 32 MiB of results: what calls for parts of the rows give, and the columns beside them as they were."""
+    g, T, d_in = torch.Generator(device=DEV).manual_seed(3), 8333, 1024
+    W, q = (torch.randint(-127, 128, s, generator=g, dtype=torch.int8, device=DEV) for s in ((d_out, d_in), (T, d_in)))
+    qs, sc = torch.rand(T, generator=g, device=DEV), torch.rand(d_out, generator=g, device=DEV)
+    w = L.BaseWeight(W, sc)
+    y = torch.full((T, d_out + pad), 9, dtype=dtype, device=DEV)
+    L.lora_base_product(w, q, qs, y[:, :d_out])
+    part = torch.full_like(y, 9)
+    for t in range(0, T, 1000):
+        L.lora_base_product(w, q[t:t + 1000], qs[t:t + 1000], part[t:t + 1000, :d_out])
+    assert torch.equal(y, part)
+    ref, mag = ref_product(q[-300:].cpu(), qs[-300:].cpu(), W.cpu(), sc.cpu(), None)[:2]
+    assert bool(((y[-300:, :d_out].cpu().double() - ref).abs() <= half(dtype) * ref.abs() + 4 * V * mag).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("rot, interleaved, pad", [(128, False, 0), (128, True, 0), (70, False, 0), (128, False, 4)])
+def test_rotary_result_larger_than_the_caches(rot, interleaved, pad, dtype):
+    """More than 32 MiB of heads, in place and not: what calls for parts of the tokens give; a skipped token is left."""
+    g, T, H, D = torch.Generator(device=DEV).manual_seed(4), 4321, 36, 128
+    x = torch.randn(T, H, D + pad, generator=g, device=DEV).to(dtype)
+    pos = torch.randint(-2, 5000, (T,), generator=g, dtype=torch.int32, device=DEV)
+    r = L.Rotary(L.lora_rotary_frequencies(rot).to(DEV), D, interleaved=interleaved)
+    y, part, own = torch.full_like(x, 9), torch.full_like(x, 9), x.clone()
+    L.lora_rotary_apply(r, pos, [x[..., :D]], [y[..., :D]])
+    L.lora_rotary_apply(r, pos, [own[..., :D]])
+    for t in range(0, T, 500):
+        L.lora_rotary_apply(r, pos[t:t + 500], [x[t:t + 500, :, :D]], [part[t:t + 500, :, :D]])
+    assert torch.equal(y, part)
+    keep = pos >= 0
+    assert torch.equal(own[keep][..., :D], part[keep][..., :D])
+    assert torch.equal(own[~keep], x[~keep])
+    assert bool((y[~keep] == 9).all()) and torch.equal(own[..., D:], x[..., D:])
