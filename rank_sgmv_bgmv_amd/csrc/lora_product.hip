@@ -400,7 +400,7 @@ hipError_t launch_few_lines(const ProductArgs &a, hipStream_t stream) {
 // each).  A stage of it is 2048 clocks of products; it takes 2444 when all
 // operands are in L2 (four waves of 128 x 128, which read a third less from LDS
 // but cannot fill each other's gaps: 2655) and about 2750 from memory, at 1.85
-// GHz.  8192^3: 411 us, 2.67 POP/s; 16384 rows through 4096 x 4096: 221 us, 2.5
+// GHz.  8192^3: 397 us, 2.77 POP/s; 16384 rows through 4096 x 4096: 207 us, 2.7
 // POP/s, the rest being the tiles' first stages and stores (8 of 57 us a tile).
 // c += a b^T on a 16 x 16 block, c kept where it is: given the choice, the
 // compiler writes the sums elsewhere and moves 200 registers back each stage.
@@ -613,9 +613,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
   // Results leave from registers.  A lane has four channels of a token in each
   // block, its neighbours 16 lanes on the next four: in bf16 two blocks change
   // places between such neighbours, so that each has eight of one block, and
-  // every store is 16 bytes a lane and 64 a token.  A token's stores follow one
-  // another, so that its lines fill up in L2: 65536 rows through
-  // 1280 x 1280 134 us block by block, 130 token by token.
+  // a store is 16 bytes a lane and 64 a token.  Whole tiles go further: the lanes
+  // of tokens 0..7 and 8..15 change their second halves, and a store writes a
+  // line of 128 bytes of eight tokens (65536 rows through 1280 x 1280 114 -> 104
+  // us, 16997 through 4096 x 4096 235 -> 226).  Elsewhere a token's stores follow
+  // one another, so that its lines fill up in L2.
   constexpr int kVec = 16 / int(sizeof(E));
   float4 sw[MT], b[MT];
 #pragma unroll
@@ -624,33 +626,53 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     sw[m] = *reinterpret_cast<const float4 *>(s_o + o);
     b[m] = *reinterpret_cast<const float4 *>(b_o + o);
   }
+  auto result = [&](int m, int j, float sx) -> uint4 {
+    float v[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec / 4; ++k) {
+      const i32x4 &c = acc[m + k][j];
+      v[k * 4] = float(c[0]) * sx * sw[m + k].x + b[m + k].x;
+      v[k * 4 + 1] = float(c[1]) * sx * sw[m + k].y + b[m + k].y;
+      v[k * 4 + 2] = float(c[2]) * sx * sw[m + k].z + b[m + k].z;
+      v[k * 4 + 3] = float(c[3]) * sx * sw[m + k].w + b[m + k].w;
+    }
+    if constexpr (kVec == 8) {
+      const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf2(v[0], v[1]), pack_bf2(v[4], v[5]), false, false);
+      const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf2(v[2], v[3]), pack_bf2(v[6], v[7]), false, false);
+      return make_uint4(lo[0], hi[0], lo[1], hi[1]);
+    }
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  };
+  const int o_lane = wm * MT * 16 + (kVec == 8 ? lane / 16 % 2 * 16 + lane / 32 * 8 : lane / 16 * 4);
   auto store = [&](auto whole, auto by) {
+    constexpr int kStep = kVec / 4;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int tt = (wn * NT + j) * 16 + lane % 16;
       const float sx = s_t[tt];
-      E *y = static_cast<E *>(a.y) + (t0 + tt) * a.ldy + o0;
+      if constexpr (decltype(whole)::value && MT % (2 * kStep) == 0) {
+        const bool low = lane % 16 < 8;
+        E *y = static_cast<E *>(a.y) + (t0 + (wn * NT + j) * 16 + lane % 8) * a.ldy + o0 + o_lane + (low ? 0 : kStep * 16);
 #pragma unroll
-      for (int m = 0; m < MT; m += kVec / 4) {
-        const int oo = (wm * MT + m) * 16 + (kVec == 8 ? lane / 16 % 2 * 16 + lane / 32 * 8 : lane / 16 * 4);
-        float v[kVec];
+        for (int m = 0; m < MT; m += 2 * kStep) {
+          const uint4 p = result(m, j, sx), q = result(m + kStep, j, sx);
+          auto move = [&](uint32_t of_p, uint32_t of_q) {
+            return uint32_t(__builtin_amdgcn_update_dpp(0, int(low ? of_q : of_p), 0x128, 0xf, 0xf, false));  // row_ror:8
+          };
+          const uint4 x = make_uint4(move(p.x, q.x), move(p.y, q.y), move(p.z, q.z), move(p.w, q.w));
+          store_vec<decltype(by)::value>(
+              y + m * 16, make_uint4(low ? p.x : x.x, low ? p.y : x.y, low ? p.z : x.z, low ? p.w : x.w), kVec);
+          store_vec<decltype(by)::value>(
+              y + 8 * a.ldy + m * 16, make_uint4(low ? x.x : q.x, low ? x.y : q.y, low ? x.z : q.z, low ? x.w : q.w), kVec);
+        }
+      } else {
+        E *y = static_cast<E *>(a.y) + (t0 + tt) * a.ldy + o0;
 #pragma unroll
-        for (int k = 0; k < kVec / 4; ++k) {
-          const i32x4 &c = acc[m + k][j];
-          v[k * 4] = float(c[0]) * sx * sw[m + k].x + b[m + k].x;
-          v[k * 4 + 1] = float(c[1]) * sx * sw[m + k].y + b[m + k].y;
-          v[k * 4 + 2] = float(c[2]) * sx * sw[m + k].z + b[m + k].z;
-          v[k * 4 + 3] = float(c[3]) * sx * sw[m + k].w + b[m + k].w;
+        for (int m = 0; m < MT; m += kStep) {
+          const int oo = o_lane + m * 16;
+          const uint4 out = result(m, j, sx);
+          if (whole || (tt < n_t && oo < n_o)) store_vec<decltype(by)::value>(y + oo, out, whole ? kVec : n_o - oo);
         }
-        uint4 out;
-        if constexpr (kVec == 8) {
-          const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf2(v[0], v[1]), pack_bf2(v[4], v[5]), false, false);
-          const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf2(v[2], v[3]), pack_bf2(v[6], v[7]), false, false);
-          out = make_uint4(lo[0], hi[0], lo[1], hi[1]);
-        } else {
-          out = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-        }
-        if (whole || (tt < n_t && oo < n_o)) store_vec<decltype(by)::value>(y + oo, out, whole ? kVec : n_o - oo);
       }
     }
   };
@@ -813,8 +835,13 @@ hipError_t launch_product(const ProductArgs &args, int dtype, hipStream_t stream
   // for a byte of results, when the writing is most of the work (17000 rows
   // through 4096 x 256 46 -> 48, x 512 64 -> 58; fp32 x 512 84 -> 87, x 1024
   // 121 -> 114).  Smaller results stay near for what reads them next.
-  const int y_by = args.d_in >= 256 * eb && reinterpret_cast<uintptr_t>(args.y) % 128 == 0 &&
-                   args.ldy * eb % 128 == 0 && int64_t(args.T) * args.d_out * eb > (int64_t(32) << 20);
+  // Results pass L2 by where every row begins on a whole line, and the operands
+  // that other tiles share stay in: 65536 rows through 1280 x 1280 128 -> 105 us,
+  // through 640 x 128 26 -> 20, 2304 rows through 14336 x 4096 112 -> 105, 1024
+  // rows through 4096 x 4096 19.8 -> 19.0; fewer take the same, and so does
+  // what reads them next.  Rows that begin inside a line would go out in parts
+  // (65536 x 1280 through 1283 channels 168 -> 202).
+  const int y_by = reinterpret_cast<uintptr_t>(args.y) % 128 == 0 && args.ldy * eb % 128 == 0;
   for (int64_t t = 0; t < args.T; t += kMostT)
     for (int64_t o = 0; o < args.d_out; o += kMostO) {
       ProductArgs a = args;

@@ -254,19 +254,19 @@ hipError_t launch_mode(const RotaryArgs &a, bool copy_rest, hipStream_t stream) 
 template <typename E>
 hipError_t launch_typed(const RotaryArgs &args, hipStream_t stream) {
   RotaryArgs a = args;
-  // Heads beyond what the L2s hold (4 MiB on each of 8 XCDs) pass them by where
-  // a lane's neighbours write whole lines: 17k tokens of 40 bf16 heads of 128
-  // 67 -> 64.5 us, of 10 fp32 ones 35.7 -> 28.9; heads of 80, halves of 80
+  // Values pass L2 by where a lane's neighbours write whole lines: 17k tokens of
+  // 40 bf16 heads of 128 take 67 -> 64.5 us, of 10 fp32 ones 35.6 -> 29.0, 1000
+  // tokens 7.8 -> 6.4; fewer or in place the same.  Heads of 80, halves of 80
   // bytes, would go from 28.7 to 39.3, and heads that begin inside a line alike.
   const int piece = (a.interleaved || a.rot_dim / 2 % HeadVec<E>::kN ? a.head_dim : a.rot_dim / 2) * int(sizeof(E));
-  bool copy_rest = false, whole = piece % 128 == 0;
+  bool copy_rest = false;
+  a.by = piece % 128 == 0;
   for (int s = 0; s < a.n_slices; ++s) {
     const lora_rotary_slice &v = a.s[s];
     copy_rest = copy_rest || v.src != v.dst;
-    whole = whole && reinterpret_cast<uintptr_t>(v.dst) % 128 == 0 && v.dst_token * int(sizeof(E)) % 128 == 0 &&
-            v.dst_head * int(sizeof(E)) % 128 == 0;
+    a.by = a.by && reinterpret_cast<uintptr_t>(v.dst) % 128 == 0 && v.dst_token * int(sizeof(E)) % 128 == 0 &&
+           v.dst_head * int(sizeof(E)) % 128 == 0;
   }
-  a.by = whole && int64_t(a.T) * a.n_heads * a.head_dim * int(sizeof(E)) > (int64_t(32) << 20);
   if (a.interleaved) return launch_mode<E, ROT_NEXT>(a, copy_rest, stream);
   if (a.rot_dim / 2 % HeadVec<E>::kN == 0) return launch_mode<E, ROT_HALVES>(a, copy_rest, stream);
   return launch_mode<E, ROT_ANY>(a, copy_rest, stream);
