@@ -782,8 +782,8 @@ hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
     const int tile = choose_tile(a, ~0u, us);
     // Whole rounds of one shape first and the rest, which would leave most CUs
     // idle in a last round, by itself: 16997 rows through 4096 x 4096, 4.2
-    // rounds of 256 x 256 tiles, 242 us instead of 254, through 4096 x 1024 67
-    // instead of 80.
+    // rounds of 256 x 256 tiles, 228 us instead of 243, through 4096 x 1024 62
+    // instead of 71.
     const int first = split_rows(a, us);
     if (first > 0) {
       ProductArgs b = a;
