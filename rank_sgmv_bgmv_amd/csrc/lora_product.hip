@@ -401,7 +401,7 @@ hipError_t launch_few_lines(const ProductArgs &a, hipStream_t stream) {
 // operands are in L2 (four waves of 128 x 128, which read a third less from LDS
 // but cannot fill each other's gaps: 2655) and about 2750 from memory, at 1.85
 // GHz.  8192^3: 397 us, 2.77 POP/s; 16384 rows through 4096 x 4096: 207 us, 2.7
-// POP/s, the rest being the tiles' first stages and stores (8 of 57 us a tile).
+// POP/s, the rest being the tiles' first stages and stores (4 of 52 us a tile).
 // c += a b^T on a 16 x 16 block, c kept where it is: given the choice, the
 // compiler writes the sums elsewhere and moves 200 registers back each stage.
 // It sees no matrix instruction here, so the waits that it would insert stand
