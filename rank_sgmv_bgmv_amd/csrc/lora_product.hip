@@ -716,9 +716,9 @@ struct TileCost {
   float alone, full, once;  // per stage, per stage with a full CU, per tile
 };
 constexpr TileCost kTileCosts[] = {
-    {256, 256, 1, 1.10f, 1.45f, 8.0f}, {192, 256, 1, 0.88f, 1.20f, 6.0f}, {128, 128, 2, 0.60f, 0.82f, 4.0f},
+    {256, 256, 1, 1.10f, 1.45f, 6.0f}, {192, 256, 1, 0.88f, 1.20f, 5.0f}, {128, 128, 2, 0.60f, 0.82f, 3.2f},
     {128, 128, 1, 0.48f, 0.48f, 3.0f}, {128, 64, 1, 0.33f, 0.33f, 2.5f},  {64, 64, 2, 0.19f, 0.45f, 3.0f},
-    {128, 160, 2, 0.75f, 1.13f, 4.0f},
+    {128, 160, 2, 0.75f, 1.13f, 3.2f},
 };
 
 // The shape of the least cost, among those whose bit is set in `among`.
