@@ -705,12 +705,12 @@ hipError_t launch_tiles(const ProductArgs &a, hipStream_t stream) {
 // tiles move the fewest bytes for each product, small ones fill more CUs.
 // Measured, with the shapes in their order here:
 //                              256x256 192x256 128x128 128x128 128x64 64x64 128x160
-//   512 rows,  4096 -> 4096       40.3    34.1    22.7    18.0   13.8  18.0    24.6
-//   512 rows,  4096 -> 14336      55.3    50.1    41.8    46.8   62.4  58.7    43.0
-//   2304 rows, 4096 -> 4096       46.8    40.3    51.5    55.3   58.4  61.4    40.4
-//   2304 rows, 14336 -> 4096       165     145     178     173    188   209     129
-//   2304 rows, 4096 -> 14336       117     132     136     156    189   210     145
-//   16997 rows, 4096 -> 4096       260     265     283     331    411   436     271
+//   512 rows,  4096 -> 4096       39.9    33.6    22.1    17.0   12.5  14.2    23.3
+//   512 rows,  4096 -> 14336      40.3    34.0    28.6    34.5   43.5  45.5    35.2
+//   2304 rows, 4096 -> 4096       41.7    36.5    49.8    49.8   54.9  58.2    37.4
+//   2304 rows, 14336 -> 4096       153     138     174     157    172   201     121
+//   2304 rows, 4096 -> 14336       101     117     116     144    175   195     127
+//   16997 rows, 4096 -> 4096       247     252     261     309    381   412     255
 struct TileCost {
   int o, t, at_once;
   float alone, full, once;  // per stage, per stage with a full CU, per tile
