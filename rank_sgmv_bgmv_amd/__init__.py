@@ -419,6 +419,15 @@ def _launch(index: int, what: str, f, *args):
         raise LoraError(st, what)
 
 
+_INT32_MAX = 0x7fffffff
+
+
+def _fits_32(what: str, a: int, b: int = 0):
+    """The C ABI's sizes are 32-bit; the call would get the low bits of a larger one."""
+    if a > _INT32_MAX or b > _INT32_MAX:
+        raise LoraError(-2, f"{what}: sizes must be below 2^31 (got {max(a, b)})")
+
+
 def _row(t, dtype, index: int) -> int:
     """The row stride of a 2-D tensor of this type and device with unit column stride; 0 if t is not plainly one."""
     if t.dtype is not dtype or t.get_device() != index:
@@ -465,6 +474,7 @@ class BaseWeight:
             raise LoraError(-2, "W must be [d_out][d_in]")
         self.ld = _rows_2d("BaseWeight", "W", W, (torch.int8,), W.device, 1)
         self.d_out, self.d_in = int(W.shape[0]), int(W.shape[1])
+        _fits_32("BaseWeight", self.d_out, self.d_in)
         for name, t in (("scale", scale), ("bias", bias)):
             if t is not None:
                 _vector("BaseWeight", name, t, torch.float32, W.device, self.d_out)
@@ -490,6 +500,7 @@ def lora_quantize_rows(x, q, scale):
         ldq = _rows_2d(what, "q", q, (torch.int8,), dev, 1)
         _vector(what, "scale", scale, torch.float32, dev, x.shape[0])
     T, d = x.shape
+    _fits_32(what, T, d)
     _launch(index, what, lib().lora_quantize_rows, x.data_ptr(), ldx, code, T, d, q.data_ptr(), ldq, scale.data_ptr())
 
 
@@ -510,12 +521,14 @@ def lora_base_product(weight: BaseWeight, q, q_scale, y):
             raise LoraError(-2, f"{what}: q must be [T][{d_in}]")
         ldy = _rows_2d(what, "y", y, _REAL, dev, weight.d_out, T)
         _vector(what, "q_scale", q_scale, torch.float32, dev, T)
+    _fits_32(what, T)
     _launch(index, what, lib().lora_base_product, weight.ref, q.data_ptr(), ldq, q_scale.data_ptr(), T, y.data_ptr(), ldy,
             code)
 
 
 def lora_base_workspace_size(weight: BaseWeight, n_tokens: int) -> int:
-    return int(lib().lora_base_workspace_size(weight.ref, n_tokens))
+    _fits_32("lora_base_workspace_size", n_tokens)
+    return int(lib().lora_base_workspace_size(weight.ref, max(n_tokens, 0)))
 
 
 def new_base_workspace(weight: BaseWeight, n_tokens: int):
@@ -540,6 +553,7 @@ def lora_base_apply(weight: BaseWeight, x, y, ws):
             raise LoraError(-2, f"{what}: x must be [T][{d_in}]")
         ldy = _rows_2d(what, "y", y, (x.dtype,), dev, weight.d_out, T)
         _vector(what, "ws", ws, torch.uint8, dev, 0)
+    _fits_32(what, T)
     _launch(index, what, lib().lora_base_apply, weight.ref, x.data_ptr(), ldx, T, y.data_ptr(), ldy, code, ws.data_ptr(),
             ws.shape[0])
 
@@ -588,6 +602,7 @@ def lora_rotary_apply(rotary: Rotary, positions, src: Sequence, dst: Optional[Se
             if b.dtype is not dtype or b.get_device() != index or b.shape != shape or (sb[2] != 1 and D > 1):
                 raise LoraError(-2, f"{what}: dst must be like src (got {b.dtype} {tuple(b.shape)} on {b.device}, "
                                     f"strides {sb})")
+        _fits_32(what, T, shape[1])
         slices += _pack_slice(pa, pb, sa[0], sa[1], sb[0], sb[1], shape[1])
     _launch(index, what, lib().lora_rotary_apply, rotary.ref, positions.data_ptr(), T, n, slices, code, 1 if inverse else 0)
 
@@ -595,6 +610,7 @@ def lora_rotary_apply(rotary: Rotary, positions, src: Sequence, dst: Optional[Se
 def lora_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = LORA_ROTARY_PLAIN, factor: float = 1.0,
                             length: float = 1.0, low: float = 0.0, high: float = 1.0):
     """Frequencies float64 [rot_dim / 2] on the host (include/lora_base.h: the scalings of long contexts)."""
+    _fits_32("lora_rotary_frequencies", rot_dim)
     freq = _torch().empty(max(int(rot_dim), 0) // 2, dtype=_torch().float64)
     _check(lib().lora_rotary_frequencies(int(scaling), float(base), int(rot_dim), float(factor), float(length),
                                          float(low), float(high), _ptr(freq) if freq.numel() else None),

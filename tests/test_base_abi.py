@@ -206,3 +206,72 @@ def test_host_tensors_are_refused():
         L.lora_quantize_rows(torch.zeros(2, 16), i8, f)
     with pytest.raises(L.LoraError):
         L.Rotary(torch.ones(4, dtype=torch.float64), 8)
+
+
+class Stand:
+    """What a call of the binding sees of a device tensor; its memory is never touched."""
+
+    def __init__(self, dtype, *shape, strides=None):
+        self.dtype, self.shape, self.device = dtype, torch.Size(shape), torch.device("cuda:0")
+        n = [1]
+        for s in shape[:0:-1]:
+            n.insert(0, n[0] * s)
+        self.strides = tuple(n) if strides is None else strides
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        return self.strides if i is None else self.strides[i]
+
+    def get_device(self):
+        return 0
+
+    def data_ptr(self):
+        return FAKE
+
+
+@pytest.fixture
+def launched(lib, monkeypatch):
+    """The arguments of the calls that the binding would make, in place of the calls."""
+    calls = []
+    monkeypatch.setattr(L, "_launch", lambda index, what, f, *args: calls.append(args))
+    return calls
+
+
+MANY = (1 << 32) + 5
+
+
+def stand_weight(d_out=8, d_in=4):
+    return L.BaseWeight(Stand(torch.int8, d_out, d_in), Stand(torch.float32, d_out))
+
+
+def stand_rotary():
+    return L.Rotary(torch_freq(2), 4)
+
+
+def torch_freq(n):
+    f = Stand(torch.float64, n)
+    f.numel = lambda: n
+    return f
+
+
+@pytest.mark.parametrize("call", [
+    lambda: L.lora_quantize_rows(Stand(torch.float32, MANY, 4), Stand(torch.int8, MANY, 4), Stand(torch.float32, MANY)),
+    lambda: L.lora_quantize_rows(Stand(torch.float32, 1, MANY), Stand(torch.int8, 1, MANY), Stand(torch.float32, 1)),
+    lambda: L.lora_base_product(stand_weight(), Stand(torch.int8, MANY, 4), Stand(torch.float32, MANY),
+                                Stand(torch.float32, MANY, 8)),
+    lambda: L.lora_base_apply(stand_weight(), Stand(torch.float32, MANY, 4), Stand(torch.float32, MANY, 8),
+                              Stand(torch.uint8, 1 << 40)),
+    lambda: L.lora_rotary_apply(stand_rotary(), Stand(torch.int32, MANY), [Stand(torch.float32, MANY, 1, 4)]),
+    lambda: L.lora_rotary_apply(stand_rotary(), Stand(torch.int32, 1), [Stand(torch.float32, 1, MANY, 4)]),
+    lambda: stand_weight(d_out=MANY), lambda: stand_weight(d_in=MANY),
+    lambda: L.lora_base_workspace_size(stand_weight(), MANY), lambda: L.new_base_workspace(stand_weight(), MANY),
+    lambda: L.lora_rotary_frequencies(MANY + 1),
+], ids=["quantize rows", "quantize columns", "product", "apply", "rotary tokens", "rotary heads", "weight rows",
+        "weight columns", "workspace size", "workspace", "frequencies"])
+def test_sizes_beyond_32_bits_are_refused(launched, call):
+    """The C ABI's sizes are 32-bit: what does not fit is refused, not cut to its low bits."""
+    with pytest.raises(L.LoraError):
+        call()
+    assert not launched
