@@ -429,7 +429,8 @@ def _fits_32(what: str, a: int, b: int = 0):
 
 
 def _row(t, dtype, index: int) -> int:
-    """The row stride of a 2-D tensor of this type and device with unit column stride; 0 if t is not plainly one."""
+    """The row stride of a 2-D tensor of this type and device with unit column stride; 0 if t is not plainly one.
+    (One below the columns is not plain either: a single row may have any.)"""
     if t.dtype is not dtype or t.get_device() != index:
         return 0
     s = t.stride()
@@ -492,7 +493,8 @@ def lora_quantize_rows(x, q, scale):
     what, index = "lora_quantize_rows", x.get_device()
     code = _REAL.get(x.dtype, -1)
     ldx, ldq = _row(x, x.dtype, index), _row(q, torch.int8, index)
-    if index < 0 or code < 0 or ldx == 0 or ldq == 0 or x.shape != q.shape or not _line(scale, torch.float32, index, x.shape[0]):
+    if (index < 0 or code < 0 or ldx == 0 or ldq == 0 or x.shape != q.shape or ldx < x.shape[1] or ldq < x.shape[1]
+            or not _line(scale, torch.float32, index, x.shape[0])):
         dev = x.device
         if x.dim() != 2 or q.dim() != 2 or x.shape != q.shape:
             raise LoraError(-2, f"{what}: x and q must be of one shape [T][d]")
@@ -512,7 +514,7 @@ def lora_base_product(weight: BaseWeight, q, q_scale, y):
     code = _REAL.get(y.dtype, -1)
     ldq, ldy = _row(q, torch.int8, index), _row(y, y.dtype, index)
     T = q.shape[0] if ldq else 0
-    if (code < 0 or ldq == 0 or ldy == 0 or q.shape[1] != d_in or y.shape[0] < T or y.shape[1] < weight.d_out
+    if (code < 0 or ldq < d_in or ldy < weight.d_out or q.shape[1] != d_in or y.shape[0] < T or y.shape[1] < weight.d_out
             or not _line(q_scale, torch.float32, index, T)):
         dev = weight.device
         ldq = _rows_2d(what, "q", q, (torch.int8,), dev, d_in)
@@ -544,7 +546,7 @@ def lora_base_apply(weight: BaseWeight, x, y, ws):
     code = _REAL.get(x.dtype, -1)
     ldx, ldy = _row(x, x.dtype, index), _row(y, x.dtype, index)
     T = x.shape[0] if ldx else 0
-    if (code < 0 or ldx == 0 or ldy == 0 or x.shape[1] != d_in or y.shape[0] < T or y.shape[1] < weight.d_out
+    if (code < 0 or ldx < d_in or ldy < weight.d_out or x.shape[1] != d_in or y.shape[0] < T or y.shape[1] < weight.d_out
             or not _line(ws, torch.uint8, index, 0)):
         dev = weight.device
         ldx = _rows_2d(what, "x", x, _REAL, dev, d_in)

@@ -275,3 +275,26 @@ def test_sizes_beyond_32_bits_are_refused(launched, call):
     with pytest.raises(L.LoraError):
         call()
     assert not launched
+
+
+def one_row(dtype, n):
+    """A tensor [1][n] as torch gives it for the transpose of a column: contiguous, with strides (1, 1)."""
+    return Stand(dtype, 1, n, strides=(1, 1))
+
+
+def test_one_row_may_have_any_row_stride(launched):
+    """Where there is one row, its stride says nothing: the call gets one that fits its columns."""
+    w = stand_weight(d_out=8, d_in=4)
+    for x, y in ((one_row(torch.float32, 4), Stand(torch.float32, 1, 8)), (Stand(torch.float32, 1, 4), one_row(torch.float32, 8))):
+        L.lora_base_apply(w, x, y, Stand(torch.uint8, 4096))
+        ldx, ldy = launched[-1][2], launched[-1][5]
+        assert ldx >= 4 and ldy >= 8
+    for q, y in ((one_row(torch.int8, 4), Stand(torch.float32, 1, 8)), (Stand(torch.int8, 1, 4), one_row(torch.float32, 8))):
+        L.lora_base_product(w, q, Stand(torch.float32, 1), y)
+        ldq, ldy = launched[-1][2], launched[-1][6]
+        assert ldq >= 4 and ldy >= 8
+    for x, q in ((one_row(torch.float32, 4), Stand(torch.int8, 1, 4)), (Stand(torch.float32, 1, 4), one_row(torch.int8, 4))):
+        L.lora_quantize_rows(x, q, Stand(torch.float32, 1))
+        ldx, ldq = launched[-1][1], launched[-1][6]
+        assert ldx >= 4 and ldq >= 4
+    assert len(launched) == 6

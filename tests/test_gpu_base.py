@@ -769,3 +769,26 @@ def test_rotary_result_larger_than_the_caches(rot, interleaved, pad, dtype):
     assert torch.equal(own[keep][..., :D], part[keep][..., :D])
     assert torch.equal(own[~keep], x[~keep])
     assert bool((y[~keep] == 9).all()) and torch.equal(own[..., D:], x[..., D:])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+def test_one_row_as_the_transpose_of_a_column(dtype):
+    """[1][d] with strides (1, 1), which torch calls contiguous, as x, q and y of the calls that take rows."""
+    g, d, n = gen(21), 200, 72
+    x = torch.randn(1, d, generator=g).to(dtype)
+    W, ws = i8((n, d), g), torch.rand(n, generator=g) * 0.01
+    w = L.BaseWeight(W.to(DEV), ws.to(DEV))
+    column = lambda k, t: torch.zeros(k, 1, dtype=t, device=DEV).t()  # noqa: E731
+    xv, qv, s, y = column(d, dtype), column(d, torch.int8), torch.zeros(1, device=DEV), column(n, dtype)
+    assert xv.stride() == (1, 1) and xv.is_contiguous()
+    xv.copy_(x)
+    L.lora_quantize_rows(xv, qv, s)
+    q, qs = ref_quantize(x)
+    assert torch.equal(qv.cpu(), q) and torch.equal(s.cpu(), qs)
+    ref, mag = ref_product(q, qs, W, ws, None)
+    tol = half(dtype) * ref.abs() + 4 * V * mag
+    L.lora_base_product(w, qv, s, y)
+    assert bool(((y.cpu().double() - ref).abs() <= tol).all())
+    y.zero_()
+    L.lora_base_apply(w, xv, y, L.new_base_workspace(w, 1))
+    assert bool(((y.cpu().double() - ref).abs() <= tol).all())
