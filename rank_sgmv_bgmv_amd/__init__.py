@@ -132,7 +132,8 @@ def _torch():
     global _torch_module, _REAL
     if _torch_module is None:
         import torch
-        _torch_module, _REAL = torch, {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32}
+        _REAL = {torch.bfloat16: LORA_BF16, torch.float32: LORA_F32}
+        _torch_module = torch  # last: who finds it, in another thread too, finds the types
     return _torch_module
 
 

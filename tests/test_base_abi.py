@@ -6,6 +6,7 @@ import ctypes
 import math
 import os
 import re
+import sys
 
 import numpy as np
 import pytest
@@ -298,3 +299,26 @@ def test_one_row_may_have_any_row_stride(launched):
         ldx, ldq = launched[-1][1], launched[-1][6]
         assert ldx >= 4 and ldq >= 4
     assert len(launched) == 6
+
+
+def test_a_second_thread_never_sees_the_types_missing(monkeypatch):
+    """At every bytecode of the binding's first look at torch: a thread that finds the module set finds its types too."""
+    monkeypatch.setattr(L, "_torch_module", None)
+    monkeypatch.setattr(L, "_REAL", {})
+    seen = []
+
+    def trace(frame, event, arg):
+        if frame.f_code is L._torch.__code__:
+            frame.f_trace_opcodes = True
+            seen.append((L._torch_module is not None, len(L._REAL)))
+            return trace
+        return None
+
+    old = sys.gettrace()
+    sys.settrace(trace)
+    try:
+        L._torch()
+    finally:
+        sys.settrace(old)
+    assert len(seen) > 5 and seen[0] == (False, 0) and seen[-1] == (True, 2)
+    assert all(types == 2 for module, types in seen if module)
