@@ -11,6 +11,8 @@ v = 2^-24 (a float32 rounding):
                    4 v m each; two products and a sum, 2 v more:
                    u |y| + 6 v m (|a| + |b|)
 """
+import fractions
+
 import numpy as np
 import pytest
 import torch
@@ -792,3 +794,28 @@ def test_one_row_as_the_transpose_of_a_column(dtype):
     y.zero_()
     L.lora_base_apply(w, xv, y, L.new_base_workspace(w, 1))
     assert bool(((y.cpu().double() - ref).abs() <= tol).all())
+
+
+PI = fractions.Fraction(31415926535897932384626433832795028841971693993751058209749445923078164062862, 10 ** 76)
+
+
+@pytest.mark.parametrize("lo, hi", [(0, 1000), (1 << 30, (1 << 31) - 1)])
+def test_rotary_angles_at_the_ends_of_the_positions(lo, hi):
+    """Pairs (1, 0) give cosine and sine themselves: no rounding follows them.  With the angle reduced exactly here, w
+    below pi / 4 is off by v / 2 as a float32 (what float64 leaves out, 2^31 by 2^-104, is nothing beside it).
+    Cosine: v / 2 of that times sin w (0.36 v), the last rounding v / 2, w^2 / 2 by one rounding and its factor by a
+    quarter (0.31 + 0.16 v), as sums of the worst: below 1.4 v.  Sine: cos w (0.44 v where w is that far off), v / 2,
+    w^3 / 6 by three roundings (0.25 v): below 1.2 v."""
+    rot, T = 32, 400
+    freq = L.lora_rotary_frequencies(rot)
+    pos = torch.from_numpy(np.random.default_rng(7).integers(lo, hi, T)).int()
+    pos[-1] = hi
+    x = torch.zeros(T, 1, rot)
+    x[..., ::2] = 1
+    x = x.to(DEV)
+    L.lora_rotary_apply(L.Rotary(freq.to(DEV), rot, interleaved=True), pos.to(DEV), [x])
+    turns = [[fractions.Fraction(p) * fractions.Fraction(f) / (2 * PI) for f in freq.tolist()] for p in pos.tolist()]
+    w = torch.tensor([[float((t - round(t)) * 2 * PI) for t in row] for row in turns], dtype=torch.float64)
+    got = x.cpu().double()[:, 0]
+    assert float((got[:, ::2] - torch.cos(w)).abs().max()) <= 1.4 * V
+    assert float((got[:, 1::2] - torch.sin(w)).abs().max()) <= 1.4 * V
