@@ -26,6 +26,22 @@ struct ProductArgs {
 };
 hipError_t launch_product(const ProductArgs &a, int dtype, hipStream_t stream);
 
+// The product's kernels, and which one a launch takes.
+enum {
+  PRODUCT_TILE = 0,       // tiles, in the order of their costs
+  PRODUCT_FEW_LINES = 7,  // up to 16, 32 and 64 rows of whole 16-byte pieces
+  PRODUCT_FEW = 10,       // up to 16 rows
+  PRODUCT_ROWS_128 = 11,  // tiles of 128 x 128 and 64 x 64 through registers
+  PRODUCT_ROWS_64 = 12,
+  PRODUCT_ANY = 13,
+  PRODUCT_KERNELS = 14
+};
+struct ProductChoice {
+  int kernel;
+  int first;  // not 0: so many rows in a launch of their own and the rest in another, each with a choice of its own
+};
+ProductChoice choose_product(const ProductArgs &a);
+
 struct RotaryArgs {
   const double *freq;
   const int32_t *positions;

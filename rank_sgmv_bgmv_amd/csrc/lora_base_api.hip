@@ -122,6 +122,20 @@ lora_status lora_base_product(const lora_base_weight *weight, const int8_t *q, i
   return launch_product(a, dtype, stream) == hipSuccess ? LORA_OK : LORA_EHIP;
 }
 
+// For the tests, in no header: the kernel that one launch of these sizes takes (16-byte aligned q and W), and in
+// *first the rows that go in a launch of their own before the others.
+int32_t lora_base_product_choice(int32_t n_tokens, int32_t d_in, int32_t d_out, int64_t ldq, int64_t ldw, int32_t *first) {
+  ProductArgs a{};
+  a.T = n_tokens;
+  a.d_in = d_in;
+  a.d_out = d_out;
+  a.ldq = ldq;
+  a.ldw = ldw;
+  const ProductChoice c = choose_product(a);
+  *first = c.first;
+  return c.kernel;
+}
+
 size_t lora_base_workspace_size(const lora_base_weight *weight, int32_t n_tokens) {
   if (check_weight(weight) != LORA_OK || n_tokens < 1) return 0;
   return base_layout(weight->d_in, n_tokens).total;

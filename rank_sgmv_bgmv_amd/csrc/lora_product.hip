@@ -773,8 +773,44 @@ double cost_of_few(const ProductArgs &a) {
 }
 
 template <typename E>
-hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
-  ProductArgs a = args;
+hipError_t launch_typed(const ProductArgs &a, hipStream_t stream) {
+  const ProductChoice c = choose_product(a);
+  if (c.first > 0) {
+    ProductArgs b = a;
+    b.T = c.first;
+    hipError_t e = launch_typed<E>(b, stream);
+    if (e != hipSuccess) return e;
+    b = a;
+    b.q += c.first * b.ldq;
+    b.q_scale += c.first;
+    b.y = static_cast<E *>(b.y) + c.first * b.ldy;
+    b.T -= c.first;
+    return launch_typed<E>(b, stream);
+  }
+  switch (c.kernel) {
+    case PRODUCT_TILE: return launch_tiles<E, 8, 4, 2, 4, 2>(a, stream);
+    case PRODUCT_TILE + 1: return launch_tiles<E, 6, 4, 2, 4, 2>(a, stream);
+    case PRODUCT_TILE + 2: return launch_tiles<E, 4, 4, 2, 2, 2>(a, stream);
+    case PRODUCT_TILE + 3: return launch_tiles<E, 4, 4, 2, 2, 4>(a, stream);
+    case PRODUCT_TILE + 4: return launch_tiles<E, 4, 2, 2, 2, 4>(a, stream);
+    case PRODUCT_TILE + 5: return launch_tiles<E, 2, 2, 2, 2, 4>(a, stream);
+    case PRODUCT_TILE + 6: return launch_tiles<E, 4, 5, 2, 2, 2>(a, stream);
+    case PRODUCT_FEW_LINES: return launch_few_lines<E, 1>(a, stream);
+    case PRODUCT_FEW_LINES + 1: return launch_few_lines<E, 2>(a, stream);
+    case PRODUCT_FEW_LINES + 2: return launch_few_lines<E, 4>(a, stream);
+    case PRODUCT_FEW: return launch_few<E>(a, stream);
+    case PRODUCT_ROWS_128: return launch_tiles<E, 4, 4, 2, 2, 2, false>(a, stream);
+    case PRODUCT_ROWS_64: return launch_tiles<E, 2, 2, 2, 2, 2, false>(a, stream);
+    default: break;
+  }
+  const dim3 grid((a.d_out + kAnyTile - 1) / kAnyTile, (a.T + kAnyTile - 1) / kAnyTile);
+  product_any_kernel<E><<<grid, 256, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+ProductChoice choose_product(const ProductArgs &a) {
   const bool lines = aligned16(a.q) && aligned16(a.W) && a.ldq % 16 == 0 && a.ldw % 16 == 0 && a.d_in % 16 == 0;
   const bool near = a.ldq <= (1 << 22) && a.ldw <= (1 << 22);  // a tile's rows within 32-bit offsets
   double us = 0;
@@ -785,43 +821,14 @@ hipError_t launch_typed(const ProductArgs &args, hipStream_t stream) {
     // rounds of 256 x 256 tiles, 228 us instead of 243, through 4096 x 1024 62
     // instead of 71.
     const int first = split_rows(a, us);
-    if (first > 0) {
-      ProductArgs b = a;
-      b.T = first;
-      hipError_t e = launch_typed<E>(b, stream);
-      if (e != hipSuccess) return e;
-      b = a;
-      b.q += first * b.ldq;
-      b.q_scale += first;
-      b.y = static_cast<E *>(b.y) + first * b.ldy;
-      b.T -= first;
-      return launch_typed<E>(b, stream);
-    }
-    if (a.T <= 64 && cost_of_few(a) < us)
-      return a.T <= 16   ? launch_few_lines<E, 1>(a, stream)
-             : a.T <= 32 ? launch_few_lines<E, 2>(a, stream)
-                         : launch_few_lines<E, 4>(a, stream);
-    switch (tile) {
-      case 0: return launch_tiles<E, 8, 4, 2, 4, 2>(a, stream);
-      case 1: return launch_tiles<E, 6, 4, 2, 4, 2>(a, stream);
-      case 2: return launch_tiles<E, 4, 4, 2, 2, 2>(a, stream);
-      case 3: return launch_tiles<E, 4, 4, 2, 2, 4>(a, stream);
-      case 4: return launch_tiles<E, 4, 2, 2, 2, 4>(a, stream);
-      case 6: return launch_tiles<E, 4, 5, 2, 2, 2>(a, stream);
-      default: return launch_tiles<E, 2, 2, 2, 2, 4>(a, stream);
-    }
+    if (first > 0) return {PRODUCT_TILE + tile, first};
+    if (a.T <= 64 && cost_of_few(a) < us) return {PRODUCT_FEW_LINES + (a.T <= 16 ? 0 : a.T <= 32 ? 1 : 2), 0};
+    return {PRODUCT_TILE + tile, 0};
   }
-  if (a.d_in >= 16 && a.T <= 16) return launch_few<E>(a, stream);
-  if (a.d_in >= 16 && near) {
-    if (choose_tile(a, 1u << 2 | 1u << 5, us) == 2) return launch_tiles<E, 4, 4, 2, 2, 2, false>(a, stream);
-    return launch_tiles<E, 2, 2, 2, 2, 2, false>(a, stream);
-  }
-  const dim3 grid((a.d_out + kAnyTile - 1) / kAnyTile, (a.T + kAnyTile - 1) / kAnyTile);
-  product_any_kernel<E><<<grid, 256, 0, stream>>>(a);
-  return hipGetLastError();
+  if (a.d_in >= 16 && a.T <= 16) return {PRODUCT_FEW, 0};
+  if (a.d_in >= 16 && near) return {choose_tile(a, 1u << 2 | 1u << 5, us) == 2 ? PRODUCT_ROWS_128 : PRODUCT_ROWS_64, 0};
+  return {PRODUCT_ANY, 0};
 }
-
-}  // namespace
 
 hipError_t launch_product(const ProductArgs &args, int dtype, hipStream_t stream) {
   // what a launch may hold, at one thread for every 16 results at least

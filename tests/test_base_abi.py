@@ -322,3 +322,29 @@ def test_a_second_thread_never_sees_the_types_missing(monkeypatch):
         sys.settrace(old)
     assert len(seen) > 5 and seen[0] == (False, 0) and seen[-1] == (True, 2)
     assert all(types == 2 for module, types in seen if module)
+
+
+def product_kernels(lib, T, d_in, d_out):
+    """The kernels that a product of rows of whole 16s takes, in turn, and the rows at which it is split."""
+    first = ctypes.c_int32(-1)
+    k = lib.lora_base_product_choice(T, d_in, d_out, ctypes.c_int64(d_in), ctypes.c_int64(d_in), ctypes.byref(first))
+    if first.value == 0:
+        return [k], []
+    assert 0 < first.value < T
+    (a, ra), (b, rb) = (product_kernels(lib, n, d_in, d_out) for n in (first.value, T - first.value))
+    return a + b, [first.value, *ra, *(first.value + r for r in rb)]
+
+
+def test_gpu_cases_take_every_kernel_of_the_product(lib):
+    """Whatever costs the choice goes by: the sizes of the GPU tests take each tile shape, each kernel for few rows, each
+    one for other rows, and splits of either large shape with different kernels for the rest."""
+    import test_gpu_base as G
+    assert {k for s in G.TILES for k in product_kernels(lib, *s)[0]} >= set(range(7)) | {11, 12}
+    rest = set()
+    for s in G.SPLITS:
+        kernels, at = product_kernels(lib, *s)
+        assert at, s
+        rest.add((kernels[0], kernels[-1]))
+    assert {a for a, _ in rest} == {0, 1} and len(rest) >= 4
+    small = [(T, 512, 384) for T in (1, 17, 48)] + [(1, 17, 70), (100, 15, 70), (16, 65, 70)]
+    assert {k for s in small for k in product_kernels(lib, *s)[0]} == {7, 8, 9, 10, 13}

@@ -819,3 +819,29 @@ def test_rotary_angles_at_the_ends_of_the_positions(lo, hi):
     got = x.cpu().double()[:, 0]
     assert float((got[:, ::2] - torch.cos(w)).abs().max()) <= 1.4 * V
     assert float((got[:, 1::2] - torch.sin(w)).abs().max()) <= 1.4 * V
+
+
+# sizes that are split into whole rounds and a rest: of 256 x 256 tiles with each of three kernels behind, of 192 x 256
+SPLITS = [(13628, 592, 1826), (4135, 1296, 4039), (7751, 1168, 2062), (16997, 4096, 4096)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("T, d_in, d_out", TILES + SPLITS)
+def test_product_in_whole_lines(T, d_in, d_out, dtype):
+    """Every tile shape and the split launches, with rows of y that begin on whole 128-byte lines, where whole tiles
+    leave past the caches; against the float64 product on the GPU, the columns and rows beside y as they were."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    rand8 = lambda n: torch.randint(-127, 128, (n, d_in), generator=g, dtype=torch.int8, device=DEV)  # noqa: E731
+    q, W = rand8(T), rand8(d_out)
+    qs, ws, b = (torch.rand(n, generator=g, device=DEV) * 0.02 for n in (T, d_out, d_out))
+    line = 128 // torch.tensor([], dtype=dtype).element_size()
+    yb = torch.full((T + 1, (d_out + line - 1) // line * line), 7.0, dtype=dtype, device=DEV)
+    assert yb.data_ptr() % 128 == 0
+    L.lora_base_product(L.BaseWeight(W, ws, b), q, qs, yb[:T, :d_out])
+    for lo in range(0, T, 4096):
+        p = (q[lo:lo + 4096].double() @ W.double().T) * qs[lo:lo + 4096, None].double() * ws.double()
+        ref = p + b.double()
+        y = yb[lo:min(lo + 4096, T), :d_out].double()
+        bad = (y - ref).abs() > half(dtype) * ref.abs() + 4 * V * (p.abs() + b.double().abs())
+        assert not bool(bad.any()), (lo, int(bad.sum()), bad.nonzero()[:4].tolist())
+    assert bool((yb[T] == 7).all()) and bool((yb[:, d_out:] == 7).all())
