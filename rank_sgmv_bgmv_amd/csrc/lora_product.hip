@@ -644,46 +644,76 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void product_tile_kernel(ProductAr
     return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
   };
   const int o_lane = wm * MT * 16 + (kVec == 8 ? lane / 16 % 2 * 16 + lane / 32 * 8 : lane / 16 * 4);
-  auto store = [&](auto whole, auto by) {
-    constexpr int kStep = kVec / 4;
+  constexpr int kStep = kVec / 4, kLine = 2 * kStep;  // blocks of 64 bytes of a token, and of 128
+  // Block m of token block j (and kStep - 1 more), 64 bytes a token.
+  auto store_half = [&](int m, int j, float sx, auto by) {
+    E *y = static_cast<E *>(a.y) + (t0 + (wn * NT + j) * 16 + lane % 16) * a.ldy + o0;
+    store_vec<decltype(by)::value>(y + o_lane + m * 16, result(m, j, sx), kVec);
+  };
+  // ... and as many again, a line of eight tokens to each store.
+  const bool low = lane % 16 < 8;
+  auto store_line = [&](int m, int j, float sx, auto by) {
+    E *y = static_cast<E *>(a.y) + (t0 + (wn * NT + j) * 16 + lane % 8) * a.ldy + o0 + o_lane + (low ? 0 : kStep * 16);
+    const uint4 p = result(m, j, sx), q = result(m + kStep, j, sx);
+    auto move = [&](uint32_t of_p, uint32_t of_q) {
+      return uint32_t(__builtin_amdgcn_update_dpp(0, int(low ? of_q : of_p), 0x128, 0xf, 0xf, false));  // row_ror:8
+    };
+    const uint4 x = make_uint4(move(p.x, q.x), move(p.y, q.y), move(p.z, q.z), move(p.w, q.w));
+    store_vec<decltype(by)::value>(
+        y + m * 16, make_uint4(low ? p.x : x.x, low ? p.y : x.y, low ? p.z : x.z, low ? p.w : x.w), kVec);
+    store_vec<decltype(by)::value>(
+        y + 8 * a.ldy + m * 16, make_uint4(low ? x.x : q.x, low ? x.y : q.y, low ? x.z : q.z, low ? x.w : q.w), kVec);
+  };
+  // The blocks of a whole tile.  Where a wave's are no whole number of lines, one
+  // line is half its and half the next wave's.  The halves of a 192-channel tile
+  // still go past L2 with the rest, although memory then writes 1.04 to 1.1 times
+  // the results: 37709 rows through 384 x 576 17.9 us, 58400 through 1024 x 384
+  // 28.8; all as half lines, 1.3 times the results, 19.8 and 31.1; these halves
+  // through L2, not a byte too many, 17.6 and 32.3 (and 16741 through 128 x 576
+  // 7.9 against 7.1).  A 64-channel tile has nothing but halves: through L2, at
+  // the same time, 64 rows through 4096 x 14336 write 1792 KiB, not 2290.
+  auto store_whole = [&](auto first_half, auto by) {
+    constexpr bool kOdd = MT % kLine != 0, kFirst = kOdd && decltype(first_half)::value;
+    constexpr std::integral_constant<bool, decltype(by)::value && (MT > kStep)> by_half{};
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const float sx = s_t[(wn * NT + j) * 16 + lane % 16];
+      if constexpr (kFirst) store_half(0, j, sx, by_half);
+#pragma unroll
+      for (int m = kFirst ? kStep : 0; m + kLine <= MT; m += kLine) store_line(m, j, sx, by);
+      if constexpr (kOdd && !kFirst) store_half(MT - kStep, j, sx, by_half);
+    }
+  };
+  auto store_part = [&] {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int tt = (wn * NT + j) * 16 + lane % 16;
       const float sx = s_t[tt];
-      if constexpr (decltype(whole)::value && MT % (2 * kStep) == 0) {
-        const bool low = lane % 16 < 8;
-        E *y = static_cast<E *>(a.y) + (t0 + (wn * NT + j) * 16 + lane % 8) * a.ldy + o0 + o_lane + (low ? 0 : kStep * 16);
+      E *y = static_cast<E *>(a.y) + (t0 + tt) * a.ldy + o0;
 #pragma unroll
-        for (int m = 0; m < MT; m += 2 * kStep) {
-          const uint4 p = result(m, j, sx), q = result(m + kStep, j, sx);
-          auto move = [&](uint32_t of_p, uint32_t of_q) {
-            return uint32_t(__builtin_amdgcn_update_dpp(0, int(low ? of_q : of_p), 0x128, 0xf, 0xf, false));  // row_ror:8
-          };
-          const uint4 x = make_uint4(move(p.x, q.x), move(p.y, q.y), move(p.z, q.z), move(p.w, q.w));
-          store_vec<decltype(by)::value>(
-              y + m * 16, make_uint4(low ? p.x : x.x, low ? p.y : x.y, low ? p.z : x.z, low ? p.w : x.w), kVec);
-          store_vec<decltype(by)::value>(
-              y + 8 * a.ldy + m * 16, make_uint4(low ? x.x : q.x, low ? x.y : q.y, low ? x.z : q.z, low ? x.w : q.w), kVec);
-        }
-      } else {
-        E *y = static_cast<E *>(a.y) + (t0 + tt) * a.ldy + o0;
-#pragma unroll
-        for (int m = 0; m < MT; m += kStep) {
-          const int oo = o_lane + m * 16;
-          const uint4 out = result(m, j, sx);
-          if (whole || (tt < n_t && oo < n_o)) store_vec<decltype(by)::value>(y + oo, out, whole ? kVec : n_o - oo);
-        }
+      for (int m = 0; m < MT; m += kStep) {
+        const int oo = o_lane + m * 16;
+        const uint4 out = result(m, j, sx);
+        if (tt < n_t && oo < n_o) store_vec<false>(y + oo, out, n_o - oo);
       }
     }
   };
   if (n_o < S::kO || n_t < S::kT) {
-    store(std::false_type{}, std::false_type{});
-  } else if (a.y_by) {
+    store_part();
+    return;
+  }
+  auto store = [&](auto by) {
+    if (MT % kLine != 0 && wm % 2 != 0)
+      store_whole(std::true_type{}, by);
+    else
+      store_whole(std::false_type{}, by);
+  };
+  if (a.y_by) {
     asm volatile("");
-    store(std::true_type{}, std::true_type{});
+    store(std::true_type{});
     asm volatile("");  // the compiler would make one of this and what follows, with ordinary stores
   } else {
-    store(std::true_type{}, std::false_type{});
+    store(std::false_type{});
   }
 }
 
