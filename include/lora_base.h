@@ -39,6 +39,7 @@ extern "C" {
 /* Sums of d_in products of 8-bit integers are held in 32 bits: 2^14 * 131071 < 2^31. */
 #define LORA_MAX_BASE_D_IN 131071
 #define LORA_MAX_HEAD_DIM 1024
+#define LORA_MAX_HEADS 65535  /* of one tensor of lora_rotary_apply */
 
 /* Symmetric 8-bit quantisation of rows.  With a = max_c |x[t][c]|,
  *
@@ -129,7 +130,7 @@ typedef struct {
   void *dst;
   int64_t src_token, src_head;
   int64_t dst_token, dst_head;
-  int32_t n_heads;
+  int32_t n_heads;  /* 1 .. LORA_MAX_HEADS */
 } lora_rotary_slice;
 
 /* Rotates up to LORA_MAX_SLICES tensors (query and key heads) of the same

@@ -79,7 +79,7 @@ class lora_rotary_slice(ctypes.Structure):
 _pack_slice = struct.Struct("@PPqqqqi4x").pack  # a lora_rotary_slice's bytes
 
 LORA_ROTARY_PLAIN, LORA_ROTARY_LINEAR, LORA_ROTARY_BASE, LORA_ROTARY_PARTS = 0, 1, 2, 3
-LORA_MAX_SLICES = 8
+LORA_MAX_SLICES, LORA_MAX_HEADS = 8, 65535
 
 _lib = None
 
@@ -578,7 +578,7 @@ class Rotary:
 
 def lora_rotary_apply(rotary: Rotary, positions, src: Sequence, dst: Optional[Sequence] = None, inverse: bool = False):
     """Rotates the heads of src, up to 8 tensors [T][heads][head_dim] of the same tokens (any token and head
-    strides), into dst (in place by default).  positions int32 [T]; tokens of a negative position are skipped."""
+    strides, 1 to LORA_MAX_HEADS heads), into dst (in place by default).  positions int32 [T]; tokens of a negative position are skipped."""
     torch = _torch()
     what, index, D = "lora_rotary_apply", rotary.index, rotary.head_dim
     n, T = len(src), positions.shape[0] if positions.dim() else 0

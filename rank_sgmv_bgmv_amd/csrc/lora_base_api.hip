@@ -181,7 +181,7 @@ lora_status lora_rotary_apply(const lora_rotary *rotary, const int32_t *position
   std::memset(&a, 0, sizeof(a));
   for (int i = 0; i < n_slices; ++i) {
     const lora_rotary_slice &s = slices[i];
-    if (s.n_heads < 1 || s.n_heads > 65535) return LORA_ESHAPE;
+    if (s.n_heads < 1 || s.n_heads > LORA_MAX_HEADS) return LORA_ESHAPE;
     for (int64_t v : {s.src_token, s.src_head, s.dst_token, s.dst_head})
       if (v < 0 || !fits(n_tokens, v) || !fits(s.n_heads, v)) return LORA_ESHAPE;
     a.s[i] = s;

@@ -348,3 +348,14 @@ def test_gpu_cases_take_every_kernel_of_the_product(lib):
     assert {a for a, _ in rest} == {0, 1} and len(rest) >= 4
     small = [(T, 512, 384) for T in (1, 17, 48)] + [(1, 17, 70), (100, 15, 70), (16, 65, 70)]
     assert {k for s in small for k in product_kernels(lib, *s)[0]} == {7, 8, 9, 10, 13}
+
+
+def test_most_heads_of_a_slice(lib):
+    """The limit on a slice's heads is the header's, and the binding's: one more is refused."""
+    text = open(os.path.join(ROOT, "include", "lora_base.h")).read()
+    most = int(re.search(r"#define\s+LORA_MAX_HEADS\s+(\d+)", text).group(1))
+    assert most == L.LORA_MAX_HEADS
+    assert re.search(r"int32_t n_heads;\s*/\*.*LORA_MAX_HEADS", text)
+    wide = dict(src_token=(most + 1) * 64, dst_token=(most + 1) * 64)
+    assert rotary(lib, [heads(n_heads=most + 1, **wide)], T=0) == ESHAPE
+    assert rotary(lib, [heads(n_heads=most, **wide)], T=0) == 0
