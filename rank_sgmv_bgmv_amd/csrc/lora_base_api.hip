@@ -43,8 +43,8 @@ lora_status check_y(const lora_base_weight *w, int32_t n_tokens, const void *y, 
 }
 
 // The quantised rows of lora_base_apply in its workspace: rows of d_in bytes
-// at a pitch of whole 16s (so that the product's 16-byte loads apply whatever
-// d_in is), then a scale for each row.
+// at a pitch of whole 16s, as the product's kernels for aligned rows need it
+// where d_in and the weight's rows are whole 16s too, then a scale for each row.
 struct BaseLayout {
   int64_t pitch;
   size_t scale, total;

@@ -735,12 +735,12 @@ hipError_t launch_tiles(const ProductArgs &a, hipStream_t stream) {
 // tiles move the fewest bytes for each product, small ones fill more CUs.
 // Measured, with the shapes in their order here:
 //                              256x256 192x256 128x128 128x128 128x64 64x64 128x160
-//   512 rows,  4096 -> 4096       39.9    33.6    22.1    17.0   12.5  14.2    23.3
-//   512 rows,  4096 -> 14336      40.3    34.0    28.6    34.5   43.5  45.5    35.2
-//   2304 rows, 4096 -> 4096       41.7    36.5    49.8    49.8   54.9  58.2    37.4
-//   2304 rows, 14336 -> 4096       153     138     174     157    172   201     121
-//   2304 rows, 4096 -> 14336       101     117     116     144    175   195     127
-//   16997 rows, 4096 -> 4096       247     252     261     309    381   412     255
+//   512 rows,  4096 -> 4096       39.8    34.0    22.7    18.1   13.0  16.2    24.0
+//   512 rows,  4096 -> 14336      40.4    34.0    28.9    34.8   43.1  44.5    35.7
+//   2304 rows, 4096 -> 4096       40.6    35.6    49.3    50.5   55.2  58.2    37.5
+//   2304 rows, 14336 -> 4096       157     141     175     157    173   202     121
+//   2304 rows, 4096 -> 14336       100     113     118     142    178   202     125
+//   16997 rows, 4096 -> 4096       239     242     258     299    376   424     251
 struct TileCost {
   int o, t, at_once;
   float alone, full, once;  // per stage, per stage with a full CU, per tile
@@ -864,20 +864,12 @@ hipError_t launch_product(const ProductArgs &args, int dtype, hipStream_t stream
   // what a launch may hold, at one thread for every 16 results at least
   constexpr int kMostT = 1 << 18, kMostO = 1 << 17;
   const int64_t eb = dtype == LORA_BF16 ? 2 : 4;
-  // Results beyond what the L2s hold (4 MiB on each of 8 XCDs) pass them by, and
-  // the operands that other tiles share stay in: 65536 rows through 1280 x 1280
-  // 127 -> 115 us, through 640 x 640 51 -> 42, 16997 rows through 4096 x 4096
-  // 245 -> 232.  Not where rows begin inside a line, which would go out in parts
-  // (65536 x 1280 through 1283 channels 168 -> 202), and not with few products
-  // for a byte of results, when the writing is most of the work (17000 rows
-  // through 4096 x 256 46 -> 48, x 512 64 -> 58; fp32 x 512 84 -> 87, x 1024
-  // 121 -> 114).  Smaller results stay near for what reads them next.
   // Results pass L2 by where every row begins on a whole line, and the operands
   // that other tiles share stay in: 65536 rows through 1280 x 1280 128 -> 105 us,
   // through 640 x 128 26 -> 20, 2304 rows through 14336 x 4096 112 -> 105, 1024
-  // rows through 4096 x 4096 19.8 -> 19.0; fewer take the same, and so does
-  // what reads them next.  Rows that begin inside a line would go out in parts
-  // (65536 x 1280 through 1283 channels 168 -> 202).
+  // rows through 4096 x 4096 19.8 -> 19.0; fewer take the same.  Rows that begin
+  // inside a line would go out in parts (65536 x 1280 through 1283 channels 168
+  // -> 202).
   const int y_by = reinterpret_cast<uintptr_t>(args.y) % 128 == 0 && args.ldy * eb % 128 == 0;
   for (int64_t t = 0; t < args.T; t += kMostT)
     for (int64_t o = 0; o < args.d_out; o += kMostO) {
