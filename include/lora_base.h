@@ -111,8 +111,8 @@ lora_status lora_base_apply(const lora_base_weight *weight, const void *x, int64
  *
  * or with `inverse` the same with -w (the gradient of the first form; for m =
  * 1 also its inverse).  The other values of a head are left as they are.
- * Angles are computed in float64, so that far positions keep theirs; the rest
- * in float32, rounded once. */
+ * Angles, m cos w and m sin w are computed in float64, for any position and
+ * angles up to 2^50, and rounded to float32; the rest in float32, rounded once. */
 typedef struct {
   const double *freq;   /* [rot_dim / 2], radians per position */
   int32_t head_dim;     /* 1 .. LORA_MAX_HEAD_DIM */

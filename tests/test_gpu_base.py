@@ -801,11 +801,10 @@ PI = fractions.Fraction(31415926535897932384626433832795028841971693993751058209
 
 @pytest.mark.parametrize("lo, hi", [(0, 1000), (1 << 30, (1 << 31) - 1)])
 def test_rotary_angles_at_the_ends_of_the_positions(lo, hi):
-    """Pairs (1, 0) give cosine and sine themselves: no rounding follows them.  With the angle reduced exactly here, w
-    below pi / 4 is off by v / 2 as a float32 (what float64 leaves out, 2^31 by 2^-104, is nothing beside it).
-    Cosine: v / 2 of that times sin w (0.36 v), the last rounding v / 2, w^2 / 2 by one rounding and its factor by a
-    quarter (0.31 + 0.16 v), as sums of the worst: below 1.4 v.  Sine: cos w (0.44 v where w is that far off), v / 2,
-    w^3 / 6 by three roundings (0.25 v): below 1.2 v."""
+    """Pairs (1, 0) give cosine and sine themselves: no rounding follows them.  The angle is reduced exactly here.  One
+    that is off by v / 2, as a float32 below pi / 4 is, and a float32 series end below 1.4 v for cosine (v / 2 of the
+    angle times sin w, the last rounding v / 2, w^2 / 2 by one rounding and its factor by a quarter) and below 1.2 v
+    for sine (cos w times v / 2, v / 2, w^3 / 6 by three roundings)."""
     rot, T = 32, 400
     freq = L.lora_rotary_frequencies(rot)
     pos = torch.from_numpy(np.random.default_rng(7).integers(lo, hi, T)).int()
@@ -845,3 +844,24 @@ def test_product_in_whole_lines(T, d_in, d_out, dtype):
         bad = (y - ref).abs() > half(dtype) * ref.abs() + 4 * V * (p.abs() + b.double().abs())
         assert not bool(bad.any()), (lo, int(bad.sum()), bad.nonzero()[:4].tolist())
     assert bool((yb[T] == 7).all()) and bool((yb[:, d_out:] == 7).all())
+
+
+@pytest.mark.parametrize("m", [1.0, 1.2])
+@pytest.mark.parametrize("hi", [1000, 1000000, (1 << 31) - 1])
+def test_rotary_cosine_and_sine_are_rounded_once(hi, m):
+    """Pairs (1, 0) give m cos w and m sin w, within half a float32 step of numbers below 2^k, 2^k v / 2, and the 2e-9 at
+    which the series end (0.03 v).  The angles are reduced exactly here; m is the float32 that the call gets."""
+    rot, T = 32, 400
+    freq = L.lora_rotary_frequencies(rot)
+    pos = torch.from_numpy(np.random.default_rng(9).integers(hi // 2, hi, T)).int()
+    x = torch.zeros(T, 1, rot)
+    x[..., ::2] = 1
+    x = x.to(DEV)
+    L.lora_rotary_apply(L.Rotary(freq.to(DEV), rot, interleaved=True, mscale=m), pos.to(DEV), [x])
+    turns = [[fractions.Fraction(p) * fractions.Fraction(f) / (2 * PI) for f in freq.tolist()] for p in pos.tolist()]
+    w = torch.tensor([[float((t - round(t)) * 2 * PI) for t in row] for row in turns], dtype=torch.float64)
+    got = x.cpu().double()[:, 0]
+    for v, ref in ((got[:, ::2], torch.cos(w)), (got[:, 1::2], torch.sin(w))):
+        ref = ref * float(np.float32(m))
+        step = torch.where(ref.abs() < 1 - V, 1.0, 2.0)  # values from 1 to 2 have steps of 2 v
+        assert bool(((v - ref).abs() <= (0.5 * step + 0.03 * m) * V).all()), float(((v - ref).abs() / step).max() / V)
