@@ -494,16 +494,17 @@ def lora_quantize_rows(x, q, scale):
     what, index = "lora_quantize_rows", x.get_device()
     code = _REAL.get(x.dtype, -1)
     ldx, ldq = _row(x, x.dtype, index), _row(q, torch.int8, index)
-    if (index < 0 or code < 0 or ldx == 0 or ldq == 0 or x.shape != q.shape or ldx < x.shape[1] or ldq < x.shape[1]
-            or not _line(scale, torch.float32, index, x.shape[0])):
+    T, d = x.shape if ldx else (0, 0)
+    if (index < 0 or code < 0 or ldx == 0 or ldx < d or ldq == 0 or ldq < d or q.shape != (T, d) or T > _INT32_MAX
+            or d > _INT32_MAX or not _line(scale, torch.float32, index, T)):
         dev = x.device
         if x.dim() != 2 or q.dim() != 2 or x.shape != q.shape:
             raise LoraError(-2, f"{what}: x and q must be of one shape [T][d]")
         ldx = _rows_2d(what, "x", x, _REAL, dev, 1)
         ldq = _rows_2d(what, "q", q, (torch.int8,), dev, 1)
-        _vector(what, "scale", scale, torch.float32, dev, x.shape[0])
-    T, d = x.shape
-    _fits_32(what, T, d)
+        T, d = x.shape
+        _vector(what, "scale", scale, torch.float32, dev, T)
+        _fits_32(what, T, d)
     _launch(index, what, lib().lora_quantize_rows, x.data_ptr(), ldx, code, T, d, q.data_ptr(), ldq, scale.data_ptr())
 
 
@@ -516,7 +517,7 @@ def lora_base_product(weight: BaseWeight, q, q_scale, y):
     ldq, ldy = _row(q, torch.int8, index), _row(y, y.dtype, index)
     T = q.shape[0] if ldq else 0
     if (code < 0 or ldq < d_in or ldy < weight.d_out or q.shape[1] != d_in or y.shape[0] < T or y.shape[1] < weight.d_out
-            or not _line(q_scale, torch.float32, index, T)):
+            or T > _INT32_MAX or not _line(q_scale, torch.float32, index, T)):
         dev = weight.device
         ldq = _rows_2d(what, "q", q, (torch.int8,), dev, d_in)
         T = q.shape[0]
@@ -524,7 +525,7 @@ def lora_base_product(weight: BaseWeight, q, q_scale, y):
             raise LoraError(-2, f"{what}: q must be [T][{d_in}]")
         ldy = _rows_2d(what, "y", y, _REAL, dev, weight.d_out, T)
         _vector(what, "q_scale", q_scale, torch.float32, dev, T)
-    _fits_32(what, T)
+        _fits_32(what, T)
     _launch(index, what, lib().lora_base_product, weight.ref, q.data_ptr(), ldq, q_scale.data_ptr(), T, y.data_ptr(), ldy,
             code)
 
@@ -548,7 +549,7 @@ def lora_base_apply(weight: BaseWeight, x, y, ws):
     ldx, ldy = _row(x, x.dtype, index), _row(y, x.dtype, index)
     T = x.shape[0] if ldx else 0
     if (code < 0 or ldx < d_in or ldy < weight.d_out or x.shape[1] != d_in or y.shape[0] < T or y.shape[1] < weight.d_out
-            or not _line(ws, torch.uint8, index, 0)):
+            or T > _INT32_MAX or not _line(ws, torch.uint8, index, 0)):
         dev = weight.device
         ldx = _rows_2d(what, "x", x, _REAL, dev, d_in)
         T = x.shape[0]
@@ -556,7 +557,7 @@ def lora_base_apply(weight: BaseWeight, x, y, ws):
             raise LoraError(-2, f"{what}: x must be [T][{d_in}]")
         ldy = _rows_2d(what, "y", y, (x.dtype,), dev, weight.d_out, T)
         _vector(what, "ws", ws, torch.uint8, dev, 0)
-    _fits_32(what, T)
+        _fits_32(what, T)
     _launch(index, what, lib().lora_base_apply, weight.ref, x.data_ptr(), ldx, T, y.data_ptr(), ldy, code, ws.data_ptr(),
             ws.shape[0])
 
@@ -584,8 +585,9 @@ def lora_rotary_apply(rotary: Rotary, positions, src: Sequence, dst: Optional[Se
     n, T = len(src), positions.shape[0] if positions.dim() else 0
     if not 1 <= n <= LORA_MAX_SLICES or (dst is not None and len(dst) != n):
         raise LoraError(-2, f"{what}: 1 to {LORA_MAX_SLICES} tensors, as many in dst as in src")
-    if not _line(positions, torch.int32, index, T):
+    if T > _INT32_MAX or not _line(positions, torch.int32, index, T):
         _vector(what, "positions", positions, torch.int32, rotary.device, T)
+        _fits_32(what, T)
     dtype = src[0].dtype
     code = _REAL.get(dtype, -1)
     if code < 0:
@@ -605,7 +607,8 @@ def lora_rotary_apply(rotary: Rotary, positions, src: Sequence, dst: Optional[Se
             if b.dtype is not dtype or b.get_device() != index or b.shape != shape or (sb[2] != 1 and D > 1):
                 raise LoraError(-2, f"{what}: dst must be like src (got {b.dtype} {tuple(b.shape)} on {b.device}, "
                                     f"strides {sb})")
-        _fits_32(what, T, shape[1])
+        if shape[1] > _INT32_MAX:
+            _fits_32(what, shape[1])
         slices += _pack_slice(pa, pb, sa[0], sa[1], sb[0], sb[1], shape[1])
     _launch(index, what, lib().lora_rotary_apply, rotary.ref, positions.data_ptr(), T, n, slices, code, 1 if inverse else 0)
 
