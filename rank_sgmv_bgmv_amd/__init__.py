@@ -12,6 +12,9 @@ Functions carry the C names:
   lora_apply_multi, lora_apply_sliced, lora_read_device_errors, lora_status_string,
   the operators around a LoRA layer (include/lora_base.h): lora_quantize_rows, lora_base_product, lora_base_apply,
   lora_base_workspace_size, lora_rotary_apply, lora_rotary_frequencies,
+  the norm, the 8-bit cache and attention over it (include/lora_layer.h): lora_norm_apply, lora_cache_pitch,
+  lora_cache_write, lora_cache_read, lora_attention_plan_size, lora_attention_workspace_size, lora_attention_plan,
+  lora_attention_apply,
   and the measurement aids lora_calib_gather_read and lora_calib_tile_stream
   (include/lora_calib.h).
 
@@ -78,6 +81,35 @@ class lora_rotary_slice(ctypes.Structure):
 
 _pack_slice = struct.Struct("@PPqqqqi4x").pack  # a lora_rotary_slice's bytes
 
+
+class lora_norm(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("eps", ctypes.c_double), ("d", ctypes.c_int32)]
+
+
+class lora_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_page", ctypes.c_int64), ("v_page", ctypes.c_int64), ("k_scale_page", ctypes.c_int64),
+                ("v_scale_page", ctypes.c_int64), ("n_pages", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class lora_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+_pack_heads = struct.Struct("@Pqq").pack  # a lora_heads' bytes
+
+
+class lora_attention(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+class lora_attention_batch(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int32), ("n_seqs", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("q_off", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("pages", ctypes.c_void_p), ("ld_pages", ctypes.c_int64), ("tree", ctypes.c_void_p)]
+
 LORA_ROTARY_PLAIN, LORA_ROTARY_LINEAR, LORA_ROTARY_BASE, LORA_ROTARY_PARTS = 0, 1, 2, 3
 LORA_MAX_SLICES, LORA_MAX_HEADS = 8, 65535
 
@@ -117,6 +149,14 @@ def lib() -> ctypes.CDLL:
             "lora_base_apply": (ctypes.c_int, [P, P, I64, I32, P, I64, ctypes.c_int, P, SZ, P]),
             "lora_rotary_apply": (ctypes.c_int, [P, P, I32, I32, P, ctypes.c_int, I32, P]),
             "lora_rotary_frequencies": (ctypes.c_int, [ctypes.c_int, ctypes.c_double, I32] + [ctypes.c_double] * 4 + [P]),
+            "lora_norm_apply": (ctypes.c_int, [P, P, I64, P, I64, P, I64, P, I64, P, I64, P, I32, ctypes.c_int, P]),
+            "lora_cache_pitch": (I32, [I32]),
+            "lora_cache_write": (ctypes.c_int, [P, P, I32, P, P, ctypes.c_int, P]),
+            "lora_cache_read": (ctypes.c_int, [P, P, I32, P, P, ctypes.c_int, P]),
+            "lora_attention_plan_size": (SZ, [P, P, P]),
+            "lora_attention_workspace_size": (SZ, [P, P, P]),
+            "lora_attention_plan": (ctypes.c_int, [P, P, P, P, SZ, P]),
+            "lora_attention_apply": (ctypes.c_int, [P, P, P, P, SZ, P, P, P, SZ, P]),
             "lora_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "lora_abi_version": (I32, []),
         }
@@ -622,6 +662,225 @@ def lora_rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = 
                                          float(low), float(high), _ptr(freq) if freq.numel() else None),
            "lora_rotary_frequencies")
     return freq
+
+
+# ---------------------- before and behind it: norm, cache, attention (lora_layer.h) --
+class Norm:
+    """A root-mean-square norm (lora_norm): weight float32 [d] on the device, and what is added to the mean square."""
+
+    def __init__(self, weight, eps: float):
+        if weight.device.type != "cuda":
+            raise LoraError(-1, "Norm: weight must be in device memory")
+        if weight.dim() != 1 or weight.shape[0] < 1:
+            raise LoraError(-2, "Norm: weight must be [d]")
+        _vector("Norm", "weight", weight, _torch().float32, weight.device, weight.shape[0])
+        _fits_32("Norm", weight.shape[0])
+        self.weight, self.device, self.d, self.eps = weight, weight.device, int(weight.shape[0]), float(eps)
+        self.c = lora_norm(_ptr(weight), self.eps, self.d)
+        self.ref, self.index = ctypes.addressof(self.c), weight.get_device()
+
+
+def lora_norm_apply(norm: Norm, x, y=None, q=None, scale=None, residual=None, total=None):
+    """h = x + residual (x without one), kept in total if given; y = h weight / sqrt(mean h^2 + eps), kept in y if given;
+    the rows of y in 8 bits in q and scale if given (lora_quantize_rows).  x, residual, total, y [T][d] of one type
+    (bfloat16 or float32), q int8 [T][d], scale float32 [T]; y or q or both.  total may be x or residual, y may be x."""
+    what, index, d = "lora_norm_apply", norm.index, norm.d
+    dtype = x.dtype
+    code = _REAL.get(dtype, -1) if _torch() else -1
+    if code < 0:
+        raise LoraError(-2, f"{what}: x must be bfloat16 or float32 (got {dtype})")
+    ldx = _row(x, dtype, index)
+    if ldx < d or x.shape[1] != d:
+        ldx = _rows_2d(what, "x", x, (dtype,), norm.device, d)
+    T = x.shape[0]
+    if x.shape[1] != d:
+        raise LoraError(-2, f"{what}: x must be [T][{d}]")
+    if T > _INT32_MAX:
+        _fits_32(what, T)
+    args = [x.data_ptr(), ldx]
+    for name, t, kind in (("residual", residual, dtype), ("total", total, dtype), ("y", y, dtype),
+                          ("q", q, _torch().int8)):
+        if t is None:
+            args += (None, 0)
+            continue
+        ld = _row(t, kind, index)
+        if ld < d or t.shape[1] != d or t.shape[0] != T:
+            if t.dim() != 2 or tuple(t.shape) != (T, d):
+                raise LoraError(-2, f"{what}: {name} must be [{T}][{d}] (got {tuple(t.shape)})")
+            ld = _rows_2d(what, name, t, (kind,), norm.device, d, T)
+        args += (t.data_ptr(), ld)
+    if scale is not None and not _line(scale, _torch().float32, index, T):
+        _vector(what, "scale", scale, _torch().float32, norm.device, T)
+    _launch(index, what, lib().lora_norm_apply, norm.ref, *args, None if scale is None else scale.data_ptr(), T, code)
+
+
+def lora_cache_pitch(head_dim: int) -> int:
+    """Bytes of a row of a cache."""
+    _fits_32("lora_cache_pitch", head_dim)
+    return int(lib().lora_cache_pitch(max(int(head_dim), 0)))
+
+
+class Cache:
+    """A cache of keys and values in 8 bits (lora_cache): k, v int8 [n_pages][heads][page_size][pitch], k_scale, v_scale
+    float32 [n_pages][heads][page_size], each page contiguous (pages may lie further apart).  Keeps the tensors alive."""
+
+    def __init__(self, k, v, k_scale, v_scale, head_dim: int):
+        torch = _torch()
+        pitch = lora_cache_pitch(head_dim)
+        if pitch == 0:
+            raise LoraError(-2, f"Cache: no head_dim {head_dim}")
+        if k.dim() != 4 or k.shape[3] != pitch or k.device.type != "cuda":
+            raise LoraError(-2, f"Cache: k must be int8 [n_pages][heads][page_size][{pitch}] in device memory")
+        n, heads, page, _ = k.shape
+        _fits_32("Cache", n, max(heads, page))
+        for name, t, dtype, shape, inner in (("k", k, torch.int8, k.shape, (page * pitch, pitch, 1)),
+                                             ("v", v, torch.int8, k.shape, (page * pitch, pitch, 1)),
+                                             ("k_scale", k_scale, torch.float32, k.shape[:3], (page, 1)),
+                                             ("v_scale", v_scale, torch.float32, k.shape[:3], (page, 1))):
+            if t.dtype != dtype or t.shape != shape or t.device != k.device or any(
+                    s != w for s, w, m in zip(t.stride()[1:], inner, shape[1:]) if m > 1):
+                raise LoraError(-2, f"Cache: {name} must be {dtype} {list(shape)} on {k.device}, each page contiguous "
+                                    f"(got {t.dtype} {list(t.shape)} on {t.device}, strides {t.stride()})")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device, self.n_pages, self.heads, self.page_size, self.head_dim = k.device, int(n), int(heads), int(page), int(head_dim)
+        self.c = lora_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), k.stride(0), v.stride(0), k_scale.stride(0),
+                            v_scale.stride(0), self.n_pages, self.heads, self.page_size, self.head_dim)
+        self.ref, self.index = ctypes.addressof(self.c), k.get_device()
+
+
+def new_cache(n_pages: int, heads: int, page_size: int, head_dim: int, device) -> Cache:
+    """An empty cache (zeros) of these sizes."""
+    torch = _torch()
+    shape = (n_pages, heads, page_size)
+    k, v = (torch.zeros(*shape, lora_cache_pitch(head_dim), dtype=torch.int8, device=device) for _ in range(2))
+    return Cache(k, v, torch.zeros(shape, device=device), torch.zeros(shape, device=device), head_dim)
+
+
+def _head_bytes(what: str, name: str, t, dtype, index: int, T: int, heads: int, d: int) -> bytes:
+    """A tensor [T][heads][d] with a head's values side by side, as the bytes of a lora_heads."""
+    shape, s = t.shape, t.stride()
+    if (t.dtype is not dtype or t.get_device() != index or len(shape) != 3 or shape[0] != T or shape[1] != heads
+            or shape[2] != d or (s[2] != 1 and d > 1)):
+        raise LoraError(-2, f"{what}: {name} must be {dtype} [{T}][{heads}][{d}] on device {index}, a head's values side "
+                            f"by side (got {t.dtype} {tuple(shape)} on {t.device}, strides {s})")
+    return _pack_heads(t.data_ptr(), s[0], s[1])
+
+
+def _cache_call(what: str, f, cache: Cache, slots, k, v):
+    torch = _torch()
+    T = slots.shape[0] if slots.dim() else 0
+    if T > _INT32_MAX or not _line(slots, torch.int32, cache.index, T):
+        _vector(what, "slots", slots, torch.int32, cache.device, T)
+        _fits_32(what, T)
+    code = _REAL.get(k.dtype, -1)
+    if code < 0:
+        raise LoraError(-2, f"{what}: k and v must be bfloat16 or float32 (got {k.dtype})")
+    kb = _head_bytes(what, "k", k, k.dtype, cache.index, T, cache.heads, cache.head_dim)
+    vb = _head_bytes(what, "v", v, k.dtype, cache.index, T, cache.heads, cache.head_dim)
+    _launch(cache.index, what, f, cache.ref, slots.data_ptr(), T, kb, vb, code)
+
+
+def lora_cache_write(cache: Cache, slots, k, v):
+    """Writes the heads k, v [T][heads][head_dim] (bfloat16 or float32, any token and head strides) of T tokens to their
+    slots int32 [T] in 8 bits; a token of a negative slot, or one beyond the cache, is skipped.  Slots must differ."""
+    _cache_call("lora_cache_write", lib().lora_cache_write, cache, slots, k, v)
+
+
+def lora_cache_read(cache: Cache, slots, k, v):
+    """Reads the heads at slots int32 [T] back into k, v [T][heads][head_dim]; tokens of slots that are not in the cache
+    are left as they were."""
+    _cache_call("lora_cache_read", lib().lora_cache_read, cache, slots, k, v)
+
+
+class Attention:
+    """Attention of one kind of layer (lora_attention): query heads (a multiple of the cache's), the factor of the
+    scores (> 0), keys that a query sees (0: all before it), first keys that stay visible, the type of q and out."""
+
+    def __init__(self, heads: int, scale: float, window: int = 0, sinks: int = 0, dtype=None):
+        torch = _torch()
+        self.dtype = torch.bfloat16 if dtype is None else dtype
+        if self.dtype not in _REAL:
+            raise LoraError(-2, f"Attention: dtype must be bfloat16 or float32 (got {self.dtype})")
+        _fits_32("Attention", max(heads, window), sinks)
+        self.heads = int(heads)
+        self.c = lora_attention(self.heads, int(window), int(sinks), float(scale), _REAL[self.dtype])
+        self.ref = ctypes.addressof(self.c)
+
+
+class AttentionBatch:
+    """The sequences of a step (lora_attention_batch): q_off int32 [S + 1], the rows of each sequence's queries, which
+    are its last tokens; lens int32 [S], its keys in the cache; pages int32 [S][max_pages]; max_q, queries of a sequence
+    at most.  tree: int64 (or uint64) [n_tokens], for drafted tokens the bits of those that each sees.  Keeps them alive."""
+
+    def __init__(self, n_tokens: int, q_off, lens, pages, max_q: int, tree=None):
+        torch, what = _torch(), "AttentionBatch"
+        if pages.dim() != 2 or pages.dtype != torch.int32 or pages.device.type != "cuda" or pages.shape[1] < 1 or (
+                pages.shape[1] > 1 and pages.stride(1) != 1):
+            raise LoraError(-2, f"{what}: pages must be int32 [S][max_pages] in device memory, rows contiguous")
+        S, dev = pages.shape[0], pages.device
+        _fits_32(what, max(S, pages.shape[1]), max(n_tokens, max_q))
+        _vector(what, "q_off", q_off, torch.int32, dev, S + 1)
+        _vector(what, "lens", lens, torch.int32, dev, S)
+        if tree is not None:
+            _vector(what, "tree", tree, torch.uint64 if tree.dtype == torch.uint64 else torch.int64, dev, n_tokens)
+        self.q_off, self.lens, self.pages, self.tree, self.device, self.T = q_off, lens, pages, tree, dev, int(n_tokens)
+        ld = int(pages.stride(0)) if S > 1 else int(pages.shape[1])
+        self.c = lora_attention_batch(self.T, int(S), int(max_q), int(pages.shape[1]), _ptr(q_off), _ptr(lens),
+                                      _ptr(pages), ld, _ptr(tree))
+        self.ref, self.index = ctypes.addressof(self.c), pages.get_device()
+
+
+def _attention_size(what: str, f, attention: Attention, cache: Cache, batch: AttentionBatch) -> int:
+    n = int(f(attention.ref, cache.ref, batch.ref))
+    if n == 0:
+        raise LoraError(-2, f"{what}: attention, cache and batch do not fit each other")
+    return n
+
+
+def lora_attention_plan_size(attention: Attention, cache: Cache, batch: AttentionBatch) -> int:
+    return _attention_size("lora_attention_plan_size", lib().lora_attention_plan_size, attention, cache, batch)
+
+
+def lora_attention_workspace_size(attention: Attention, cache: Cache, batch: AttentionBatch) -> int:
+    return _attention_size("lora_attention_workspace_size", lib().lora_attention_workspace_size, attention, cache, batch)
+
+
+def new_attention_plan(attention: Attention, cache: Cache, batch: AttentionBatch):
+    """Memory for the plan of batches of these sizes."""
+    torch = _torch()
+    return torch.empty(lora_attention_plan_size(attention, cache, batch), dtype=torch.uint8, device=batch.device)
+
+
+def new_attention_workspace(attention: Attention, cache: Cache, batch: AttentionBatch):
+    """A workspace for lora_attention_apply on batches of these sizes."""
+    torch = _torch()
+    return torch.empty(lora_attention_workspace_size(attention, cache, batch), dtype=torch.uint8, device=batch.device)
+
+
+def lora_attention_plan(attention: Attention, cache: Cache, batch: AttentionBatch, plan):
+    """Cuts a step's work into pieces, from q_off and lens: once a step, for every layer of this window, these sinks and
+    heads."""
+    what, torch = "lora_attention_plan", _torch()
+    if not _line(plan, torch.uint8, batch.index, 0):
+        _vector(what, "plan", plan, torch.uint8, batch.device, 0)
+    _launch(batch.index, what, lib().lora_attention_plan, attention.ref, cache.ref, batch.ref, plan.data_ptr(), plan.shape[0])
+
+
+def lora_attention_apply(attention: Attention, cache: Cache, batch: AttentionBatch, plan, q, out, ws):
+    """out = softmax(scale q k^T) v over the keys in the cache that each query sees (include/lora_layer.h): q, out
+    [n_tokens][heads][head_dim] of the attention's type (any token and head strides; out may be q), a plan of
+    lora_attention_plan for this batch, a workspace of new_attention_workspace."""
+    torch, what, index = _torch(), "lora_attention_apply", batch.index
+    if cache.index != index:
+        raise LoraError(-1, f"{what}: every tensor must be on {batch.device} (the cache is on {cache.device})")
+    for name, t in (("plan", plan), ("ws", ws)):
+        if not _line(t, torch.uint8, index, 0):
+            _vector(what, name, t, torch.uint8, batch.device, 0)
+    T, heads, d = batch.T, attention.heads, cache.head_dim
+    qb = _head_bytes(what, "q", q, attention.dtype, index, T, heads, d)
+    ob = _head_bytes(what, "out", out, attention.dtype, index, T, heads, d)
+    _launch(index, what, lib().lora_attention_apply, attention.ref, cache.ref, batch.ref, plan.data_ptr(), plan.shape[0], qb,
+            ob, ws.data_ptr(), ws.shape[0])
 
 
 def lora_read_device_errors(plan) -> int:

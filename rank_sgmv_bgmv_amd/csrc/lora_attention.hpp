@@ -1,0 +1,220 @@
+// Device helpers shared by the attention kernels: 8-bit values as float16,
+// swaps between the quarters of a wave, the walk over a plan's items, masks.
+#pragma once
+
+#include "lora_device.hpp"
+#include "lora_layer.hpp"
+
+namespace lora {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kNoScore = -3.0e38f;  // the running maximum before the first key
+constexpr int kNever = 0x7fffffff;
+
+// Two bytes of u (8-bit values plus 128, so 0 .. 255) as float16, (u - 128) /
+// 512 each.  The bytes are taken as the float16 numbers u * 2^-24 that their
+// bits are; one fused multiply-add moves and shifts them, with no rounding.
+__device__ __forceinline__ f16x2 bytes_to_f16(uint32_t halves) {
+  const f16x2 up = {_Float16(32768.f), _Float16(32768.f)}, off = {_Float16(-0.25f), _Float16(-0.25f)};
+  return __builtin_elementwise_fma(__builtin_bit_cast(f16x2, halves), up, off);
+}
+constexpr uint32_t kByteBias = 0x80808080u;
+constexpr float kByteScale = 512.f;
+
+// Two floats as float16, to the nearest.
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const f32x2 f = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
+}
+
+__device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  const uint4 u = make_uint4(a, b, c, d);
+  return __builtin_bit_cast(f16x8, u);
+}
+
+// v of the lane 32, and 16, away.
+__device__ __forceinline__ float other_half(float v) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(threadIdx.x & 32 ? s[0] : s[1]);
+}
+__device__ __forceinline__ float other_quarter(float v) {
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(threadIdx.x & 16 ? s[0] : s[1]);
+}
+// over the lanes l, l ^ 32 (and the four l ^ 16, l ^ 32, l ^ 48)
+__device__ __forceinline__ float half_max(float v) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+__device__ __forceinline__ float quarters_max(float v) {
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return half_max(fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])));
+}
+__device__ __forceinline__ float quarters_sum(float v) {
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return half_sum(__uint_as_float(s[0]) + __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float wave_max_f(float v) {
+#define LORA_ROR(n) \
+  v = fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), 0x120 + (n), 0xf, 0xf, false)))
+  LORA_ROR(1);
+  LORA_ROR(2);
+  LORA_ROR(4);
+  LORA_ROR(8);
+#undef LORA_ROR
+  return quarters_max(v);
+}
+
+// An exponent e with |v| in [2^(e-1), 2^e), held to -60 .. 100: what tiles are scaled by on their way to float16.
+__device__ __forceinline__ int tile_exponent(float v) {
+  return v > 0.f ? min(max(__builtin_amdgcn_frexp_expf(v), -60), 100) : -60;
+}
+
+// The plan made for this call.
+__device__ __forceinline__ bool plan_matches(const AttnArgs &a) {
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < A_KEYS; i += 4) {
+    const int4 w = gload<int4>(a.plan + A_KEY + i);
+    ok = ok && w.x == a.key[i] && w.y == a.key[i + 1] && w.z == a.key[i + 2] && w.w == a.key[i + 3];
+  }
+  return uniform(ok);
+}
+
+__device__ __forceinline__ AttnUnit load_unit(const AttnArgs &a, int kind, int m) {
+  const char *at = reinterpret_cast<const char *>(a.plan) + a.s.unit[kind] + size_t(m) * sizeof(AttnUnit);
+  const int4 w0 = gload<int4>(at), w1 = gload<int4>(at + 16), w2 = gload<int4>(at + 32);
+  AttnUnit u;
+  u.q0 = uniform(w0.x), u.n = uniform(w0.y), u.len = uniform(w0.z), u.row0 = uniform(w0.w);
+  u.rows = uniform(w1.x), u.seq = uniform(w1.y), u.ntiles = uniform(w1.z), u.sink_tiles = uniform(w1.w);
+  u.main = uniform(w2.x), u.nsplit = uniform(w2.y), u.slot = uniform(w2.z);
+  return u;
+}
+
+// Piece `part` of a unit: its tiles v0 .. v1 - 1.
+__device__ __forceinline__ void piece_tiles(const AttnUnit &u, int part, int &v0, int &v1) {
+  v0 = int(int64_t(u.ntiles) * part / u.nsplit);
+  v1 = int(int64_t(u.ntiles) * (part + 1) / u.nsplit);
+}
+
+// Which page a block of 16 keys lies in; -1 where its keys are not seen: past the sequence's end, or no page of the cache.
+__device__ __forceinline__ int block_page(const AttnArgs &a, const AttnUnit &u, int key) {
+  if (key >= u.len) return -1;
+  const int p = gload<int>(a.pages + int64_t(u.seq) * a.ld_pages + (key >> a.page_bits));
+  return p >= 0 && p < a.c.n_pages ? p : -1;
+}
+
+__device__ __forceinline__ int tile_key(const AttnUnit &u, int v) {
+  return (v < u.sink_tiles ? v : u.main + v - u.sink_tiles) * kKeyTile;
+}
+
+// What a row sees: keys up to its position within the window, the first ones, and of a tree's drafted tokens those of its mask.
+struct RowSight {
+  int pos, first_end;  // position; the end of the first keys that stay visible
+  uint64_t mask;       // the drafted tokens of a tree
+  __device__ __forceinline__ void set(const AttnArgs &a, const AttnUnit &u, int row) {
+    const int i = row / a.s.group, context = u.len - u.n;
+    pos = -1, mask = 0;
+    if (row < u.row0 + u.rows) {
+      pos = context + i;
+      if (a.tree) {
+        mask = gload<uint64_t>(a.tree + u.q0 + i) & (~uint64_t(0) >> (LORA_MAX_TREE - u.n));
+        pos = context + __popcll(mask & ((uint64_t(1) << i) - 1));
+      }
+    }
+    first_end = min(a.sinks, pos + 1);
+  }
+  // (keys are not negative, so that none is within the window of a negative position)
+  __device__ __forceinline__ bool sees(const AttnArgs &a, const AttnUnit &u, int key) const {
+    const bool near = uint32_t(pos - key) < uint32_t(a.window) || key < first_end;
+    const int draft = key - (u.len - u.n);
+    if (!a.tree || draft < 0) return near;
+    return draft < LORA_MAX_TREE && (mask >> draft & 1);
+  }
+};
+
+// Whether every row at positions lo .. hi sees all of a tile.
+__device__ __forceinline__ bool all_seen(const AttnArgs &a, const AttnUnit &u, int key, int lo, int hi) {
+  const int last = key + kKeyTile - 1;
+  return last <= (a.tree ? u.len - u.n - 1 : lo) && (hi - key < a.window || last < a.sinks);
+}
+
+template <typename E>
+__device__ __forceinline__ float to_float(E v) {
+  if constexpr (sizeof(E) == 4) return v;
+  else return bf_to_f(v);
+}
+
+// N values of a query head at p (any alignment of elements), of which n are there.
+template <typename E, int N>
+__device__ __forceinline__ void load_query(const E *p, int n, float *f) {
+  if constexpr (sizeof(E) == 2) {
+    typedef uint32_t U __attribute__((ext_vector_type(4), aligned(2)));
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+      if (n >= i + 8) {
+        const U u = *(const LORA_GLOBAL U *)(p + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[i + 2 * j] = bf_lo(u[j]), f[i + 2 * j + 1] = bf_hi(u[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[i + j] = i + j < n ? bf_to_f(gload<uint16_t>(p + i + j)) : 0.f;
+      }
+    }
+  } else {
+    typedef float U __attribute__((ext_vector_type(4), aligned(4)));
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      if (n >= i + 4) {
+        const U u = *(const LORA_GLOBAL U *)(p + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[i + j] = u[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[i + j] = i + j < n ? gload<float>(p + i + j) : 0.f;
+      }
+    }
+  }
+}
+
+// Four output values at p, of which n are there.
+template <typename E>
+__device__ __forceinline__ void store_four(E *p, const float *f, int n) {
+  if (n >= 4) {
+    if constexpr (sizeof(E) == 2) {
+      typedef uint32_t U __attribute__((ext_vector_type(2), aligned(2)));
+      const U u = {pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3])};
+      *(LORA_GLOBAL U *)p = u;
+    } else {
+      typedef float U __attribute__((ext_vector_type(4), aligned(4)));
+      const U u = {f[0], f[1], f[2], f[3]};
+      *(LORA_GLOBAL U *)p = u;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n) {
+        if constexpr (sizeof(E) == 2) gstore(p + j, f_to_bf(f[j]));
+        else gstore(p + j, f[j]);
+      }
+  }
+}
+
+// Row `row` of a sequence in the query or output heads.
+template <typename E>
+__device__ __forceinline__ E *row_at(const AttnArgs &a, const lora_heads &h, const AttnUnit &u, int kv_head, int row) {
+  const int i = row / a.s.group, g = row - i * a.s.group;
+  return static_cast<E *>(h.data) + int64_t(u.q0 + i) * h.token + int64_t(kv_head * a.s.group + g) * h.head;
+}
+
+hipError_t launch_attention_few(const AttnArgs &a, int dtype, hipStream_t stream);
+hipError_t launch_attention_many(const AttnArgs &a, int dtype, hipStream_t stream);
+
+}  // namespace lora
