@@ -12,7 +12,12 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kNoScore = -3.0e38f;  // the running maximum before the first key
-constexpr int kNever = 0x7fffffff;
+// The largest weight of a row is 2^kHeadroom when its maximum is taken, and no more than 2^(kHeadroom + kSlack) before
+// the maximum is taken anew, so that float16 holds it.  Weights that are 2^-(14 + kHeadroom) of the largest and less are
+// held to a fixed 2^-(25 + kHeadroom) of it.  A slack of 7 takes a maximum anew 3 or 4 times a row instead of at every
+// new one; float32 calls, whose second float16 number begins 2^-11 lower, have the headroom instead.
+template <bool F32> constexpr float kHeadroom = F32 ? 14.f : 8.f;
+template <bool F32> constexpr float kSlack = F32 ? 1.f : 7.f;
 
 // Two bytes of u (8-bit values plus 128, so 0 .. 255) as float16, (u - 128) /
 // 512 each.  The bytes are taken as the float16 numbers u * 2^-24 that their
@@ -28,6 +33,12 @@ constexpr float kByteScale = 512.f;
 __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const f32x2 f = {a, b};
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
+}
+
+// acc + a.lo + a.hi
+__device__ __forceinline__ float sum_f16(uint32_t a, float acc) {
+  const f16x2 ones = {_Float16(1.f), _Float16(1.f)};
+  return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, a), ones, acc, false);
 }
 
 __device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -70,6 +81,20 @@ __device__ __forceinline__ float wave_max_f(float v) {
   LORA_ROR(8);
 #undef LORA_ROR
   return quarters_max(v);
+}
+
+// The largest over the wave, of the bits of floats that are not negative too.
+__device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
+#define LORA_ROR(n) v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x120 + (n), 0xf, 0xf, false)))
+  LORA_ROR(1);
+  LORA_ROR(2);
+  LORA_ROR(4);
+  LORA_ROR(8);
+#undef LORA_ROR
+  const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(uint32_t(s[0]), uint32_t(s[1]));
+  const auto t = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(uint32_t(t[0]), uint32_t(t[1]));
 }
 
 // An exponent e with |v| in [2^(e-1), 2^e), held to -60 .. 100: what tiles are scaled by on their way to float16.

@@ -26,6 +26,13 @@
 namespace lora {
 namespace {
 
+// Holds the computation of x to this place: products and exponentials have no order of their own for the compiler, which
+// would gather them.
+template <typename T>
+__device__ __forceinline__ void pin(T &x) {
+  asm volatile("" : "+v"(x));
+}
+
 // NW waves; DP: the head padded; F32: queries and outputs in float32.
 template <int DP, int NW, bool F32>
 __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArgs a) {
@@ -36,11 +43,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
   constexpr int kKUnits = 64 * DP / 16, kKPer = (kKUnits + kThreads - 1) / kThreads;
   constexpr int kVUnits = 16 * DP / 4, kVPer = (kVUnits + kThreads - 1) / kThreads;
   constexpr int kPages = 1024;                  // key blocks whose pages are looked up at once
+  // LDS: K [2][64][kChunks] and V^T [2][DP][8] in pieces of 16 bytes; of 2 NW tiles the scales of K and V, [2 NW][64]
+  // each, and what else is known of them; the pages of key blocks
   extern __shared__ __align__(16) char lds[];
-  uint4 *lds_k = reinterpret_cast<uint4 *>(lds);                      // [2][64][kChunks]
-  uint4 *lds_v = lds_k + 2 * 64 * kChunks;                            // [2][DP][8]
-  float *lds_s = reinterpret_cast<float *>(lds_v + 2 * DP * 8);       // F32: [2][2][64] scales of K and V
-  int *lds_pages = reinterpret_cast<int *>(lds_s + (F32 ? 256 : 0));  // [kPages]
+  constexpr int kRing = 2 * NW;
+  constexpr int kV = 2 * 64 * DP * 2, kKS = 2 * kV, kVS = kKS + kRing * 256, kMeta = kVS + kRing * 256, kList = kMeta + kRing * 16;
+  int *lds_pages = reinterpret_cast<int *>(lds + kList);
 
   if (!plan_matches(a)) {
     if (!a.s.few_blocks && blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(a.plan + H_ERR, 1);  // (else counted there)
@@ -110,82 +118,78 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
       for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
     float M = kNoScore, l = 0.f;
 
-    // staging: raw values of a tile and the scales they are widened with
+    const int in_page = (1 << a.page_bits) - 1;
+    auto fetch_pages = [&](int v, int n) {  // of tiles v .. v + n - 1, to their places in the list
+      for (int i = tid; i < 4 * n; i += kThreads) {
+        const int t = v + i / 4;
+        lds_pages[((v - v0) * 4 + i) % kPages] = t < v1 ? block_page(a, u, tile_key(u, t) + (i % 4) * 16) : -1;
+      }
+    };
+
+    // The scales of a tile, a key a lane, are one wave's work: over a power of two that leaves them below 1 (fp32: those
+    // of V), to LDS.  All waves do a tile each at once, NW tiles ahead, so that none waits for another.
+    uint32_t sk = 0, sv = 0;
+    auto load_scales = [&](int v) {
+      const int page = v < v1 ? lds_pages[((v - v0) * 4 + lane / 16) % kPages] : -1;
+      sk = sv = 0;
+      if (page >= 0) {
+        const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + lane) & in_page);
+        sk = gload<uint32_t>(a.c.k_scale + page * a.c.k_scale_page + slot);
+        sv = gload<uint32_t>(a.c.v_scale + page * a.c.v_scale_page + slot);
+      }
+    };
+    auto put_scales = [&](int v) {
+      constexpr uint32_t kInf = 0x7f800000u;
+      const int at = (v - v0) % kRing;
+      const uint64_t seen = __ballot(lds_pages[((v - v0) * 4 + lane / 16) % kPages] >= 0), nan = __ballot(sv > kInf);
+      const uint32_t v_fine = sv > kInf ? 0u : sv, k_fine = sk > kInf ? 0u : sk;
+      const int e_k = tile_exponent(__uint_as_float(wave_max_bits(k_fine))), e_v = tile_exponent(__uint_as_float(wave_max_bits(v_fine)));
+      // (NaN scales of V become zeros: the rows that see the key get their NaN from its score)
+      const float ks = __uint_as_float(sk);
+      reinterpret_cast<float *>(lds + kKS)[at * 64 + lane] = F32 ? ks : ks * ldexpf(1.f, -e_k);
+      reinterpret_cast<float *>(lds + kVS)[at * 64 + lane] = __uint_as_float(v_fine) * ldexpf(1.f, -e_v);
+      const int hidden = (seen & 1 ? 0 : 1) | (seen >> 16 & 1 ? 0 : 2) | (seen >> 32 & 1 ? 0 : 4) | (seen >> 48 & 1 ? 0 : 8);
+      if (lane == 0)
+        reinterpret_cast<int4 *>(lds + kMeta)[at] = make_int4((e_k + 128) | (e_v + 128) << 8 | hidden << 16, 0, int(nan), int(nan >> 32));
+    };
+
+    // Raw values of a tile of K and one of V on their way.  A wave's rows lie in one block of 16 keys.  What is past a
+    // row's end, or in no page, is read from elsewhere in the cache: it meets zeros of the queries, or is not seen.
     uint4 k_raw[kKPer];
     uint32_t v_raw[kVPer][4];
-    float k_sc[kKPer], top_k = 0.f, top_v = 0.f;
-    float4 v_sc[kVPer];
-    int e_k = 0, e_v = 0, bad = 0;
-    uint64_t nan = 0;
-
-    auto fetch_pages = [&](int v) {  // of tiles v .. v + kPages / 4
-      lds_barrier();
-      for (int i = tid; i < kPages; i += kThreads) {
-        const int t = v + i / 4;
-        lds_pages[i] = t < v1 ? block_page(a, u, tile_key(u, t) + (i % 4) * 16) : -1;
-      }
-      lds_barrier();
-    };
-    auto load_tile = [&](int v) {
-      const int key = tile_key(u, v), at = (v - v0) % (kPages / 4) * 4;
-      const int in_page = (1 << a.page_bits) - 1;
-      const int4 ids = *reinterpret_cast<const int4 *>(lds_pages + at);
-      bad = uniform((ids.x < 0 ? 1 : 0) | (ids.y < 0 ? 2 : 0) | (ids.z < 0 ? 4 : 0) | (ids.w < 0 ? 8 : 0));
+    auto load_k = [&](int v) {
 #pragma unroll
       for (int i = 0; i < kKPer; ++i) {
-        const int n = i * kThreads + tid, r = n / (DP / 16), byte = n % (DP / 16) * 16;
-        k_raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        k_sc[i] = 0.f;
-        if (kKUnits % kThreads && n >= kKUnits) continue;
-        const int page = lds_pages[at + r / 16];
-        if (page >= 0) {
-          const int64_t slot = (int64_t(head) << a.page_bits) + ((key + r) & in_page);
-          if (byte < a.pitch) k_raw[i] = gload<uint4>(a.c.k + page * a.c.k_page + slot * a.pitch + byte);
-          k_sc[i] = gload<float>(a.c.k_scale + page * a.c.k_scale_page + slot);
-        }
+        const int first = i * kThreads + wave * 64;
+        if (kKUnits % kThreads && first >= kKUnits) continue;
+        const int n = first + lane, r = n / (DP / 16), byte = n % (DP / 16) * 16, block = first / (DP / 16) / 16;
+        const int page = max(uniform(lds_pages[((v - v0) * 4 + block) % kPages]), 0);
+        const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + block * 16) & in_page);
+        k_raw[i] = gload_at<uint4>(a.c.k + page * a.c.k_page + slot * a.pitch,
+                                   uint32_t(r % 16 * a.pitch + (byte < a.pitch ? byte : 0)));
       }
+    };
+    auto load_v = [&](int v) {
 #pragma unroll
       for (int i = 0; i < kVPer; ++i) {
-        const int n = i * kThreads + tid, byte = n % (DP / 4) * 4, r = n / (DP / 4) * 4;
+        const int first = i * kThreads + wave * 64;
+        if (kVUnits % kThreads && first >= kVUnits) continue;
+        const int n = first + lane, byte = n % (DP / 4) * 4, r = n / (DP / 4) * 4, block = first / (DP / 4) * 4 / 16;
+        const int page = max(uniform(lds_pages[((v - v0) * 4 + block) % kPages]), 0);
+        const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + block * 16) & in_page);
+        const int8_t *base = a.c.v + page * a.c.v_page + slot * a.pitch;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v_raw[i][j] = 0u;
-        v_sc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (kVUnits % kThreads && n >= kVUnits) continue;
-        const int page = lds_pages[at + r / 16];
-        if (page >= 0) {
-          const int64_t slot = (int64_t(head) << a.page_bits) + ((key + r) & in_page);
-          const int8_t *p = a.c.v + page * a.c.v_page + slot * a.pitch + byte;
-          if (byte < a.pitch) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v_raw[i][j] = gload<uint32_t>(p + j * a.pitch);
-          }
-          v_sc[i] = gload<float4>(a.c.v_scale + page * a.c.v_scale_page + slot);
-        }
-      }
-      // every wave finds the tile's largest scales by itself
-      top_k = top_v = 0.f;
-      const int page = lds_pages[at + lane / 16];
-      if (page >= 0) {
-        const int64_t slot = (int64_t(head) << a.page_bits) + ((key + lane) & in_page);
-        top_k = gload<float>(a.c.k_scale + page * a.c.k_scale_page + slot);
-        top_v = gload<float>(a.c.v_scale + page * a.c.v_scale_page + slot);
+        for (int j = 0; j < 4; ++j)
+          v_raw[i][j] = gload_at<uint32_t>(base + j * a.pitch, uint32_t(r % 16 * a.pitch + (byte < a.pitch ? byte : 0)));
       }
     };
-    auto put_tile = [&](int buf) {
-      nan = __ballot(top_v != top_v);
-      if constexpr (F32) {
-        if (wave == 0) lds_s[(buf * 2) * 64 + lane] = top_k;
-      }
-      const float tk = wave_max_f(fmaxf(top_k, 0.f)), tv = wave_max_f(fmaxf(top_v, 0.f));
-      e_k = uniform(tile_exponent(tk)), e_v = uniform(tile_exponent(tv));
-      const float down_k = ldexpf(1.f, -e_k), down_v = ldexpf(1.f, -e_v);
-      if constexpr (F32) {
-        if (wave == 0) lds_s[(buf * 2 + 1) * 64 + lane] = top_v == top_v ? top_v * down_v : 0.f;
-      }
+    // .. and widened into their buffers
+    auto put_k = [&](int v) {
 #pragma unroll
       for (int i = 0; i < kKPer; ++i) {
-        const int n = i * kThreads + tid, r = n / (DP / 16), chunk = n % (DP / 16) * 2;
-        if (kKUnits % kThreads && n >= kKUnits) continue;
+        const int first = i * kThreads + wave * 64;
+        if (kKUnits % kThreads && first >= kKUnits) continue;
+        const int n = first + lane, r = n / (DP / 16), chunk = n % (DP / 16) * 2;
         const uint32_t w[4] = {k_raw[i].x, k_raw[i].y, k_raw[i].z, k_raw[i].w};
         uint32_t h[8];
         if constexpr (F32) {
@@ -193,167 +197,226 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
           for (int j = 0; j < 8; ++j)
             h[j] = __builtin_bit_cast(uint32_t, bytes_to_f16(__builtin_amdgcn_perm(0u, w[j / 2] ^ kByteBias, j % 2 ? 0x0c030c02u : 0x0c010c00u)));
         } else {
-          const float f = k_sc[i] * down_k;
+          const float f = reinterpret_cast<const float *>(lds + kKS)[(v - v0) % kRing * 64 + r];
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             h[j] = pack_f16(float(int8_t(w[j / 2] >> (j % 2 * 16))) * f, float(int8_t(w[j / 2] >> (j % 2 * 16 + 8))) * f);
         }
-        uint4 *to = lds_k + (buf * 64 + r) * kChunks;
-        to[chunk ^ (r & kMask)] = make_uint4(h[0], h[1], h[2], h[3]);
-        to[(chunk + 1) ^ (r & kMask)] = make_uint4(h[4], h[5], h[6], h[7]);
+        const int to = (r * kChunks + (chunk ^ (r & kMask))) * 16 + ((v - v0) & 1) * (64 * DP * 2);
+        *reinterpret_cast<uint4 *>(lds + to) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(lds + (to ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
       }
+    };
+    auto put_v = [&](int v, int j0, int j1) {  // columns j0 .. j1 - 1 of a lane's four
 #pragma unroll
       for (int i = 0; i < kVPer; ++i) {
-        const int n = i * kThreads + tid, c = n % (DP / 4), quad = n / (DP / 4);
-        if (kVUnits % kThreads && n >= kVUnits) continue;
-        float f[4] = {v_sc[i].x * down_v, v_sc[i].y * down_v, v_sc[i].z * down_v, v_sc[i].w * down_v};
-        // NaN scales: the rows that see the key get their NaN from its weight
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[j] = f[j] == f[j] ? f[j] : 0.f;
+        const int first = i * kThreads + wave * 64;
+        if (kVUnits % kThreads && first >= kVUnits) continue;
+        const int n = first + lane, c = n % (DP / 4), quad = n / (DP / 4);
+        const float4 f = reinterpret_cast<const float4 *>(lds + kVS)[(v - v0) % kRing * 16 + quad];
         // keys 4 quad .. of a 16-key block are places 8 (quad & 1) + 4 (quad >> 1) .. of its 16
         const int chunk = quad / 4 * 2 + (quad & 1), part = quad >> 1 & 1;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = j0; j < j1; ++j) {
           uint32_t lo, hi;
           if constexpr (F32) {
             const uint32_t pick = 0x0c040c00u + 0x10001u * j;
             lo = __builtin_bit_cast(uint32_t, bytes_to_f16(__builtin_amdgcn_perm(v_raw[i][1] ^ kByteBias, v_raw[i][0] ^ kByteBias, pick)));
             hi = __builtin_bit_cast(uint32_t, bytes_to_f16(__builtin_amdgcn_perm(v_raw[i][3] ^ kByteBias, v_raw[i][2] ^ kByteBias, pick)));
           } else {
-            lo = pack_f16(float(int8_t(v_raw[i][0] >> (8 * j))) * f[0], float(int8_t(v_raw[i][1] >> (8 * j))) * f[1]);
-            hi = pack_f16(float(int8_t(v_raw[i][2] >> (8 * j))) * f[2], float(int8_t(v_raw[i][3] >> (8 * j))) * f[3]);
+            lo = pack_f16(float(int8_t(v_raw[i][0] >> (8 * j))) * f.x, float(int8_t(v_raw[i][1] >> (8 * j))) * f.y);
+            hi = pack_f16(float(int8_t(v_raw[i][2] >> (8 * j))) * f.z, float(int8_t(v_raw[i][3] >> (8 * j))) * f.w);
           }
           const int d = 4 * c + j;
-          uint2 *to = reinterpret_cast<uint2 *>(lds_v + (buf * DP + d) * 8 + (chunk ^ ((d ^ d >> 2) & 7)));
-          to[part] = make_uint2(lo, hi);
+          *reinterpret_cast<uint2 *>(lds + kV + (d * 8 + (chunk ^ ((d ^ d >> 2) & 7))) * 16 + part * 8 + ((v - v0) & 1) * (64 * DP * 2)) =
+              make_uint2(lo, hi);
         }
       }
     };
+    // Operands from LDS, kRead at a time, the next ones on their way while these are used.  Their places differ from a
+    // lane's first by an exclusive or of a constant.
+    constexpr int kRead = 2, kKGroups = 2 * kSteps / kRead, kVGroups = 4 * kBlocks / kRead;
+    const int k_first = (col * kChunks + (half ^ (col & kMask))) * 16;
+    const int v_first = kV + (col * 8 + (half ^ ((col ^ col >> 2) & 7))) * 16;
+    auto read_k = [&](int at, int g, f16x8 (&f)[kRead]) {
+#pragma unroll
+      for (int j = 0; j < kRead; ++j) {
+        const int kb = (kRead * g + j) / kSteps, st = (kRead * g + j) % kSteps;
+        f[j] = __builtin_bit_cast(f16x8, *reinterpret_cast<const uint4 *>(lds + (at ^ 32 * st) + kb * 32 * DP * 2));
+      }
+    };
+    auto read_v = [&](int at, int g, f16x8 (&f)[kRead]) {
+#pragma unroll
+      for (int j = 0; j < kRead; ++j) {
+        const int st = (kRead * g + j) / kBlocks, b = (kRead * g + j) % kBlocks;
+        f[j] = __builtin_bit_cast(f16x8, *reinterpret_cast<const uint4 *>(lds + (at ^ 32 * st) + b * 32 * 128));
+      }
+    };
+    // The scores of K tile v, and between the groups of products what `between` does.
+    auto scores = [&](int v, f32x16 (&s)[2], auto between) {
+      f16x8 f[2][kRead];
+      int at = k_first + ((v - v0) & 1) * (64 * DP * 2);
+      pin(at);  // (else the places of all operands are kept in registers)
+      read_k(at, 0, f[0]);
+#pragma unroll
+      for (int g = 0; g < kKGroups; ++g) {
+        if (g + 1 < kKGroups) read_k(at, g + 1, f[(g + 1) % 2]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < kRead; ++j) {
+          const int kb = (kRead * g + j) / kSteps, st = (kRead * g + j) % kSteps;
+          if (st == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
+          }
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t) s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[g % 2][j], q[t][st], s[kb], 0, 0, 0);
+        }
+        pin(s[kRead * g / kSteps]);
+        between(g);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
 
-    auto use_tile = [&](int buf, int key, int ek, int ev, int hidden, uint64_t nans) {
-      // rows that see nothing of the tile: before its first key, or beyond the window
-      if (idle || (!a.tree && key > p_hi) || (p_lo - (key + kKeyTile - 1) >= a.window && key >= a.sinks)) return;
-      const bool whole = hidden == 0 && nans == 0 && all_seen(a, u, key, p_lo, p_hi);
-      f32x16 s[2];
+    // Tile v: its scores s become weights and outputs, those of v + 1 are computed, V of v + 1 and K of v + 2 are widened.
+    // (In the last tiles what is read and put for the next ones is of no use, and does no harm.)
+    auto step = [&](int v, f32x16 (&s)[2], f32x16 (&s_next)[2]) {
+      if (!idle) {
+        const int key = tile_key(u, v), turn = (v - v0) % kRing;
+        const int4 meta = reinterpret_cast<const int4 *>(lds + kMeta)[turn];
+        const int word = uniform(meta.x), e_k = (word & 255) - 128, e_v = (word >> 8 & 255) - 128, bad = word >> 16;
+        const uint64_t nan = uint32_t(uniform(meta.z)) | uint64_t(uint32_t(uniform(meta.w))) << 32;
+        const bool whole = bad == 0 && nan == 0 && all_seen(a, u, key, p_lo, p_hi);
+        if constexpr (F32) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
+          for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
-        const int r = kb * 32 + col;
-        const uint4 *from = lds_k + (buf * 64 + r) * kChunks;
-#pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
-          const f16x8 kf = __builtin_bit_cast(f16x8, from[(2 * st + half) ^ (r & kMask)]);
-#pragma unroll
-          for (int t = 0; t < kTerms; ++t) s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[t][st], s[kb], 0, 0, 0);
+            for (int g = 0; g < 4; ++g) {
+              const float4 f = reinterpret_cast<const float4 *>(lds + kKS)[turn * 16 + kb * 8 + g * 2 + half];
+              s[kb][4 * g] *= f.x, s[kb][4 * g + 1] *= f.y, s[kb][4 * g + 2] *= f.z, s[kb][4 * g + 3] *= f.w;
+            }
         }
-      }
-      if constexpr (F32) {
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const float4 f = *reinterpret_cast<const float4 *>(lds_s + buf * 128 + kb * 32 + g * 8 + half * 4);
-            s[kb][4 * g] *= f.x, s[kb][4 * g + 1] *= f.y, s[kb][4 * g + 2] *= f.z, s[kb][4 * g + 3] *= f.w;
-          }
-      }
-      uint32_t seen = 0xffffffffu;
-      if (!whole) {
-        seen = 0;
+        if (!whole) {
+          uint32_t seen = 0, hit = 0;
 #pragma nounroll
-        for (int n = 0; n < 32; ++n) {
-          const int at = n / 4 * 8 + half * 4 + n % 4;
-          seen |= !(hidden >> (at / 16) & 1) && sight.sees(a, u, key + at) ? 1u << n : 0u;
-        }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) s[kb][i] = seen >> (kb * 16 + i) & 1 ? s[kb][i] : -__builtin_inff();
-      }
-      // (held away from zero, where a hidden key's score would be NaN; it is what scores near zero are multiplied with)
-      const float factor = fminf(fmaxf(F32 ? score : ldexpf(score, ek), 1e-37f), 1e37f);
-      float top = -__builtin_inff();
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
-      top = half_max(top);
-      const float m = fmaxf(M, top * factor + float(ev) - 14.f), less = m - float(ev);
-      const float fade = __builtin_amdgcn_exp2f(M - m);
-      M = m;
-      float sum = 0.f;
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[kb][i] = __builtin_amdgcn_exp2f(fmaf(s[kb][i], factor, -less));
-      if (nans) {
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if ((nans >> (kb * 32 + i / 4 * 8 + half * 4 + i % 4) & 1) && (seen >> (kb * 16 + i) & 1)) s[kb][i] = __builtin_nanf("");
-      }
-      uint32_t r[kTerms][16];
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float p[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            p[i] = s[kb][4 * g + i];
-            sum += p[i];
+          for (int n = 0; n < 32; ++n) {
+            const int at = n / 4 * 8 + half * 4 + n % 4;
+            seen |= !(bad >> (at / 16) & 1) && sight.sees(a, u, key + at) ? 1u << n : 0u;
+            hit |= uint32_t(nan >> at & 1) << n;
           }
-          if constexpr (F32) {
-            const float4 f = *reinterpret_cast<const float4 *>(lds_s + buf * 128 + 64 + kb * 32 + g * 8 + half * 4);
-            p[0] *= f.x, p[1] *= f.y, p[2] *= f.z, p[3] *= f.w;
-          }
-          uint32_t *to = r[0] + kb * 8 + 2 * g;
-          to[0] = pack_f16(p[0], p[1]), to[1] = pack_f16(p[2], p[3]);
-          if constexpr (F32) {
-            const f16x2 r0 = __builtin_bit_cast(f16x2, to[0]), r1 = __builtin_bit_cast(f16x2, to[1]);
-            r[kTerms - 1][kb * 8 + 2 * g] = pack_f16(p[0] - float(r0.x), p[1] - float(r0.y));
-            r[kTerms - 1][kb * 8 + 2 * g + 1] = pack_f16(p[2] - float(r1.x), p[3] - float(r1.y));
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float x = hit >> i & 1 ? __builtin_nanf("") : s[i / 16][i % 16];
+            s[i / 16][i % 16] = seen >> i & 1 ? x : -__builtin_inff();
           }
         }
-      l = fmaf(l, fade, sum * ldexpf(1.f, -ev));
-      if (__any(fade != 1.f)) {
+        // (held away from zero, where a hidden key's score would be NaN; it is what scores near zero are multiplied with)
+        const float factor = fminf(fmaxf(F32 ? score : ldexpf(score, e_k), 1e-37f), 1e37f);
+        float top = -__builtin_inff();
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) o[b] *= fade;
-      }
+        for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+        top = half_max(top) * factor + (float(e_v) - kHeadroom<F32>);
+        if (__any(top > M + kSlack<F32>)) {
+          const float m = fmaxf(M, top), fade = __builtin_amdgcn_exp2f(M - m);
+          M = m;
+          l *= fade;
 #pragma unroll
-      for (int st = 0; st < 4; ++st)
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-          const int d = b * 32 + col;
-          const f16x8 vf = __builtin_bit_cast(f16x8, lds_v[(buf * DP + d) * 8 + ((2 * st + half) ^ ((d ^ d >> 2) & 7))]);
-#pragma unroll
-          for (int t = 0; t < kTerms; ++t)
-            o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, frag(r[t][4 * st], r[t][4 * st + 1], r[t][4 * st + 2], r[t][4 * st + 3]), o[b], 0, 0, 0);
+          for (int b = 0; b < kBlocks; ++b) o[b] *= fade;
         }
+        const float less = M - float(e_v);
+        float sum = 0.f;
+        uint32_t r[kTerms][16];
+        scores(v + 1, s_next, [&](int g) {
+          // weights of 8 / kKGroups groups of four keys
+#pragma unroll
+          for (int n = g * 8 / kKGroups; n < (g + 1) * 8 / kKGroups; ++n) {
+            float p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(s[n / 4][n % 4 * 4 + i], factor, -less));
+            if constexpr (F32) {
+              sum += (p[0] + p[1]) + (p[2] + p[3]);
+              const float4 f = reinterpret_cast<const float4 *>(lds + kVS)[turn * 16 + n * 2 + half];
+              p[0] *= f.x, p[1] *= f.y, p[2] *= f.z, p[3] *= f.w;
+            }
+            r[0][2 * n] = pack_f16(p[0], p[1]), r[0][2 * n + 1] = pack_f16(p[2], p[3]);
+            if constexpr (F32) {
+              const f16x2 r0 = __builtin_bit_cast(f16x2, r[0][2 * n]), r1 = __builtin_bit_cast(f16x2, r[0][2 * n + 1]);
+              r[kTerms - 1][2 * n] = pack_f16(p[0] - float(r0.x), p[1] - float(r0.y));
+              r[kTerms - 1][2 * n + 1] = pack_f16(p[2] - float(r1.x), p[3] - float(r1.y));
+            } else {
+              // the sum takes the weights as the outputs do, rounded
+              sum = sum_f16(r[0][2 * n + 1], sum_f16(r[0][2 * n], sum));
+            }
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t) pin(r[t][2 * n]), pin(r[t][2 * n + 1]);
+          }
+        });
+        l = fmaf(sum, ldexpf(1.f, -e_v), l);
+        f16x8 f[2][kRead];
+        int at = v_first + ((v - v0) & 1) * (64 * DP * 2);
+        pin(at);
+        read_v(at, 0, f[0]);
+#pragma unroll
+        for (int g = 0; g < kVGroups; ++g) {
+          if (g + 1 < kVGroups) read_v(at, g + 1, f[(g + 1) % 2]);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int j = 0; j < kRead; ++j) {
+            const int st = (kRead * g + j) / kBlocks, b = (kRead * g + j) % kBlocks;
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t)
+              o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                  f[g % 2][j], frag(r[t][4 * st], r[t][4 * st + 1], r[t][4 * st + 2], r[t][4 * st + 3]), o[b], 0, 0, 0);
+          }
+#pragma unroll
+          for (int j = 0; j < kRead; ++j) pin(o[(kRead * g + j) % kBlocks]);
+          // the next tiles, in pieces between the products
+          if (g == kVGroups / 8) put_v(v + 1, 0, 2);
+          if (g == kVGroups * 3 / 8) put_v(v + 1, 2, 4);
+          if (g == kVGroups * 5 / 8) put_k(v + 2);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+        put_v(v + 1, 0, 4);
+        put_k(v + 2);
+      }
+      if (v + 2 < v1) load_v(v + 2);
+      if (v + 3 < v1) load_k(v + 3);
+      if ((v - v0) % NW == 0) {
+        put_scales(v + NW + wave);
+        load_scales(v + 2 * NW + wave);
+      }
+      // half the list of pages anew, well before it is needed
+      constexpr int kHalf = kPages / 8;
+      const int next_half = (v - v0) / kHalf * kHalf + kHalf;
+      if ((v - v0) % kHalf == kHalf / 2 && next_half >= 2 * kHalf && v0 + next_half < v1) fetch_pages(v0 + next_half, kHalf);
+      lds_barrier();
     };
 
     if (v0 < v1) {
-      fetch_pages(v0);
-      load_tile(v0);
-      // what the tile in use was put with (bad: of the tile that is being loaded)
-      int hidden = bad;
-      put_tile(0);
-      if (v0 + 1 < v1) load_tile(v0 + 1);
+      fetch_pages(v0, kPages / 4);
       lds_barrier();
+      load_k(v0);
+      load_v(v0);
+      load_scales(v0 + wave);
+      put_scales(v0 + wave);
+      load_scales(v0 + NW + wave);
+      lds_barrier();
+      put_k(v0);
+      put_v(v0, 0, 4);
+      if (v0 + 1 < v1) {
+        load_k(v0 + 1);
+        put_k(v0 + 1);
+        load_v(v0 + 1);
+        if (v0 + 2 < v1) load_k(v0 + 2);
+      }
+      lds_barrier();
+      f32x16 s[2][2];
+      if (!idle) scores(v0, s[0], [](int) {});
+      lds_barrier();  // the first buffer's next tile comes within the loop
       for (int v = v0; v < v1; ++v) {
-        const int buf = (v - v0) & 1, key = tile_key(u, v), ek = e_k, ev = e_v, hid = hidden;
-        const uint64_t nans = nan;
-        if (v + 1 < v1) {
-          hidden = bad;
-          put_tile(buf ^ 1);
-          if (v + 2 < v1) {
-            if ((v + 2 - v0) % (kPages / 4) == 0) fetch_pages(v + 2);
-            load_tile(v + 2);
-          }
-        }
-        use_tile(buf, key, ek, ev, hid, nans);
-        lds_barrier();
+        step(v, s[0], s[1]);
+        s[0][0] = s[1][0], s[0][1] = s[1][1];
       }
     }
 
@@ -390,7 +453,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
 template <int DP, int NW, bool F32>
 hipError_t launch_many(const AttnArgs &a, hipStream_t stream) {
   const auto kernel = attention_many_kernel<DP, NW, F32>;
-  constexpr size_t smem = size_t(2) * 64 * DP * 2 * 2 + (F32 ? 1024 : 0) + 4096;
+  constexpr size_t smem = size_t(2) * 64 * DP * 2 * 2 + 2 * NW * (512 + 16) + 4096;
   static const bool once = raise_lds_limit(reinterpret_cast<const void *>(kernel), smem);
   (void)once;
   const int64_t items = int64_t(a.s.items[ATTN_MANY]) * a.s.kv_heads;

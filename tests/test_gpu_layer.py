@@ -11,7 +11,8 @@ Tolerances, with u = eps / 2 of the output's type, v = 2^-24 (a float32 rounding
              a maximum taken off: s <= (D + 8) 2v S, S = scale sum |q k|, and 4 v (|score| + |largest score|) more; in
              bfloat16 calls of many rows K is rounded to float16: h S more.
              A weight in float16 is off by h (two of them, in float32 calls, by h^2), its value too where it is rounded
-             to float16 (many rows, bfloat16), exp2 and scales by 8 v.
+             to float16 (many rows, bfloat16), exp2 and scales by 8 v.  Where the sum takes the rounded weights (many
+             rows, bfloat16) theirs move the output by sum p h |v - o|, which is no more than h (A + |o|).
              The sums over n keys are off by 2 v n A.  Then u |o|.  All times 1.05, for what is not first order (s < 0.03).
 """
 import math
@@ -388,11 +389,12 @@ class Step:
                 if not f32:
                     off = off + H * size
                 weight = 8 * V + (H * H if f32 else 2 * H + H * H)
+                also = 0.0 if f32 else H
                 e = torch.zeros(n, self.d, dtype=torch.float64)
                 for c in range(0, length, 256):
                     e += (p[:, c:c + 256, None] * off[:, c:c + 256, None] * (vz[None, c:c + 256] - o[:, None]).abs()).sum(1)
                 A = p @ vz.abs()
-                tol[lo:lo + n, h] = 1.05 * (e + (weight + 2 * V * length) * A) + half(self.dtype) * o.abs()
+                tol[lo:lo + n, h] = 1.05 * (e + (weight + 2 * V * length) * A + also * o.abs()) + half(self.dtype) * o.abs()
         return out, tol
 
     def check(self, **kw):
