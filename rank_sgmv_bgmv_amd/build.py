@@ -27,7 +27,7 @@ LIB = os.path.join(OUT_DIR, "liblora_hip.so")
 SOURCES = ["lora_api.hip", "lora_plan.hip", "lora_valu.hip", "lora_mfma.hip", "lora_merge.hip", "lora_calib.hip",
            "lora_base_api.hip", "lora_quantize.hip", "lora_product.hip", "lora_rotary.hip", "lora_layer_api.hip",
            "lora_norm.hip", "lora_cache.hip", "lora_attention_plan.hip", "lora_attention_few.hip",
-           "lora_attention_many.hip"]
+           "lora_attention_many.hip", "lora_attention_exact.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

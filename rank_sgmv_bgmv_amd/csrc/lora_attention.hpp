@@ -241,5 +241,6 @@ __device__ __forceinline__ E *row_at(const AttnArgs &a, const lora_heads &h, con
 
 hipError_t launch_attention_few(const AttnArgs &a, int dtype, hipStream_t stream);
 hipError_t launch_attention_many(const AttnArgs &a, int dtype, hipStream_t stream);
+hipError_t launch_attention_exact(const AttnArgs &a, int dtype, hipStream_t stream);
 
 }  // namespace lora

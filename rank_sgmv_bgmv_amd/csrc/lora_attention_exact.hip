@@ -1,0 +1,473 @@
+// Attention of many rows over the 8-bit cache (prompts, long drafts), and the
+// joining of cut units.
+//
+// A workgroup takes 32 rows a wave of a sequence's (query, query head) pairs for
+// one cache head, and goes over their key tiles of 64.  A tile is widened to
+// float16 once for all waves and laid in LDS, K as it is and V transposed, two
+// tiles in turn: while one is used the next is converted and the one after it is
+// on its way from memory.
+//
+//     S^T = K Q^T      32 x 32 x 16 products of float16: keys are rows, queries columns
+//     O^T += V^T P^T   the same; P^T comes out of S^T in the lanes that need it
+//
+// V^T's keys stand in LDS in the order in which a lane holds its weights, so
+// that an operand is 16 bytes in a row; pieces of 16 bytes are exchanged within
+// rows so that neighbouring lanes meet different banks.
+//
+// For bf16 the scales go into the float16 values, over a power of two common to
+// a tile (eK, eV): one rounding of 2^-12 a value, as many as the weights have,
+// and nothing is left to do per score but exp2.  For fp32 the 8-bit values are
+// widened exactly, the scales meet scores and weights in float32, and queries
+// and weights are two float16 numbers each.  Maximum and sum as in the kernel
+// for few rows.
+
+#include "lora_attention.hpp"
+
+namespace lora {
+namespace {
+
+// Holds the computation of x to this place: products and exponentials have no order of their own for the compiler, which
+// would gather them.
+template <typename T>
+__device__ __forceinline__ void pin(T &x) {
+  asm volatile("" : "+v"(x));
+}
+
+// NW waves; DP: the head padded; F32: queries and outputs in float32.
+template <int DP, int NW, bool F32>
+__global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnArgs a) {
+  typedef std::conditional_t<F32, float, uint16_t> E;
+  constexpr int kThreads = 64 * NW, kSteps = DP / 16, kBlocks = DP / 32, kTerms = F32 ? 2 : 1;
+  constexpr int kChunks = DP / 8;               // 16-byte pieces of a K row
+  constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
+  constexpr int kKUnits = 64 * DP / 16, kKPer = (kKUnits + kThreads - 1) / kThreads;
+  constexpr int kVUnits = 16 * DP / 4, kVPer = (kVUnits + kThreads - 1) / kThreads;
+  constexpr int kPages = 1024;                  // key blocks whose pages are looked up at once
+  // LDS: K [2][64][kChunks] and V^T [2][DP][8] in pieces of 16 bytes; of 2 NW tiles the scales of K and V, [2 NW][64]
+  // each, and what else is known of them; the pages of key blocks
+  extern __shared__ __align__(16) char lds[];
+  constexpr int kRing = 2 * NW;
+  constexpr int kV = 2 * 64 * DP * 2, kKS = 2 * kV, kVS = kKS + kRing * 256, kMeta = kVS + kRing * 256, kList = kMeta + kRing * 16;
+  int *lds_pages = reinterpret_cast<int *>(lds + kList);
+
+  if (!plan_matches(a)) {
+    if (!a.s.few_blocks && blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(a.plan + H_ERR, 1);  // (else counted there)
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64), col = lane % 32, half = lane / 32;
+  const int kv = a.s.kv_heads, D = a.s.head_dim;
+  const int64_t n_items = int64_t(uniform(gload<int>(a.plan + A_ITEMS + ATTN_MANY))) * kv;
+
+  for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
+    const int item = int(it / kv), head = int(it % kv);
+    const int2 im = gload<int2>(reinterpret_cast<const char *>(a.plan) + a.s.item[ATTN_MANY] + size_t(item) * 8);
+    const AttnUnit u = load_unit(a, ATTN_MANY, uniform(im.x));
+    int v0, v1;
+    piece_tiles(u, uniform(im.y), v0, v1);
+
+    // queries: lane (col, half) holds values 16 s + 8 half .. of row col of its wave
+    const int row_first = u.row0 + wave * 32, row = row_first + col, row_end = u.row0 + u.rows;
+    const bool idle = row_first >= row_end;
+    f16x8 q[kTerms][kSteps];
+    RowSight sight;
+    sight.set(a, u, row);
+    float shift;
+    {
+      float f[kSteps][8];
+      float top = 0.f;
+      const E *p = row < row_end ? row_at<const E>(a, a.q, u, head, row) : nullptr;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int d = 16 * s + 8 * half;
+        load_query<E, 8>(p + d, row < row_end ? D - d : 0, f[s]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float v = fabsf(f[s][i]);
+          top = fmaxf(top, v < __uint_as_float(0x7f800000u) ? v : 0.f);
+        }
+      }
+      top = wave_max_f(top);
+      const int x = top > 0.f ? min(15 - __builtin_amdgcn_frexp_expf(top), 100) : 0;
+      shift = ldexpf(1.f, -x);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        uint32_t w[kTerms][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float y0 = ldexpf(f[s][2 * i], x), y1 = ldexpf(f[s][2 * i + 1], x);
+          w[0][i] = pack_f16(y0, y1);
+          if constexpr (F32) {
+            const f16x2 r = __builtin_bit_cast(f16x2, w[0][i]);
+            w[kTerms - 1][i] = pack_f16(y0 - float(r.x), y1 - float(r.y));
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t) q[t][s] = frag(w[t][0], w[t][1], w[t][2], w[t][3]);
+      }
+    }
+    const float score = a.scale * shift * (F32 ? kByteScale : 1.f);
+    // positions of the wave's rows
+    const int context = u.len - u.n;
+    const int p_lo = a.tree ? context : context + row_first / a.s.group;
+    const int p_hi = a.tree ? u.len - 1 : context + (min(row_first + 32, row_end) - 1) / a.s.group;
+
+    f32x16 o[kBlocks];
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
+    float M = kNoScore, l = 0.f;
+
+    const int in_page = (1 << a.page_bits) - 1;
+    auto fetch_pages = [&](int v, int n) {  // of tiles v .. v + n - 1, to their places in the list
+      for (int i = tid; i < 4 * n; i += kThreads) {
+        const int t = v + i / 4;
+        lds_pages[((v - v0) * 4 + i) % kPages] = t < v1 ? block_page(a, u, tile_key(u, t) + (i % 4) * 16) : -1;
+      }
+    };
+
+    // The scales of a tile, a key a lane, are one wave's work: over a power of two that leaves them below 1 (fp32: those
+    // of V), to LDS.  All waves do a tile each at once, NW tiles ahead, so that none waits for another.
+    uint32_t sk = 0, sv = 0;
+    auto load_scales = [&](int v) {
+      const int page = v < v1 ? lds_pages[((v - v0) * 4 + lane / 16) % kPages] : -1;
+      sk = sv = 0;
+      if (page >= 0) {
+        const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + lane) & in_page);
+        sk = gload<uint32_t>(a.c.k_scale + page * a.c.k_scale_page + slot);
+        sv = gload<uint32_t>(a.c.v_scale + page * a.c.v_scale_page + slot);
+      }
+    };
+    auto put_scales = [&](int v) {
+      constexpr uint32_t kInf = 0x7f800000u;
+      const int at = (v - v0) % kRing;
+      const uint64_t seen = __ballot(lds_pages[((v - v0) * 4 + lane / 16) % kPages] >= 0), nan = __ballot(sv > kInf);
+      const uint32_t v_fine = sv > kInf ? 0u : sv, k_fine = sk > kInf ? 0u : sk;
+      const int e_k = tile_exponent(__uint_as_float(wave_max_bits(k_fine))), e_v = tile_exponent(__uint_as_float(wave_max_bits(v_fine)));
+      // (NaN scales of V become zeros: the rows that see the key get their NaN from its score)
+      const float ks = __uint_as_float(sk);
+      reinterpret_cast<float *>(lds + kKS)[at * 64 + lane] = F32 ? ks : ks * ldexpf(1.f, -e_k);
+      reinterpret_cast<float *>(lds + kVS)[at * 64 + lane] = __uint_as_float(v_fine) * ldexpf(1.f, -e_v);
+      const int hidden = (seen & 1 ? 0 : 1) | (seen >> 16 & 1 ? 0 : 2) | (seen >> 32 & 1 ? 0 : 4) | (seen >> 48 & 1 ? 0 : 8);
+      if (lane == 0)
+        reinterpret_cast<int4 *>(lds + kMeta)[at] = make_int4((e_k + 128) | (e_v + 128) << 8 | hidden << 16, 0, int(nan), int(nan >> 32));
+    };
+
+    // Raw values of a tile of K and one of V on their way.  A wave's rows lie in one block of 16 keys.  What is past a
+    // row's end, or in no page, is read from elsewhere in the cache: it meets zeros of the queries, or is not seen.
+    uint4 k_raw[kKPer];
+    uint32_t v_raw[kVPer][4];
+    auto load_k = [&](int v) {
+#pragma unroll
+      for (int i = 0; i < kKPer; ++i) {
+        const int first = i * kThreads + wave * 64;
+        if (kKUnits % kThreads && first >= kKUnits) continue;
+        const int n = first + lane, r = n / (DP / 16), byte = n % (DP / 16) * 16, block = first / (DP / 16) / 16;
+        const int page = max(uniform(lds_pages[((v - v0) * 4 + block) % kPages]), 0);
+        const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + block * 16) & in_page);
+        k_raw[i] = gload_at<uint4>(a.c.k + page * a.c.k_page + slot * a.pitch,
+                                   uint32_t(r % 16 * a.pitch + (byte < a.pitch ? byte : 0)));
+      }
+    };
+    auto load_v = [&](int v) {
+#pragma unroll
+      for (int i = 0; i < kVPer; ++i) {
+        const int first = i * kThreads + wave * 64;
+        if (kVUnits % kThreads && first >= kVUnits) continue;
+        const int n = first + lane, byte = n % (DP / 4) * 4, r = n / (DP / 4) * 4, block = first / (DP / 4) * 4 / 16;
+        const int page = max(uniform(lds_pages[((v - v0) * 4 + block) % kPages]), 0);
+        const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + block * 16) & in_page);
+        const int8_t *base = a.c.v + page * a.c.v_page + slot * a.pitch;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v_raw[i][j] = gload_at<uint32_t>(base + j * a.pitch, uint32_t(r % 16 * a.pitch + (byte < a.pitch ? byte : 0)));
+      }
+    };
+    // .. and widened into their buffers
+    auto put_k = [&](int v) {
+#pragma unroll
+      for (int i = 0; i < kKPer; ++i) {
+        const int first = i * kThreads + wave * 64;
+        if (kKUnits % kThreads && first >= kKUnits) continue;
+        const int n = first + lane, r = n / (DP / 16), chunk = n % (DP / 16) * 2;
+        const uint32_t w[4] = {k_raw[i].x, k_raw[i].y, k_raw[i].z, k_raw[i].w};
+        uint32_t h[8];
+        if constexpr (F32) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            h[j] = __builtin_bit_cast(uint32_t, bytes_to_f16(__builtin_amdgcn_perm(0u, w[j / 2] ^ kByteBias, j % 2 ? 0x0c030c02u : 0x0c010c00u)));
+        } else {
+          const float f = reinterpret_cast<const float *>(lds + kKS)[(v - v0) % kRing * 64 + r];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            h[j] = pack_f16(float(int8_t(w[j / 2] >> (j % 2 * 16))) * f, float(int8_t(w[j / 2] >> (j % 2 * 16 + 8))) * f);
+        }
+        const int to = (r * kChunks + (chunk ^ (r & kMask))) * 16 + ((v - v0) & 1) * (64 * DP * 2);
+        *reinterpret_cast<uint4 *>(lds + to) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4 *>(lds + (to ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+      }
+    };
+    auto put_v = [&](int v, int j0, int j1) {  // columns j0 .. j1 - 1 of a lane's four
+#pragma unroll
+      for (int i = 0; i < kVPer; ++i) {
+        const int first = i * kThreads + wave * 64;
+        if (kVUnits % kThreads && first >= kVUnits) continue;
+        const int n = first + lane, c = n % (DP / 4), quad = n / (DP / 4);
+        const float4 f = reinterpret_cast<const float4 *>(lds + kVS)[(v - v0) % kRing * 16 + quad];
+        // keys 4 quad .. of a 16-key block are places 8 (quad & 1) + 4 (quad >> 1) .. of its 16
+        const int chunk = quad / 4 * 2 + (quad & 1), part = quad >> 1 & 1;
+#pragma unroll
+        for (int j = j0; j < j1; ++j) {
+          uint32_t lo, hi;
+          if constexpr (F32) {
+            const uint32_t pick = 0x0c040c00u + 0x10001u * j;
+            lo = __builtin_bit_cast(uint32_t, bytes_to_f16(__builtin_amdgcn_perm(v_raw[i][1] ^ kByteBias, v_raw[i][0] ^ kByteBias, pick)));
+            hi = __builtin_bit_cast(uint32_t, bytes_to_f16(__builtin_amdgcn_perm(v_raw[i][3] ^ kByteBias, v_raw[i][2] ^ kByteBias, pick)));
+          } else {
+            lo = pack_f16(float(int8_t(v_raw[i][0] >> (8 * j))) * f.x, float(int8_t(v_raw[i][1] >> (8 * j))) * f.y);
+            hi = pack_f16(float(int8_t(v_raw[i][2] >> (8 * j))) * f.z, float(int8_t(v_raw[i][3] >> (8 * j))) * f.w);
+          }
+          const int d = 4 * c + j;
+          *reinterpret_cast<uint2 *>(lds + kV + (d * 8 + (chunk ^ ((d ^ d >> 2) & 7))) * 16 + part * 8 + ((v - v0) & 1) * (64 * DP * 2)) =
+              make_uint2(lo, hi);
+        }
+      }
+    };
+    // Operands from LDS, kRead at a time, the next ones on their way while these are used.  Their places differ from a
+    // lane's first by an exclusive or of a constant.
+    constexpr int kRead = 2, kKGroups = 2 * kSteps / kRead, kVGroups = 4 * kBlocks / kRead;
+    const int k_first = (col * kChunks + (half ^ (col & kMask))) * 16;
+    const int v_first = kV + (col * 8 + (half ^ ((col ^ col >> 2) & 7))) * 16;
+    auto read_k = [&](int at, int g, f16x8 (&f)[kRead]) {
+#pragma unroll
+      for (int j = 0; j < kRead; ++j) {
+        const int kb = (kRead * g + j) / kSteps, st = (kRead * g + j) % kSteps;
+        f[j] = __builtin_bit_cast(f16x8, *reinterpret_cast<const uint4 *>(lds + (at ^ 32 * st) + kb * 32 * DP * 2));
+      }
+    };
+    auto read_v = [&](int at, int g, f16x8 (&f)[kRead]) {
+#pragma unroll
+      for (int j = 0; j < kRead; ++j) {
+        const int st = (kRead * g + j) / kBlocks, b = (kRead * g + j) % kBlocks;
+        f[j] = __builtin_bit_cast(f16x8, *reinterpret_cast<const uint4 *>(lds + (at ^ 32 * st) + b * 32 * 128));
+      }
+    };
+    // The scores of K tile v, and between the groups of products what `between` does.
+    auto scores = [&](int v, f32x16 (&s)[2], auto between) {
+      f16x8 f[2][kRead];
+      int at = k_first + ((v - v0) & 1) * (64 * DP * 2);
+      pin(at);  // (else the places of all operands are kept in registers)
+      read_k(at, 0, f[0]);
+#pragma unroll
+      for (int g = 0; g < kKGroups; ++g) {
+        if (g + 1 < kKGroups) read_k(at, g + 1, f[(g + 1) % 2]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < kRead; ++j) {
+          const int kb = (kRead * g + j) / kSteps, st = (kRead * g + j) % kSteps;
+          if (st == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
+          }
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t) s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[g % 2][j], q[t][st], s[kb], 0, 0, 0);
+        }
+        pin(s[kRead * g / kSteps]);
+        between(g);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+
+    // Tile v: its scores s become weights and outputs, those of v + 1 are computed, V of v + 1 and K of v + 2 are widened.
+    // (In the last tiles what is read and put for the next ones is of no use, and does no harm.)
+    auto step = [&](int v, f32x16 (&s)[2], f32x16 (&s_next)[2]) {
+      if (!idle) {
+        const int key = tile_key(u, v), turn = (v - v0) % kRing;
+        const int4 meta = reinterpret_cast<const int4 *>(lds + kMeta)[turn];
+        const int word = uniform(meta.x), e_k = (word & 255) - 128, e_v = (word >> 8 & 255) - 128, bad = word >> 16;
+        const uint64_t nan = uint32_t(uniform(meta.z)) | uint64_t(uint32_t(uniform(meta.w))) << 32;
+        const bool whole = bad == 0 && nan == 0 && all_seen(a, u, key, p_lo, p_hi);
+        if constexpr (F32) {
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const float4 f = reinterpret_cast<const float4 *>(lds + kKS)[turn * 16 + kb * 8 + g * 2 + half];
+              s[kb][4 * g] *= f.x, s[kb][4 * g + 1] *= f.y, s[kb][4 * g + 2] *= f.z, s[kb][4 * g + 3] *= f.w;
+            }
+        }
+        if (!whole) {
+          uint32_t seen = 0, hit = 0;
+#pragma nounroll
+          for (int n = 0; n < 32; ++n) {
+            const int at = n / 4 * 8 + half * 4 + n % 4;
+            seen |= !(bad >> (at / 16) & 1) && sight.sees(a, u, key + at) ? 1u << n : 0u;
+            hit |= uint32_t(nan >> at & 1) << n;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float x = hit >> i & 1 ? __builtin_nanf("") : s[i / 16][i % 16];
+            s[i / 16][i % 16] = seen >> i & 1 ? x : -__builtin_inff();
+          }
+        }
+        // (held away from zero, where a hidden key's score would be NaN; it is what scores near zero are multiplied with)
+        const float factor = fminf(fmaxf(F32 ? score : ldexpf(score, e_k), 1e-37f), 1e37f);
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
+        top = half_max(top) * factor + (float(e_v) - kHeadroom<F32>);
+        if (__any(top > M + kSlack<F32>)) {
+          const float m = fmaxf(M, top), fade = __builtin_amdgcn_exp2f(M - m);
+          M = m;
+          l *= fade;
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) o[b] *= fade;
+        }
+        const float less = M - float(e_v);
+        float sum = 0.f;
+        uint32_t r[kTerms][16];
+        scores(v + 1, s_next, [&](int g) {
+          // weights of 8 / kKGroups groups of four keys
+#pragma unroll
+          for (int n = g * 8 / kKGroups; n < (g + 1) * 8 / kKGroups; ++n) {
+            float p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(s[n / 4][n % 4 * 4 + i], factor, -less));
+            if constexpr (F32) {
+              sum += (p[0] + p[1]) + (p[2] + p[3]);
+              const float4 f = reinterpret_cast<const float4 *>(lds + kVS)[turn * 16 + n * 2 + half];
+              p[0] *= f.x, p[1] *= f.y, p[2] *= f.z, p[3] *= f.w;
+            }
+            r[0][2 * n] = pack_f16(p[0], p[1]), r[0][2 * n + 1] = pack_f16(p[2], p[3]);
+            if constexpr (F32) {
+              const f16x2 r0 = __builtin_bit_cast(f16x2, r[0][2 * n]), r1 = __builtin_bit_cast(f16x2, r[0][2 * n + 1]);
+              r[kTerms - 1][2 * n] = pack_f16(p[0] - float(r0.x), p[1] - float(r0.y));
+              r[kTerms - 1][2 * n + 1] = pack_f16(p[2] - float(r1.x), p[3] - float(r1.y));
+            } else {
+              // the sum takes the weights as the outputs do, rounded
+              sum = sum_f16(r[0][2 * n + 1], sum_f16(r[0][2 * n], sum));
+            }
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t) pin(r[t][2 * n]), pin(r[t][2 * n + 1]);
+          }
+        });
+        l = fmaf(sum, ldexpf(1.f, -e_v), l);
+        f16x8 f[2][kRead];
+        int at = v_first + ((v - v0) & 1) * (64 * DP * 2);
+        pin(at);
+        read_v(at, 0, f[0]);
+#pragma unroll
+        for (int g = 0; g < kVGroups; ++g) {
+          if (g + 1 < kVGroups) read_v(at, g + 1, f[(g + 1) % 2]);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int j = 0; j < kRead; ++j) {
+            const int st = (kRead * g + j) / kBlocks, b = (kRead * g + j) % kBlocks;
+#pragma unroll
+            for (int t = 0; t < kTerms; ++t)
+              o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                  f[g % 2][j], frag(r[t][4 * st], r[t][4 * st + 1], r[t][4 * st + 2], r[t][4 * st + 3]), o[b], 0, 0, 0);
+          }
+#pragma unroll
+          for (int j = 0; j < kRead; ++j) pin(o[(kRead * g + j) % kBlocks]);
+          // the next tiles, in pieces between the products
+          if (g == kVGroups / 8) put_v(v + 1, 0, 2);
+          if (g == kVGroups * 3 / 8) put_v(v + 1, 2, 4);
+          if (g == kVGroups * 5 / 8) put_k(v + 2);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+        put_v(v + 1, 0, 4);
+        put_k(v + 2);
+      }
+      if (v + 2 < v1) load_v(v + 2);
+      if (v + 3 < v1) load_k(v + 3);
+      if ((v - v0) % NW == 0) {
+        put_scales(v + NW + wave);
+        load_scales(v + 2 * NW + wave);
+      }
+      // half the list of pages anew, well before it is needed
+      constexpr int kHalf = kPages / 8;
+      const int next_half = (v - v0) / kHalf * kHalf + kHalf;
+      if ((v - v0) % kHalf == kHalf / 2 && next_half >= 2 * kHalf && v0 + next_half < v1) fetch_pages(v0 + next_half, kHalf);
+      lds_barrier();
+    };
+
+    if (v0 < v1) {
+      fetch_pages(v0, kPages / 4);
+      lds_barrier();
+      load_k(v0);
+      load_v(v0);
+      load_scales(v0 + wave);
+      put_scales(v0 + wave);
+      load_scales(v0 + NW + wave);
+      lds_barrier();
+      put_k(v0);
+      put_v(v0, 0, 4);
+      if (v0 + 1 < v1) {
+        load_k(v0 + 1);
+        put_k(v0 + 1);
+        load_v(v0 + 1);
+        if (v0 + 2 < v1) load_k(v0 + 2);
+      }
+      lds_barrier();
+      f32x16 s[2][2];
+      if (!idle) scores(v0, s[0], [](int) {});
+      lds_barrier();  // the first buffer's next tile comes within the loop
+      for (int v = v0; v < v1; ++v) {
+        step(v, s[0], s[1]);
+        s[0][0] = s[1][0], s[0][1] = s[1][1];
+      }
+    }
+
+    // (V in float16 is value * scale / 2^eV; for fp32 value / 512 * scale / 2^eV)
+    l = half_sum(l);
+    const float up = F32 ? kByteScale : 1.f;
+    if (row < row_end) {
+      if (u.nsplit == 1) {
+        const float inv = l == 0.f ? 0.f : up / l;
+        E *to = row_at<E>(a, a.out, u, head, row);
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int d = b * 32 + g * 8 + half * 4;
+            const float f[4] = {o[b][4 * g] * inv, o[b][4 * g + 1] * inv, o[b][4 * g + 2] * inv, o[b][4 * g + 3] * inv};
+            store_four(to + d, f, D - d);
+          }
+      } else {
+        const int64_t at = (int64_t(u.slot + uniform(im.y)) * kv + head) * a.s.many_rows + (row - u.row0);
+        float *part = reinterpret_cast<float *>(a.ws + a.s.part[ATTN_MANY]) + at * DP;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            gstore(part + b * 32 + g * 8 + half * 4,
+                   make_float4(o[b][4 * g] * up, o[b][4 * g + 1] * up, o[b][4 * g + 2] * up, o[b][4 * g + 3] * up));
+        if (half == 0) gstore(reinterpret_cast<float *>(a.ws + a.s.stat[ATTN_MANY]) + at * 2, make_float2(M, l));
+      }
+    }
+  }
+}
+
+template <int DP, int NW, bool F32>
+hipError_t launch_exact(const AttnArgs &a, hipStream_t stream) {
+  const auto kernel = attention_exact_kernel<DP, NW, F32>;
+  constexpr size_t smem = size_t(2) * 64 * DP * 2 * 2 + 2 * NW * (512 + 16) + 4096;
+  static const bool once = raise_lds_limit(reinterpret_cast<const void *>(kernel), smem);
+  (void)once;
+  const int64_t items = int64_t(a.s.items[ATTN_MANY]) * a.s.kv_heads;
+  kernel<<<dim3(uint32_t(items < 65536 ? items : 65536)), 64 * NW, smem, stream>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attention_exact(const AttnArgs &a, int dtype, hipStream_t stream) {
+  if (dtype == LORA_BF16) return launch_exact<256, 4, false>(a, stream);
+  if (a.s.dp == 64) return launch_exact<64, 4, true>(a, stream);
+  if (a.s.dp == 128) return launch_exact<128, 4, true>(a, stream);
+  return launch_exact<256, 4, true>(a, stream);
+}
+
+}  // namespace lora

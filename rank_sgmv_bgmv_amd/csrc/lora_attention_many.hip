@@ -33,11 +33,11 @@ __device__ __forceinline__ void pin(T &x) {
   asm volatile("" : "+v"(x));
 }
 
-// NW waves; DP: the head padded; F32: queries and outputs in float32.
-template <int DP, int NW, bool F32>
-__global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArgs a) {
-  typedef std::conditional_t<F32, float, uint16_t> E;
-  constexpr int kThreads = 64 * NW, kSteps = DP / 16, kBlocks = DP / 32, kTerms = F32 ? 2 : 1;
+// NW waves; DP: the head padded.
+template <int DP, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) {
+  typedef uint16_t E;
+  constexpr int kThreads = 64 * NW, kSteps = DP / 16, kBlocks = DP / 32;
   constexpr int kChunks = DP / 8;               // 16-byte pieces of a K row
   constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
   constexpr int kKUnits = 64 * DP / 16, kKPer = (kKUnits + kThreads - 1) / kThreads;
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
     // queries: lane (col, half) holds values 16 s + 8 half .. of row col of its wave
     const int row_first = u.row0 + wave * 32, row = row_first + col, row_end = u.row0 + u.rows;
     const bool idle = row_first >= row_end;
-    f16x8 q[kTerms][kSteps];
+    f16x8 q[kSteps];
     RowSight sight;
     sight.set(a, u, row);
     float shift;
@@ -91,21 +91,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
       shift = ldexpf(1.f, -x);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        uint32_t w[kTerms][4];
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float y0 = ldexpf(f[s][2 * i], x), y1 = ldexpf(f[s][2 * i + 1], x);
-          w[0][i] = pack_f16(y0, y1);
-          if constexpr (F32) {
-            const f16x2 r = __builtin_bit_cast(f16x2, w[0][i]);
-            w[kTerms - 1][i] = pack_f16(y0 - float(r.x), y1 - float(r.y));
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < kTerms; ++t) q[t][s] = frag(w[t][0], w[t][1], w[t][2], w[t][3]);
+        for (int i = 0; i < 4; ++i) w[i] = pack_f16(ldexpf(f[s][2 * i], x), ldexpf(f[s][2 * i + 1], x));
+        q[s] = frag(w[0], w[1], w[2], w[3]);
       }
     }
-    const float score = a.scale * shift * (F32 ? kByteScale : 1.f);
+    const float score = a.scale * shift;
     // positions of the wave's rows
     const int context = u.len - u.n;
     const int p_lo = a.tree ? context : context + row_first / a.s.group;
@@ -146,7 +138,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
       const int e_k = tile_exponent(__uint_as_float(wave_max_bits(k_fine))), e_v = tile_exponent(__uint_as_float(wave_max_bits(v_fine)));
       // (NaN scales of V become zeros: the rows that see the key get their NaN from its score)
       const float ks = __uint_as_float(sk);
-      reinterpret_cast<float *>(lds + kKS)[at * 64 + lane] = F32 ? ks : ks * ldexpf(1.f, -e_k);
+      reinterpret_cast<float *>(lds + kKS)[at * 64 + lane] = ks * ldexpf(1.f, -e_k);
       reinterpret_cast<float *>(lds + kVS)[at * 64 + lane] = __uint_as_float(v_fine) * ldexpf(1.f, -e_v);
       const int hidden = (seen & 1 ? 0 : 1) | (seen >> 16 & 1 ? 0 : 2) | (seen >> 32 & 1 ? 0 : 4) | (seen >> 48 & 1 ? 0 : 8);
       if (lane == 0)
@@ -157,25 +149,25 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
     // row's end, or in no page, is read from elsewhere in the cache: it meets zeros of the queries, or is not seen.
     uint4 k_raw[kKPer];
     uint32_t v_raw[kVPer][4];
-    auto load_k = [&](int v) {
+    auto load_k = [&](int v, const int (&pages)[kKPer]) {
 #pragma unroll
       for (int i = 0; i < kKPer; ++i) {
         const int first = i * kThreads + wave * 64;
         if (kKUnits % kThreads && first >= kKUnits) continue;
         const int n = first + lane, r = n / (DP / 16), byte = n % (DP / 16) * 16, block = first / (DP / 16) / 16;
-        const int page = max(uniform(lds_pages[((v - v0) * 4 + block) % kPages]), 0);
+        const int page = max(pages[i], 0);
         const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + block * 16) & in_page);
         k_raw[i] = gload_at<uint4>(a.c.k + page * a.c.k_page + slot * a.pitch,
                                    uint32_t(r % 16 * a.pitch + (byte < a.pitch ? byte : 0)));
       }
     };
-    auto load_v = [&](int v) {
+    auto load_v = [&](int v, const int (&pages)[kVPer]) {
 #pragma unroll
       for (int i = 0; i < kVPer; ++i) {
         const int first = i * kThreads + wave * 64;
         if (kVUnits % kThreads && first >= kVUnits) continue;
         const int n = first + lane, byte = n % (DP / 4) * 4, r = n / (DP / 4) * 4, block = first / (DP / 4) * 4 / 16;
-        const int page = max(uniform(lds_pages[((v - v0) * 4 + block) % kPages]), 0);
+        const int page = max(pages[i], 0);
         const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + block * 16) & in_page);
         const int8_t *base = a.c.v + page * a.c.v_page + slot * a.pitch;
 #pragma unroll
@@ -190,18 +182,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
         const int first = i * kThreads + wave * 64;
         if (kKUnits % kThreads && first >= kKUnits) continue;
         const int n = first + lane, r = n / (DP / 16), chunk = n % (DP / 16) * 2;
+        pin(k_raw[i].x), pin(k_raw[i].y), pin(k_raw[i].z), pin(k_raw[i].w);  // (else widened, and waited for, as soon as loaded)
         const uint32_t w[4] = {k_raw[i].x, k_raw[i].y, k_raw[i].z, k_raw[i].w};
         uint32_t h[8];
-        if constexpr (F32) {
+        const float f = reinterpret_cast<const float *>(lds + kKS)[(v - v0) % kRing * 64 + r];
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            h[j] = __builtin_bit_cast(uint32_t, bytes_to_f16(__builtin_amdgcn_perm(0u, w[j / 2] ^ kByteBias, j % 2 ? 0x0c030c02u : 0x0c010c00u)));
-        } else {
-          const float f = reinterpret_cast<const float *>(lds + kKS)[(v - v0) % kRing * 64 + r];
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            h[j] = pack_f16(float(int8_t(w[j / 2] >> (j % 2 * 16))) * f, float(int8_t(w[j / 2] >> (j % 2 * 16 + 8))) * f);
-        }
+        for (int j = 0; j < 8; ++j)
+          h[j] = pack_f16(float(int8_t(w[j / 2] >> (j % 2 * 16))) * f, float(int8_t(w[j / 2] >> (j % 2 * 16 + 8))) * f);
         const int to = (r * kChunks + (chunk ^ (r & kMask))) * 16 + ((v - v0) & 1) * (64 * DP * 2);
         *reinterpret_cast<uint4 *>(lds + to) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4 *>(lds + (to ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
@@ -214,19 +201,14 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
         if (kVUnits % kThreads && first >= kVUnits) continue;
         const int n = first + lane, c = n % (DP / 4), quad = n / (DP / 4);
         const float4 f = reinterpret_cast<const float4 *>(lds + kVS)[(v - v0) % kRing * 16 + quad];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pin(v_raw[i][j]);
         // keys 4 quad .. of a 16-key block are places 8 (quad & 1) + 4 (quad >> 1) .. of its 16
         const int chunk = quad / 4 * 2 + (quad & 1), part = quad >> 1 & 1;
 #pragma unroll
         for (int j = j0; j < j1; ++j) {
-          uint32_t lo, hi;
-          if constexpr (F32) {
-            const uint32_t pick = 0x0c040c00u + 0x10001u * j;
-            lo = __builtin_bit_cast(uint32_t, bytes_to_f16(__builtin_amdgcn_perm(v_raw[i][1] ^ kByteBias, v_raw[i][0] ^ kByteBias, pick)));
-            hi = __builtin_bit_cast(uint32_t, bytes_to_f16(__builtin_amdgcn_perm(v_raw[i][3] ^ kByteBias, v_raw[i][2] ^ kByteBias, pick)));
-          } else {
-            lo = pack_f16(float(int8_t(v_raw[i][0] >> (8 * j))) * f.x, float(int8_t(v_raw[i][1] >> (8 * j))) * f.y);
-            hi = pack_f16(float(int8_t(v_raw[i][2] >> (8 * j))) * f.z, float(int8_t(v_raw[i][3] >> (8 * j))) * f.w);
-          }
+          const uint32_t lo = pack_f16(float(int8_t(v_raw[i][0] >> (8 * j))) * f.x, float(int8_t(v_raw[i][1] >> (8 * j))) * f.y);
+          const uint32_t hi = pack_f16(float(int8_t(v_raw[i][2] >> (8 * j))) * f.z, float(int8_t(v_raw[i][3] >> (8 * j))) * f.w);
           const int d = 4 * c + j;
           *reinterpret_cast<uint2 *>(lds + kV + (d * 8 + (chunk ^ ((d ^ d >> 2) & 7))) * 16 + part * 8 + ((v - v0) & 1) * (64 * DP * 2)) =
               make_uint2(lo, hi);
@@ -252,12 +234,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
         f[j] = __builtin_bit_cast(f16x8, *reinterpret_cast<const uint4 *>(lds + (at ^ 32 * st) + b * 32 * 128));
       }
     };
-    // The scores of K tile v, and between the groups of products what `between` does.
-    auto scores = [&](int v, f32x16 (&s)[2], auto between) {
-      f16x8 f[2][kRead];
+    // The scores of K tile v, and between the groups of products what `between` does.  f: the first operands.
+    auto first_k = [&](int v) {
       int at = k_first + ((v - v0) & 1) * (64 * DP * 2);
       pin(at);  // (else the places of all operands are kept in registers)
-      read_k(at, 0, f[0]);
+      return at;
+    };
+    auto scores = [&](int at, f16x8 (&f)[2][kRead], f32x16 (&s)[2], auto between) {
 #pragma unroll
       for (int g = 0; g < kKGroups; ++g) {
         if (g + 1 < kKGroups) read_k(at, g + 1, f[(g + 1) % 2]);
@@ -269,8 +252,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
           }
-#pragma unroll
-          for (int t = 0; t < kTerms; ++t) s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[g % 2][j], q[t][st], s[kb], 0, 0, 0);
+          s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[g % 2][j], q[st], s[kb], 0, 0, 0);
         }
         pin(s[kRead * g / kSteps]);
         between(g);
@@ -279,23 +261,31 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
     };
 
     // Tile v: its scores s become weights and outputs, those of v + 1 are computed, V of v + 1 and K of v + 2 are widened.
-    // (In the last tiles what is read and put for the next ones is of no use, and does no harm.)
+    // (In the last tiles what is read and put for the next ones is of no use, and does no harm.)  What a step begins with
+    // is read from LDS before the barrier in front of it: what is known of its tile, and the pages of its loads.
+    int4 meta;
+    int page_k[kKPer], page_v[kVPer];
+    auto look_ahead = [&](int v) {
+      meta = reinterpret_cast<const int4 *>(lds + kMeta)[(v - v0) % kRing];
+#pragma unroll
+      for (int i = 0; i < kKPer; ++i) page_k[i] = lds_pages[((v + 3 - v0) * 4 + (i * kThreads + wave * 64) / (DP / 16) / 16) % kPages];
+#pragma unroll
+      for (int i = 0; i < kVPer; ++i) page_v[i] = lds_pages[((v + 2 - v0) * 4 + (i * kThreads + wave * 64) / (DP / 4) * 4 / 16) % kPages];
+    };
     auto step = [&](int v, f32x16 (&s)[2], f32x16 (&s_next)[2]) {
+      const int word = uniform(meta.x), e_k = (word & 255) - 128, e_v = (word >> 8 & 255) - 128, bad = word >> 16;
+      const uint64_t nan = uint32_t(uniform(meta.z)) | uint64_t(uint32_t(uniform(meta.w))) << 32;
+      const int key = tile_key(u, v);
+      int pk[kKPer], pv[kVPer];
+#pragma unroll
+      for (int i = 0; i < kKPer; ++i) pk[i] = uniform(page_k[i]);
+#pragma unroll
+      for (int i = 0; i < kVPer; ++i) pv[i] = uniform(page_v[i]);
       if (!idle) {
-        const int key = tile_key(u, v), turn = (v - v0) % kRing;
-        const int4 meta = reinterpret_cast<const int4 *>(lds + kMeta)[turn];
-        const int word = uniform(meta.x), e_k = (word & 255) - 128, e_v = (word >> 8 & 255) - 128, bad = word >> 16;
-        const uint64_t nan = uint32_t(uniform(meta.z)) | uint64_t(uint32_t(uniform(meta.w))) << 32;
+        const int at_k = first_k(v + 1);
+        f16x8 fk[2][kRead];
+        read_k(at_k, 0, fk[0]);
         const bool whole = bad == 0 && nan == 0 && all_seen(a, u, key, p_lo, p_hi);
-        if constexpr (F32) {
-#pragma unroll
-          for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              const float4 f = reinterpret_cast<const float4 *>(lds + kKS)[turn * 16 + kb * 8 + g * 2 + half];
-              s[kb][4 * g] *= f.x, s[kb][4 * g + 1] *= f.y, s[kb][4 * g + 2] *= f.z, s[kb][4 * g + 3] *= f.w;
-            }
-        }
         if (!whole) {
           uint32_t seen = 0, hit = 0;
 #pragma nounroll
@@ -311,12 +301,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
           }
         }
         // (held away from zero, where a hidden key's score would be NaN; it is what scores near zero are multiplied with)
-        const float factor = fminf(fmaxf(F32 ? score : ldexpf(score, e_k), 1e-37f), 1e37f);
+        const float factor = fminf(fmaxf(ldexpf(score, e_k), 1e-37f), 1e37f);
         float top = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
-        top = half_max(top) * factor + (float(e_v) - kHeadroom<F32>);
-        if (__any(top > M + kSlack<F32>)) {
+        top = half_max(top) * factor + (float(e_v) - kHeadroom<false>);
+        if (__any(top > M + kSlack<false>)) {
           const float m = fmaxf(M, top), fade = __builtin_amdgcn_exp2f(M - m);
           M = m;
           l *= fade;
@@ -325,48 +315,33 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
         }
         const float less = M - float(e_v);
         float sum = 0.f;
-        uint32_t r[kTerms][16];
-        scores(v + 1, s_next, [&](int g) {
-          // weights of 8 / kKGroups groups of four keys
+        uint32_t r[16];
+        int at_v = v_first + ((v - v0) & 1) * (64 * DP * 2);
+        pin(at_v);
+        f16x8 fv[2][kRead];
+        scores(at_k, fk, s_next, [&](int g) {
+          // weights of 8 / kKGroups groups of four keys; the sum takes them as the outputs do, rounded
 #pragma unroll
           for (int n = g * 8 / kKGroups; n < (g + 1) * 8 / kKGroups; ++n) {
             float p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(s[n / 4][n % 4 * 4 + i], factor, -less));
-            if constexpr (F32) {
-              sum += (p[0] + p[1]) + (p[2] + p[3]);
-              const float4 f = reinterpret_cast<const float4 *>(lds + kVS)[turn * 16 + n * 2 + half];
-              p[0] *= f.x, p[1] *= f.y, p[2] *= f.z, p[3] *= f.w;
-            }
-            r[0][2 * n] = pack_f16(p[0], p[1]), r[0][2 * n + 1] = pack_f16(p[2], p[3]);
-            if constexpr (F32) {
-              const f16x2 r0 = __builtin_bit_cast(f16x2, r[0][2 * n]), r1 = __builtin_bit_cast(f16x2, r[0][2 * n + 1]);
-              r[kTerms - 1][2 * n] = pack_f16(p[0] - float(r0.x), p[1] - float(r0.y));
-              r[kTerms - 1][2 * n + 1] = pack_f16(p[2] - float(r1.x), p[3] - float(r1.y));
-            } else {
-              // the sum takes the weights as the outputs do, rounded
-              sum = sum_f16(r[0][2 * n + 1], sum_f16(r[0][2 * n], sum));
-            }
-#pragma unroll
-            for (int t = 0; t < kTerms; ++t) pin(r[t][2 * n]), pin(r[t][2 * n + 1]);
+            r[2 * n] = pack_f16(p[0], p[1]), r[2 * n + 1] = pack_f16(p[2], p[3]);
+            sum = sum_f16(r[2 * n + 1], sum_f16(r[2 * n], sum));
+            pin(r[2 * n]), pin(r[2 * n + 1]);
           }
+          if (g == kKGroups - 1) read_v(at_v, 0, fv[0]);
         });
         l = fmaf(sum, ldexpf(1.f, -e_v), l);
-        f16x8 f[2][kRead];
-        int at = v_first + ((v - v0) & 1) * (64 * DP * 2);
-        pin(at);
-        read_v(at, 0, f[0]);
 #pragma unroll
         for (int g = 0; g < kVGroups; ++g) {
-          if (g + 1 < kVGroups) read_v(at, g + 1, f[(g + 1) % 2]);
+          if (g + 1 < kVGroups) read_v(at_v, g + 1, fv[(g + 1) % 2]);
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int j = 0; j < kRead; ++j) {
             const int st = (kRead * g + j) / kBlocks, b = (kRead * g + j) % kBlocks;
-#pragma unroll
-            for (int t = 0; t < kTerms; ++t)
-              o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                  f[g % 2][j], frag(r[t][4 * st], r[t][4 * st + 1], r[t][4 * st + 2], r[t][4 * st + 3]), o[b], 0, 0, 0);
+            o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fv[g % 2][j], frag(r[4 * st], r[4 * st + 1], r[4 * st + 2], r[4 * st + 3]),
+                                                          o[b], 0, 0, 0);
           }
 #pragma unroll
           for (int j = 0; j < kRead; ++j) pin(o[(kRead * g + j) % kBlocks]);
@@ -380,8 +355,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
         put_v(v + 1, 0, 4);
         put_k(v + 2);
       }
-      if (v + 2 < v1) load_v(v + 2);
-      if (v + 3 < v1) load_k(v + 3);
+      if (v + 2 < v1) load_v(v + 2, pv);
+      if (v + 3 < v1) load_k(v + 3, pk);
       if ((v - v0) % NW == 0) {
         put_scales(v + NW + wave);
         load_scales(v + 2 * NW + wave);
@@ -390,14 +365,23 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
       constexpr int kHalf = kPages / 8;
       const int next_half = (v - v0) / kHalf * kHalf + kHalf;
       if ((v - v0) % kHalf == kHalf / 2 && next_half >= 2 * kHalf && v0 + next_half < v1) fetch_pages(v0 + next_half, kHalf);
+      look_ahead(v + 1);
       lds_barrier();
     };
 
     if (v0 < v1) {
       fetch_pages(v0, kPages / 4);
       lds_barrier();
-      load_k(v0);
-      load_v(v0);
+      auto pages_of = [&](int v, int (&pk)[kKPer], int (&pv)[kVPer]) {
+#pragma unroll
+        for (int i = 0; i < kKPer; ++i) pk[i] = uniform(lds_pages[((v - v0) * 4 + (i * kThreads + wave * 64) / (DP / 16) / 16) % kPages]);
+#pragma unroll
+        for (int i = 0; i < kVPer; ++i) pv[i] = uniform(lds_pages[((v - v0) * 4 + (i * kThreads + wave * 64) / (DP / 4) * 4 / 16) % kPages]);
+      };
+      int pk[kKPer], pv[kVPer];
+      pages_of(v0, pk, pv);
+      load_k(v0, pk);
+      load_v(v0, pv);
       load_scales(v0 + wave);
       put_scales(v0 + wave);
       load_scales(v0 + NW + wave);
@@ -405,14 +389,24 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
       put_k(v0);
       put_v(v0, 0, 4);
       if (v0 + 1 < v1) {
-        load_k(v0 + 1);
+        pages_of(v0 + 1, pk, pv);
+        load_k(v0 + 1, pk);
         put_k(v0 + 1);
-        load_v(v0 + 1);
-        if (v0 + 2 < v1) load_k(v0 + 2);
+        load_v(v0 + 1, pv);
+        if (v0 + 2 < v1) {
+          pages_of(v0 + 2, pk, pv);
+          load_k(v0 + 2, pk);
+        }
       }
       lds_barrier();
       f32x16 s[2][2];
-      if (!idle) scores(v0, s[0], [](int) {});
+      look_ahead(v0);
+      if (!idle) {
+        f16x8 f[2][kRead];
+        const int at = first_k(v0);
+        read_k(at, 0, f[0]);
+        scores(at, f, s[0], [](int) {});
+      }
       lds_barrier();  // the first buffer's next tile comes within the loop
       for (int v = v0; v < v1; ++v) {
         step(v, s[0], s[1]);
@@ -420,12 +414,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
       }
     }
 
-    // (V in float16 is value * scale / 2^eV; for fp32 value / 512 * scale / 2^eV)
+    // (V in float16 is value * scale / 2^eV)
     l = half_sum(l);
-    const float up = F32 ? kByteScale : 1.f;
     if (row < row_end) {
       if (u.nsplit == 1) {
-        const float inv = l == 0.f ? 0.f : up / l;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         E *to = row_at<E>(a, a.out, u, head, row);
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
@@ -443,16 +436,16 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_many_kernel(AttnArg
 #pragma unroll
           for (int g = 0; g < 4; ++g)
             gstore(part + b * 32 + g * 8 + half * 4,
-                   make_float4(o[b][4 * g] * up, o[b][4 * g + 1] * up, o[b][4 * g + 2] * up, o[b][4 * g + 3] * up));
+                   make_float4(o[b][4 * g], o[b][4 * g + 1], o[b][4 * g + 2], o[b][4 * g + 3]));
         if (half == 0) gstore(reinterpret_cast<float *>(a.ws + a.s.stat[ATTN_MANY]) + at * 2, make_float2(M, l));
       }
     }
   }
 }
 
-template <int DP, int NW, bool F32>
+template <int DP, int NW>
 hipError_t launch_many(const AttnArgs &a, hipStream_t stream) {
-  const auto kernel = attention_many_kernel<DP, NW, F32>;
+  const auto kernel = attention_many_kernel<DP, NW>;
   constexpr size_t smem = size_t(2) * 64 * DP * 2 * 2 + 2 * NW * (512 + 16) + 4096;
   static const bool once = raise_lds_limit(reinterpret_cast<const void *>(kernel), smem);
   (void)once;
@@ -520,14 +513,9 @@ hipError_t launch_join(const AttnArgs &a, int kind, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_attention_many(const AttnArgs &a, int dtype, hipStream_t stream) {
-  if (dtype == LORA_BF16) {
-    if (a.s.dp == 64) return launch_many<64, 8, false>(a, stream);
-    if (a.s.dp == 128) return launch_many<128, 8, false>(a, stream);
-    return launch_many<256, 4, false>(a, stream);
-  }
-  if (a.s.dp == 64) return launch_many<64, 4, true>(a, stream);
-  if (a.s.dp == 128) return launch_many<128, 4, true>(a, stream);
-  return launch_many<256, 4, true>(a, stream);
+  if (dtype != LORA_BF16 || a.s.dp > 128) return launch_attention_exact(a, dtype, stream);
+  if (a.s.dp == 64) return launch_many<64, 8>(a, stream);
+  return launch_many<128, 8>(a, stream);
 }
 
 hipError_t launch_attention(const AttnArgs &a, int dtype, hipStream_t stream) {
