@@ -423,8 +423,8 @@ void launch_few(const AttnArgs &a, hipStream_t stream) {
 hipError_t launch_attention_few(const AttnArgs &a, int dtype, hipStream_t stream) {
   const int dp = a.s.dp, b = a.s.few_blocks;
   if (dtype == LORA_BF16) {
-    if (dp == 64) b == 1 ? launch_few<64, 1, false>(a, stream) : b == 2 ? launch_few<64, 2, false>(a, stream) : launch_few<64, 4, false>(a, stream);
-    else if (dp == 128) b == 1 ? launch_few<128, 1, false>(a, stream) : b == 2 ? launch_few<128, 2, false>(a, stream) : launch_few<128, 4, false>(a, stream);
+    if (dp == 64) b == 1 ? launch_few<64, 1, false>(a, stream) : launch_few<64, 2, false>(a, stream);
+    else if (dp == 128) b == 1 ? launch_few<128, 1, false>(a, stream) : launch_few<128, 2, false>(a, stream);
     else b == 1 ? launch_few<256, 1, false>(a, stream) : launch_few<256, 2, false>(a, stream);
   } else {
     if (dp == 64) b == 1 ? launch_few<64, 1, true>(a, stream) : launch_few<64, 2, true>(a, stream);

@@ -26,6 +26,18 @@
 namespace lora {
 namespace {
 
+#define LORA_LDS __attribute__((address_space(3)))
+template <typename T>
+__device__ __forceinline__ T lds_get(int at) {
+  typedef typename Raw<sizeof(T)>::type R;
+  return __builtin_bit_cast(T, *(const LORA_LDS R *)uintptr_t(uint32_t(at)));
+}
+template <typename T>
+__device__ __forceinline__ void lds_put(int at, const T &v) {
+  typedef typename Raw<sizeof(T)>::type R;
+  *(LORA_LDS R *)uintptr_t(uint32_t(at)) = __builtin_bit_cast(R, v);
+}
+
 // Holds the computation of x to this place: products and exponentials have no order of their own for the compiler, which
 // would gather them.
 template <typename T>
@@ -45,7 +57,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
   constexpr int kPages = 1024;                  // key blocks whose pages are looked up at once
   // LDS: K [2][64][kChunks] and V^T [2][DP][8] in pieces of 16 bytes; of 2 NW tiles the scales of K and V, [2 NW][64]
   // each, and what else is known of them; the pages of key blocks
-  extern __shared__ __align__(16) char lds[];
+  extern __shared__ __align__(1024) char lds[];
+  // (addresses as whole numbers: an exclusive or of them is an address, with no base to be added behind it)
+  const int base = int(uintptr_t((LORA_LDS char *)lds));
   constexpr int kRing = 2 * NW;
   constexpr int kV = 2 * 64 * DP * 2, kKS = 2 * kV, kVS = kKS + kRing * 256, kMeta = kVS + kRing * 256, kList = kMeta + kRing * 16;
   int *lds_pages = reinterpret_cast<int *>(lds + kList);
@@ -149,16 +163,26 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
     // row's end, or in no page, is read from elsewhere in the cache: it meets zeros of the queries, or is not seen.
     uint4 k_raw[kKPer];
     uint32_t v_raw[kVPer][4];
+    // A thread's units lie kThreads apart, whole blocks of 16 keys: what it reads and where it goes is the first unit's
+    // but for a constant.
+    constexpr int kKRows = kThreads / (DP / 16), kVQuads = kThreads / (DP / 4);
+    static_assert((kKPer == 1 || kKRows % 16 == 0) && (kVPer == 1 || kVQuads % 4 == 0), "units of a thread whole blocks apart");
+    const int k_row = tid / (DP / 16), k_byte = tid % (DP / 16) * 16, v_quad = tid / (DP / 4), v_byte = tid % (DP / 4) * 4;
+    const uint32_t k_off = uint32_t(k_row % 16 * a.pitch + (k_byte < a.pitch ? k_byte : 0));
+    const uint32_t v_off = uint32_t(v_quad % 4 * 4 * a.pitch + (v_byte < a.pitch ? v_byte : 0));
+    const int k_to = base + (k_row * kChunks + (k_byte / 8 ^ (k_row & kMask))) * 16;
+    // keys 4 quad .. of a 16-key block are places 8 (quad & 1) + 4 (quad >> 1) .. of its 16
+    const int v_to = base + kV + v_byte * 128 + ((v_quad / 4 * 2 + (v_quad & 1)) ^ (v_byte & 4) ^ (v_byte / 4 & 7)) * 16 + (v_quad >> 1 & 1) * 8;
+    auto block_at = [&](int v, int block, int page, const int8_t *values, int64_t page_bytes) {
+      const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + block * 16) & in_page);
+      return values + max(page, 0) * page_bytes + slot * a.pitch;
+    };
     auto load_k = [&](int v, const int (&pages)[kKPer]) {
 #pragma unroll
       for (int i = 0; i < kKPer; ++i) {
         const int first = i * kThreads + wave * 64;
         if (kKUnits % kThreads && first >= kKUnits) continue;
-        const int n = first + lane, r = n / (DP / 16), byte = n % (DP / 16) * 16, block = first / (DP / 16) / 16;
-        const int page = max(pages[i], 0);
-        const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + block * 16) & in_page);
-        k_raw[i] = gload_at<uint4>(a.c.k + page * a.c.k_page + slot * a.pitch,
-                                   uint32_t(r % 16 * a.pitch + (byte < a.pitch ? byte : 0)));
+        k_raw[i] = gload_at<uint4>(block_at(v, first / (DP / 16) / 16, pages[i], a.c.k, a.c.k_page), k_off);
       }
     };
     auto load_v = [&](int v, const int (&pages)[kVPer]) {
@@ -166,72 +190,65 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
       for (int i = 0; i < kVPer; ++i) {
         const int first = i * kThreads + wave * 64;
         if (kVUnits % kThreads && first >= kVUnits) continue;
-        const int n = first + lane, byte = n % (DP / 4) * 4, r = n / (DP / 4) * 4, block = first / (DP / 4) * 4 / 16;
-        const int page = max(pages[i], 0);
-        const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + block * 16) & in_page);
-        const int8_t *base = a.c.v + page * a.c.v_page + slot * a.pitch;
+        const int8_t *base = block_at(v, first / (DP / 4) / 4, pages[i], a.c.v, a.c.v_page);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v_raw[i][j] = gload_at<uint32_t>(base + j * a.pitch, uint32_t(r % 16 * a.pitch + (byte < a.pitch ? byte : 0)));
+        for (int j = 0; j < 4; ++j) v_raw[i][j] = gload_at<uint32_t>(base + j * a.pitch, v_off);
       }
     };
     // .. and widened into their buffers
     auto put_k = [&](int v) {
+      int to = k_to + ((v - v0) & 1) * (64 * DP * 2), from = base + kKS + ((v - v0) % kRing * 64 + k_row) * 4;
+      pin(to);
+      pin(from);
 #pragma unroll
       for (int i = 0; i < kKPer; ++i) {
-        const int first = i * kThreads + wave * 64;
-        if (kKUnits % kThreads && first >= kKUnits) continue;
-        const int n = first + lane, r = n / (DP / 16), chunk = n % (DP / 16) * 2;
+        if (kKUnits % kThreads && i * kThreads + wave * 64 >= kKUnits) continue;
         pin(k_raw[i].x), pin(k_raw[i].y), pin(k_raw[i].z), pin(k_raw[i].w);  // (else widened, and waited for, as soon as loaded)
         const uint32_t w[4] = {k_raw[i].x, k_raw[i].y, k_raw[i].z, k_raw[i].w};
         uint32_t h[8];
-        const float f = reinterpret_cast<const float *>(lds + kKS)[(v - v0) % kRing * 64 + r];
+        const float f = lds_get<float>(from + i * kKRows * 4);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           h[j] = pack_f16(float(int8_t(w[j / 2] >> (j % 2 * 16))) * f, float(int8_t(w[j / 2] >> (j % 2 * 16 + 8))) * f);
-        const int to = (r * kChunks + (chunk ^ (r & kMask))) * 16 + ((v - v0) & 1) * (64 * DP * 2);
-        *reinterpret_cast<uint4 *>(lds + to) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4 *>(lds + (to ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
+        lds_put(to + i * kKRows * DP * 2, make_uint4(h[0], h[1], h[2], h[3]));
+        lds_put((to ^ 16) + i * kKRows * DP * 2, make_uint4(h[4], h[5], h[6], h[7]));
       }
     };
     auto put_v = [&](int v, int j0, int j1) {  // columns j0 .. j1 - 1 of a lane's four
+      int to = v_to + ((v - v0) & 1) * (64 * DP * 2), from = base + kVS + ((v - v0) % kRing * 16 + v_quad) * 16;
+      pin(to);
+      pin(from);
 #pragma unroll
       for (int i = 0; i < kVPer; ++i) {
-        const int first = i * kThreads + wave * 64;
-        if (kVUnits % kThreads && first >= kVUnits) continue;
-        const int n = first + lane, c = n % (DP / 4), quad = n / (DP / 4);
-        const float4 f = reinterpret_cast<const float4 *>(lds + kVS)[(v - v0) % kRing * 16 + quad];
+        if (kVUnits % kThreads && i * kThreads + wave * 64 >= kVUnits) continue;
+        const float4 f = lds_get<float4>(from + i * kVQuads * 16);
 #pragma unroll
         for (int j = 0; j < 4; ++j) pin(v_raw[i][j]);
-        // keys 4 quad .. of a 16-key block are places 8 (quad & 1) + 4 (quad >> 1) .. of its 16
-        const int chunk = quad / 4 * 2 + (quad & 1), part = quad >> 1 & 1;
 #pragma unroll
         for (int j = j0; j < j1; ++j) {
           const uint32_t lo = pack_f16(float(int8_t(v_raw[i][0] >> (8 * j))) * f.x, float(int8_t(v_raw[i][1] >> (8 * j))) * f.y);
           const uint32_t hi = pack_f16(float(int8_t(v_raw[i][2] >> (8 * j))) * f.z, float(int8_t(v_raw[i][3] >> (8 * j))) * f.w);
-          const int d = 4 * c + j;
-          *reinterpret_cast<uint2 *>(lds + kV + (d * 8 + (chunk ^ ((d ^ d >> 2) & 7))) * 16 + part * 8 + ((v - v0) & 1) * (64 * DP * 2)) =
-              make_uint2(lo, hi);
+          lds_put((to ^ 16 * (j ^ i * (kVQuads / 2))) + 128 * j, make_uint2(lo, hi));
         }
       }
     };
     // Operands from LDS, kRead at a time, the next ones on their way while these are used.  Their places differ from a
     // lane's first by an exclusive or of a constant.
     constexpr int kRead = 2, kKGroups = 2 * kSteps / kRead, kVGroups = 4 * kBlocks / kRead;
-    const int k_first = (col * kChunks + (half ^ (col & kMask))) * 16;
-    const int v_first = kV + (col * 8 + (half ^ ((col ^ col >> 2) & 7))) * 16;
+    const int k_first = base + (col * kChunks + (half ^ (col & kMask))) * 16;
+    const int v_first = base + kV + (col * 8 + (half ^ ((col ^ col >> 2) & 7))) * 16;
     auto read_k = [&](int at, int g, f16x8 (&f)[kRead]) {
 #pragma unroll
       for (int j = 0; j < kRead; ++j) {
         const int kb = (kRead * g + j) / kSteps, st = (kRead * g + j) % kSteps;
-        f[j] = __builtin_bit_cast(f16x8, *reinterpret_cast<const uint4 *>(lds + (at ^ 32 * st) + kb * 32 * DP * 2));
+        f[j] = lds_get<f16x8>((at ^ 32 * st) + kb * 32 * DP * 2);
       }
     };
     auto read_v = [&](int at, int g, f16x8 (&f)[kRead]) {
 #pragma unroll
       for (int j = 0; j < kRead; ++j) {
         const int st = (kRead * g + j) / kBlocks, b = (kRead * g + j) % kBlocks;
-        f[j] = __builtin_bit_cast(f16x8, *reinterpret_cast<const uint4 *>(lds + (at ^ 32 * st) + b * 32 * 128));
+        f[j] = lds_get<f16x8>((at ^ 32 * st) + b * 32 * 128);
       }
     };
     // The scores of K tile v, and between the groups of products what `between` does.  f: the first operands.
@@ -514,8 +531,9 @@ hipError_t launch_join(const AttnArgs &a, int kind, hipStream_t stream) {
 
 hipError_t launch_attention_many(const AttnArgs &a, int dtype, hipStream_t stream) {
   if (dtype != LORA_BF16 || a.s.dp > 128) return launch_attention_exact(a, dtype, stream);
-  if (a.s.dp == 64) return launch_many<64, 8>(a, stream);
-  return launch_many<128, 8>(a, stream);
+  const bool wide = a.s.many_rows == 256;
+  if (a.s.dp == 64) return wide ? launch_many<64, 8>(a, stream) : launch_many<64, 4>(a, stream);
+  return wide ? launch_many<128, 8>(a, stream) : launch_many<128, 4>(a, stream);
 }
 
 hipError_t launch_attention(const AttnArgs &a, int dtype, hipStream_t stream) {

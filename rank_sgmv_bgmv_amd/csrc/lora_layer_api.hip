@@ -124,14 +124,19 @@ AttnShape attention_shape(const lora_attention &t, const lora_cache &c, const lo
   s.T = b.n_tokens, s.S = b.n_seqs, s.kv_heads = c.n_heads, s.group = t.n_heads / c.n_heads, s.head_dim = c.head_dim;
   s.dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
   const bool f32 = t.dtype == LORA_F32;
-  // row blocks of 16 for which the kernel for few rows has registers
-  const int blocks = f32 ? (s.dp == 256 ? 1 : 2) : (s.dp == 256 ? 2 : 4);
+  // The kernel for few rows has registers for two row blocks of 16 (one of fp32 heads beyond 128).  32 sequences that
+  // verify 4n drafted tokens over 8192 keys, 8 heads of 128, take 178 us there and 190 in the other kernel with 32 rows;
+  // with four blocks it spilled: 589 us against 204 for 48 rows.  fp32: 198 and 513 us for 32 rows of 128, 1570 against
+  // 1562 of 256.
+  const int blocks = f32 && s.dp == 256 ? 1 : 2;
   const int64_t q = b.max_q < s.T ? b.max_q : s.T, most = q * s.group;
   // all sequences are short, or those of one token are
   const int64_t few = most <= 16 * blocks ? most : s.group <= 16 * blocks ? s.group : 0;
-  s.few_blocks = few == 0 ? 0 : few <= 16 ? 1 : few <= 32 ? 2 : 4;
+  s.few_blocks = few == 0 ? 0 : few <= 16 ? 1 : 2;
   s.few_rows = 16 * s.few_blocks;
-  s.many_rows = most <= s.few_rows ? 0 : s.dp == 256 || f32 ? 128 : 256;
+  // Units of 128 rows, two workgroups a CU, where no sequence has more: 32 drafts of 24 tokens for 32 heads over 32768
+  // keys take 394 us, 417 in units of 256; a prompt of 16384 takes 1388 us in units of 256 and 1515 in those of 128.
+  s.many_rows = most <= s.few_rows ? 0 : s.dp == 256 || f32 || most <= 128 ? 128 : 256;
   const int64_t wide = int64_t(s.T) * s.group;
   s.units[ATTN_FEW] = s.few_rows ? s.S : 0;
   s.units[ATTN_MANY] = s.many_rows ? int(s.S + wide / s.many_rows) : 0;
