@@ -37,17 +37,18 @@ __device__ __forceinline__ void pin(T &x) {
 template <int DP, int NW, bool F32>
 __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnArgs a) {
   typedef std::conditional_t<F32, float, uint16_t> E;
-  constexpr int kThreads = 64 * NW, kSteps = DP / 16, kBlocks = DP / 32, kTerms = F32 ? 2 : 1;
+  constexpr int kVD = DP == 256 ? 128 : DP, kHalves = DP / kVD;  // columns of V that a workgroup takes
+  constexpr int kThreads = 64 * NW, kSteps = DP / 16, kBlocks = kVD / 32, kTerms = F32 ? 2 : 1;
   constexpr int kChunks = DP / 8;               // 16-byte pieces of a K row
   constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
   constexpr int kKUnits = 64 * DP / 16, kKPer = (kKUnits + kThreads - 1) / kThreads;
-  constexpr int kVUnits = 16 * DP / 4, kVPer = (kVUnits + kThreads - 1) / kThreads;
+  constexpr int kVUnits = 16 * kVD / 4, kVPer = (kVUnits + kThreads - 1) / kThreads;
   constexpr int kPages = 1024;                  // key blocks whose pages are looked up at once
-  // LDS: K [2][64][kChunks] and V^T [2][DP][8] in pieces of 16 bytes; of 2 NW tiles the scales of K and V, [2 NW][64]
+  // LDS: K [2][64][kChunks] and V^T [2][kVD][8] in pieces of 16 bytes; of 2 NW tiles the scales of K and V, [2 NW][64]
   // each, and what else is known of them; the pages of key blocks
   extern __shared__ __align__(16) char lds[];
   constexpr int kRing = 2 * NW;
-  constexpr int kV = 2 * 64 * DP * 2, kKS = 2 * kV, kVS = kKS + kRing * 256, kMeta = kVS + kRing * 256, kList = kMeta + kRing * 16;
+  constexpr int kV = 2 * 64 * DP * 2, kKS = kV + 2 * 64 * kVD * 2, kVS = kKS + kRing * 256, kMeta = kVS + kRing * 256, kList = kMeta + kRing * 16;
   int *lds_pages = reinterpret_cast<int *>(lds + kList);
 
   if (!plan_matches(a)) {
@@ -56,10 +57,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
   }
   const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64), col = lane % 32, half = lane / 32;
   const int kv = a.s.kv_heads, D = a.s.head_dim;
-  const int64_t n_items = int64_t(uniform(gload<int>(a.plan + A_ITEMS + ATTN_MANY))) * kv;
+  const int64_t n_items = int64_t(uniform(gload<int>(a.plan + A_ITEMS + ATTN_MANY))) * kv * kHalves;
 
   for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
-    const int item = int(it / kv), head = int(it % kv);
+    const int item = int(it / (kv * kHalves)), head = int(it / kHalves % kv), d0 = int(it % kHalves) * kVD;
     const int2 im = gload<int2>(reinterpret_cast<const char *>(a.plan) + a.s.item[ATTN_MANY] + size_t(item) * 8);
     const AttnUnit u = load_unit(a, ATTN_MANY, uniform(im.x));
     int v0, v1;
@@ -174,7 +175,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
       for (int i = 0; i < kVPer; ++i) {
         const int first = i * kThreads + wave * 64;
         if (kVUnits % kThreads && first >= kVUnits) continue;
-        const int n = first + lane, byte = n % (DP / 4) * 4, r = n / (DP / 4) * 4, block = first / (DP / 4) * 4 / 16;
+        const int n = first + lane, byte = d0 + n % (kVD / 4) * 4, r = n / (kVD / 4) * 4, block = first / (kVD / 4) * 4 / 16;
         const int page = max(uniform(lds_pages[((v - v0) * 4 + block) % kPages]), 0);
         const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + block * 16) & in_page);
         const int8_t *base = a.c.v + page * a.c.v_page + slot * a.pitch;
@@ -212,7 +213,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
       for (int i = 0; i < kVPer; ++i) {
         const int first = i * kThreads + wave * 64;
         if (kVUnits % kThreads && first >= kVUnits) continue;
-        const int n = first + lane, c = n % (DP / 4), quad = n / (DP / 4);
+        const int n = first + lane, c = n % (kVD / 4), quad = n / (kVD / 4);
         const float4 f = reinterpret_cast<const float4 *>(lds + kVS)[(v - v0) % kRing * 16 + quad];
         // keys 4 quad .. of a 16-key block are places 8 (quad & 1) + 4 (quad >> 1) .. of its 16
         const int chunk = quad / 4 * 2 + (quad & 1), part = quad >> 1 & 1;
@@ -228,7 +229,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
             hi = pack_f16(float(int8_t(v_raw[i][2] >> (8 * j))) * f.z, float(int8_t(v_raw[i][3] >> (8 * j))) * f.w);
           }
           const int d = 4 * c + j;
-          *reinterpret_cast<uint2 *>(lds + kV + (d * 8 + (chunk ^ ((d ^ d >> 2) & 7))) * 16 + part * 8 + ((v - v0) & 1) * (64 * DP * 2)) =
+          *reinterpret_cast<uint2 *>(lds + kV + (d * 8 + (chunk ^ ((d ^ d >> 2) & 7))) * 16 + part * 8 + ((v - v0) & 1) * (64 * kVD * 2)) =
               make_uint2(lo, hi);
         }
       }
@@ -353,7 +354,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
         });
         l = fmaf(sum, ldexpf(1.f, -e_v), l);
         f16x8 f[2][kRead];
-        int at = v_first + ((v - v0) & 1) * (64 * DP * 2);
+        int at = v_first + ((v - v0) & 1) * (64 * kVD * 2);
         pin(at);
         read_v(at, 0, f[0]);
 #pragma unroll
@@ -431,20 +432,20 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
         for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const int d = b * 32 + g * 8 + half * 4;
+            const int d = d0 + b * 32 + g * 8 + half * 4;
             const float f[4] = {o[b][4 * g] * inv, o[b][4 * g + 1] * inv, o[b][4 * g + 2] * inv, o[b][4 * g + 3] * inv};
             store_four(to + d, f, D - d);
           }
       } else {
         const int64_t at = (int64_t(u.slot + uniform(im.y)) * kv + head) * a.s.many_rows + (row - u.row0);
-        float *part = reinterpret_cast<float *>(a.ws + a.s.part[ATTN_MANY]) + at * DP;
+        float *part = reinterpret_cast<float *>(a.ws + a.s.part[ATTN_MANY]) + at * DP + d0;
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
           for (int g = 0; g < 4; ++g)
             gstore(part + b * 32 + g * 8 + half * 4,
                    make_float4(o[b][4 * g] * up, o[b][4 * g + 1] * up, o[b][4 * g + 2] * up, o[b][4 * g + 3] * up));
-        if (half == 0) gstore(reinterpret_cast<float *>(a.ws + a.s.stat[ATTN_MANY]) + at * 2, make_float2(M, l));
+        if (half == 0 && d0 == 0) gstore(reinterpret_cast<float *>(a.ws + a.s.stat[ATTN_MANY]) + at * 2, make_float2(M, l));
       }
     }
   }
@@ -453,10 +454,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
 template <int DP, int NW, bool F32>
 hipError_t launch_exact(const AttnArgs &a, hipStream_t stream) {
   const auto kernel = attention_exact_kernel<DP, NW, F32>;
-  constexpr size_t smem = size_t(2) * 64 * DP * 2 * 2 + 2 * NW * (512 + 16) + 4096;
+  constexpr int kHalves = DP == 256 ? 2 : 1;
+  constexpr size_t smem = size_t(2) * 64 * (DP + DP / kHalves) * 2 + 2 * NW * (512 + 16) + 4096;
   static const bool once = raise_lds_limit(reinterpret_cast<const void *>(kernel), smem);
   (void)once;
-  const int64_t items = int64_t(a.s.items[ATTN_MANY]) * a.s.kv_heads;
+  const int64_t items = int64_t(a.s.items[ATTN_MANY]) * a.s.kv_heads * kHalves;
   kernel<<<dim3(uint32_t(items < 65536 ? items : 65536)), 64 * NW, smem, stream>>>(a);
   return hipGetLastError();
 }
