@@ -253,8 +253,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
         f[j] = __builtin_bit_cast(f16x8, *reinterpret_cast<const uint4 *>(lds + (at ^ 32 * st) + b * 32 * 128));
       }
     };
-    // The scores of K tile v, and between the groups of products what `between` does.
-    auto scores = [&](int v, f32x16 (&s)[2], auto between) {
+    // The scores of K tile v.
+    auto scores = [&](int v, f32x16 (&s)[2]) {
       f16x8 f[2][kRead];
       int at = k_first + ((v - v0) & 1) * (64 * DP * 2);
       pin(at);  // (else the places of all operands are kept in registers)
@@ -273,16 +273,16 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
 #pragma unroll
           for (int t = 0; t < kTerms; ++t) s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[g % 2][j], q[t][st], s[kb], 0, 0, 0);
         }
-        pin(s[kRead * g / kSteps]);
-        between(g);
         __builtin_amdgcn_sched_barrier(0);
       }
     };
 
-    // Tile v: its scores s become weights and outputs, those of v + 1 are computed, V of v + 1 and K of v + 2 are widened.
-    // (In the last tiles what is read and put for the next ones is of no use, and does no harm.)
-    auto step = [&](int v, f32x16 (&s)[2], f32x16 (&s_next)[2]) {
+    // Tile v: its scores become weights and outputs, and tile v + 1 is widened.  (In the last tiles what is read and put for
+    // the next ones is of no use, and does no harm.)
+    auto step = [&](int v) {
       if (!idle) {
+        f32x16 s[2];
+        scores(v, s);
         const int key = tile_key(u, v), turn = (v - v0) % kRing;
         const int4 meta = reinterpret_cast<const int4 *>(lds + kMeta)[turn];
         const int word = uniform(meta.x), e_k = (word & 255) - 128, e_v = (word >> 8 & 255) - 128, bad = word >> 16;
@@ -327,31 +327,28 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
         const float less = M - float(e_v);
         float sum = 0.f;
         uint32_t r[kTerms][16];
-        scores(v + 1, s_next, [&](int g) {
-          // weights of 8 / kKGroups groups of four keys
 #pragma unroll
-          for (int n = g * 8 / kKGroups; n < (g + 1) * 8 / kKGroups; ++n) {
-            float p[4];
+        for (int n = 0; n < 8; ++n) {  // groups of four keys
+          float p[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(s[n / 4][n % 4 * 4 + i], factor, -less));
-            if constexpr (F32) {
-              sum += (p[0] + p[1]) + (p[2] + p[3]);
-              const float4 f = reinterpret_cast<const float4 *>(lds + kVS)[turn * 16 + n * 2 + half];
-              p[0] *= f.x, p[1] *= f.y, p[2] *= f.z, p[3] *= f.w;
-            }
-            r[0][2 * n] = pack_f16(p[0], p[1]), r[0][2 * n + 1] = pack_f16(p[2], p[3]);
-            if constexpr (F32) {
-              const f16x2 r0 = __builtin_bit_cast(f16x2, r[0][2 * n]), r1 = __builtin_bit_cast(f16x2, r[0][2 * n + 1]);
-              r[kTerms - 1][2 * n] = pack_f16(p[0] - float(r0.x), p[1] - float(r0.y));
-              r[kTerms - 1][2 * n + 1] = pack_f16(p[2] - float(r1.x), p[3] - float(r1.y));
-            } else {
-              // the sum takes the weights as the outputs do, rounded
-              sum = sum_f16(r[0][2 * n + 1], sum_f16(r[0][2 * n], sum));
-            }
-#pragma unroll
-            for (int t = 0; t < kTerms; ++t) pin(r[t][2 * n]), pin(r[t][2 * n + 1]);
+          for (int i = 0; i < 4; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(s[n / 4][n % 4 * 4 + i], factor, -less));
+          if constexpr (F32) {
+            sum += (p[0] + p[1]) + (p[2] + p[3]);
+            const float4 f = reinterpret_cast<const float4 *>(lds + kVS)[turn * 16 + n * 2 + half];
+            p[0] *= f.x, p[1] *= f.y, p[2] *= f.z, p[3] *= f.w;
           }
-        });
+          r[0][2 * n] = pack_f16(p[0], p[1]), r[0][2 * n + 1] = pack_f16(p[2], p[3]);
+          if constexpr (F32) {
+            const f16x2 r0 = __builtin_bit_cast(f16x2, r[0][2 * n]), r1 = __builtin_bit_cast(f16x2, r[0][2 * n + 1]);
+            r[kTerms - 1][2 * n] = pack_f16(p[0] - float(r0.x), p[1] - float(r0.y));
+            r[kTerms - 1][2 * n + 1] = pack_f16(p[2] - float(r1.x), p[3] - float(r1.y));
+          } else {
+            // the sum takes the weights as the outputs do, rounded
+            sum = sum_f16(r[0][2 * n + 1], sum_f16(r[0][2 * n], sum));
+          }
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t) pin(r[t][2 * n]), pin(r[t][2 * n + 1]);
+        }
         l = fmaf(sum, ldexpf(1.f, -e_v), l);
         f16x8 f[2][kRead];
         int at = v_first + ((v - v0) & 1) * (64 * kVD * 2);
@@ -369,20 +366,18 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
               o[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
                   f[g % 2][j], frag(r[t][4 * st], r[t][4 * st + 1], r[t][4 * st + 2], r[t][4 * st + 3]), o[b], 0, 0, 0);
           }
-#pragma unroll
-          for (int j = 0; j < kRead; ++j) pin(o[(kRead * g + j) % kBlocks]);
           // the next tiles, in pieces between the products
           if (g == kVGroups / 8) put_v(v + 1, 0, 2);
           if (g == kVGroups * 3 / 8) put_v(v + 1, 2, 4);
-          if (g == kVGroups * 5 / 8) put_k(v + 2);
+          if (g == kVGroups * 5 / 8) put_k(v + 1);
           __builtin_amdgcn_sched_barrier(0);
         }
       } else {
         put_v(v + 1, 0, 4);
-        put_k(v + 2);
+        put_k(v + 1);
       }
       if (v + 2 < v1) load_v(v + 2);
-      if (v + 3 < v1) load_k(v + 3);
+      if (v + 2 < v1) load_k(v + 2);
       if ((v - v0) % NW == 0) {
         put_scales(v + NW + wave);
         load_scales(v + 2 * NW + wave);
@@ -407,18 +402,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
       put_v(v0, 0, 4);
       if (v0 + 1 < v1) {
         load_k(v0 + 1);
-        put_k(v0 + 1);
         load_v(v0 + 1);
-        if (v0 + 2 < v1) load_k(v0 + 2);
       }
       lds_barrier();
-      f32x16 s[2][2];
-      if (!idle) scores(v0, s[0], [](int) {});
-      lds_barrier();  // the first buffer's next tile comes within the loop
-      for (int v = v0; v < v1; ++v) {
-        step(v, s[0], s[1]);
-        s[0][0] = s[1][0], s[0][1] = s[1][1];
-      }
+      for (int v = v0; v < v1; ++v) step(v);
     }
 
     // (V in float16 is value * scale / 2^eV; for fp32 value / 512 * scale / 2^eV)

@@ -153,7 +153,7 @@ AttnShape attention_shape(const lora_attention &t, const lora_cache &c, const lo
   for (int k = 0; k < ATTN_KINDS; ++k) {
     const int rows = k == ATTN_FEW ? s.few_rows : s.many_rows;
     s.target[k] = (total[k] - 1) / s.kv_heads + 1;
-    s.least[k] = 4;
+    s.least[k] = k == ATTN_FEW ? 4 : 2;
     // a unit is cut into no more than twice its share of the target, and not at all where it has few tiles
     s.cut[k] = s.units[k] && tiles > s.least[k] ? (s.units[k] < s.target[k] ? s.units[k] : s.target[k]) : 0;
     s.items[k] = s.units[k] + (s.cut[k] ? s.target[k] : 0);
