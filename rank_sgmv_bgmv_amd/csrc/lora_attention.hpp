@@ -113,6 +113,18 @@ __device__ __forceinline__ bool plan_matches(const AttnArgs &a) {
   return uniform(ok);
 }
 
+// A uniform value of which the compiler knows nothing: what depends on it is computed where it is used, and not kept in
+// registers from before the loop over the items.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+
+// Item `item` of a kind: its unit and which piece of it.
+__device__ __forceinline__ int2 load_item(const AttnArgs &a, int kind, uint32_t item) {
+  return gload<int2>(reinterpret_cast<const char *>(a.plan) + a.s.item[kind] + size_t(item) * 8);
+}
+
 __device__ __forceinline__ AttnUnit load_unit(const AttnArgs &a, int kind, int m) {
   const char *at = reinterpret_cast<const char *>(a.plan) + a.s.unit[kind] + size_t(m) * sizeof(AttnUnit);
   const int4 w0 = gload<int4>(at), w1 = gload<int4>(at + 16), w2 = gload<int4>(at + 32);
@@ -237,6 +249,12 @@ template <typename E>
 __device__ __forceinline__ E *row_at(const AttnArgs &a, const lora_heads &h, const AttnUnit &u, int kv_head, int row) {
   const int i = row / a.s.group, g = row - i * a.s.group;
   return static_cast<E *>(h.data) + int64_t(u.q0 + i) * h.token + int64_t(kv_head * a.s.group + g) * h.head;
+}
+
+// Workgroups of a kind: cache heads (times `share` that a head is divided among) x items, heads in turn, so that the units
+// of a sequence that read the same keys come to one XCD where there are 8 heads.
+inline dim3 item_grid(const AttnArgs &a, int kind, int share = 1) {
+  return dim3(uint32_t(a.s.kv_heads * share), uint32_t(a.s.items[kind] < 65535 ? a.s.items[kind] : 65535));
 }
 
 hipError_t launch_attention_few(const AttnArgs &a, int dtype, hipStream_t stream);

@@ -57,11 +57,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
   }
   const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64), col = lane % 32, half = lane / 32;
   const int kv = a.s.kv_heads, D = a.s.head_dim;
-  const int64_t n_items = int64_t(uniform(gload<int>(a.plan + A_ITEMS + ATTN_MANY))) * kv * kHalves;
+  const int n_items = uniform(gload<int>(a.plan + A_ITEMS + ATTN_MANY));
 
-  for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
-    const int item = int(it / (kv * kHalves)), head = int(it / kHalves % kv), d0 = int(it % kHalves) * kVD;
-    const int2 im = gload<int2>(reinterpret_cast<const char *>(a.plan) + a.s.item[ATTN_MANY] + size_t(item) * 8);
+  for (int item = blockIdx.y; item < n_items; item += gridDim.y) {
+    const int share = opaque(blockIdx.x), head = share / kHalves, d0 = share % kHalves * kVD;
+    const int2 im = load_item(a, ATTN_MANY, item);
     const AttnUnit u = load_unit(a, ATTN_MANY, uniform(im.x));
     int v0, v1;
     piece_tiles(u, uniform(im.y), v0, v1);
@@ -445,8 +445,7 @@ hipError_t launch_exact(const AttnArgs &a, hipStream_t stream) {
   constexpr size_t smem = size_t(2) * 64 * (DP + DP / kHalves) * 2 + 2 * NW * (512 + 16) + 4096;
   static const bool once = raise_lds_limit(reinterpret_cast<const void *>(kernel), smem);
   (void)once;
-  const int64_t items = int64_t(a.s.items[ATTN_MANY]) * a.s.kv_heads * kHalves;
-  kernel<<<dim3(uint32_t(items < 65536 ? items : 65536)), 64 * NW, smem, stream>>>(a);
+  kernel<<<item_grid(a, ATTN_MANY, kHalves), 64 * NW, smem, stream>>>(a);
   return hipGetLastError();
 }
 

@@ -51,11 +51,11 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
   }
   const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), col = lane % 16, quarter = lane / 16;
   const int kv = a.s.kv_heads, D = a.s.head_dim;
-  const int64_t n_items = int64_t(uniform(gload<int>(a.plan + A_ITEMS + ATTN_FEW))) * kv;
+  const int n_items = uniform(gload<int>(a.plan + A_ITEMS + ATTN_FEW));
 
-  for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
-    const int item = int(it / kv), head = int(it % kv);
-    const int2 im = gload<int2>(reinterpret_cast<const char *>(a.plan) + a.s.item[ATTN_FEW] + size_t(item) * 8);
+  for (int item = blockIdx.y; item < n_items; item += gridDim.y) {
+    const int head = opaque(blockIdx.x);
+    const int2 im = load_item(a, ATTN_FEW, item);
     const AttnUnit u = load_unit(a, ATTN_FEW, uniform(im.x));
     int v0, v1;
     piece_tiles(u, uniform(im.y), v0, v1);
@@ -414,8 +414,7 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
 
 template <int DP, int kBlocks, bool F32>
 void launch_few(const AttnArgs &a, hipStream_t stream) {
-  const int64_t items = int64_t(a.s.items[ATTN_FEW]) * a.s.kv_heads;
-  attention_few_kernel<DP, kBlocks, F32><<<dim3(uint32_t(items < 65536 ? items : 65536)), kFewThreads, 0, stream>>>(a);
+  attention_few_kernel<DP, kBlocks, F32><<<item_grid(a, ATTN_FEW), kFewThreads, 0, stream>>>(a);
 }
 
 }  // namespace

@@ -21,6 +21,8 @@
 // and weights are two float16 numbers each.  Maximum and sum as in the kernel
 // for few rows.
 
+#include <algorithm>
+
 #include "lora_attention.hpp"
 
 namespace lora {
@@ -70,11 +72,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
   }
   const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64), col = lane % 32, half = lane / 32;
   const int kv = a.s.kv_heads, D = a.s.head_dim;
-  const int64_t n_items = int64_t(uniform(gload<int>(a.plan + A_ITEMS + ATTN_MANY))) * kv;
+  const int n_items = uniform(gload<int>(a.plan + A_ITEMS + ATTN_MANY));
 
-  for (int64_t it = blockIdx.x; it < n_items; it += gridDim.x) {
-    const int item = int(it / kv), head = int(it % kv);
-    const int2 im = gload<int2>(reinterpret_cast<const char *>(a.plan) + a.s.item[ATTN_MANY] + size_t(item) * 8);
+  for (int item = blockIdx.y; item < n_items; item += gridDim.y) {
+    const int head = opaque(blockIdx.x);
+    const int2 im = load_item(a, ATTN_MANY, item);
     const AttnUnit u = load_unit(a, ATTN_MANY, uniform(im.x));
     int v0, v1;
     piece_tiles(u, uniform(im.y), v0, v1);
@@ -466,44 +468,54 @@ hipError_t launch_many(const AttnArgs &a, hipStream_t stream) {
   constexpr size_t smem = size_t(2) * 64 * DP * 2 * 2 + 2 * NW * (512 + 16) + 4096;
   static const bool once = raise_lds_limit(reinterpret_cast<const void *>(kernel), smem);
   (void)once;
-  const int64_t items = int64_t(a.s.items[ATTN_MANY]) * a.s.kv_heads;
-  kernel<<<dim3(uint32_t(items < 65536 ? items : 65536)), 64 * NW, smem, stream>>>(a);
+  kernel<<<item_grid(a, ATTN_MANY), 64 * NW, smem, stream>>>(a);
   return hipGetLastError();
 }
 
 constexpr int kJoinThreads = 256, kJoinRows = 16;
 
 // out = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) l_i over the pieces of a cut unit, in their order; 16 rows of a cache
-// head a workgroup.
+// head a workgroup, the cut units of both kinds in one launch.  Four pieces are on their way at once.
 template <int DP, typename E>
-__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a, int kind, int most_rows) {
-  constexpr int kCols = DP / 16;
+__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a, int first_kind, int kinds) {
+  constexpr int kCols = DP / 16, kAtOnce = 4;
+  const int kind = first_kind + blockIdx.z % kinds, head = blockIdx.y;
+  const int most_rows = kind == ATTN_FEW ? a.s.few_rows : a.s.many_rows;
+  int n = gload<int>(a.plan + A_CUT + kind);
   if (!plan_matches(a)) return;
-  const int kv = a.s.kv_heads, D = a.s.head_dim, tiles = (most_rows + kJoinRows - 1) / kJoinRows;
-  const int64_t n = int64_t(uniform(gload<int>(a.plan + A_CUT + kind))) * kv * tiles;
-  const int row_in = threadIdx.x / 16, d0 = threadIdx.x % 16 * kCols;
-  for (int64_t it = blockIdx.x; it < n; it += gridDim.x) {
-    const int tile = int(it % tiles), head = int(it / tiles % kv), cut = int(it / tiles / kv);
+  n = uniform(n);
+  const int kv = a.s.kv_heads, D = a.s.head_dim;
+  const int r = blockIdx.x * kJoinRows + threadIdx.x / 16, d0 = threadIdx.x % 16 * kCols;
+  for (int cut = blockIdx.z / kinds; cut < n; cut += gridDim.z / kinds) {
     const int m = uniform(gload<int>(reinterpret_cast<const char *>(a.plan) + a.s.cutlist[kind] + size_t(cut) * 4));
     const AttnUnit u = load_unit(a, kind, m);
-    const int r = tile * kJoinRows + row_in;
     if (r >= u.rows) continue;
     const float *part = reinterpret_cast<const float *>(a.ws + a.s.part[kind]);
     const float *stat = reinterpret_cast<const float *>(a.ws + a.s.stat[kind]);
     float M = kNoScore, l = 0.f, y[kCols];
 #pragma unroll
     for (int c = 0; c < kCols; ++c) y[c] = 0.f;
-    for (int i = 0; i < u.nsplit; ++i) {
-      const int64_t at = (int64_t(u.slot + i) * kv + head) * most_rows + r;
-      const float2 ml = gload<float2>(stat + at * 2);
-      const float top = fmaxf(M, ml.x), old = __builtin_amdgcn_exp2f(M - top), now = __builtin_amdgcn_exp2f(ml.x - top);
-      M = top;
-      l = l * old + ml.y * now;
+    for (int i0 = 0; i0 < u.nsplit; i0 += kAtOnce) {
+      float2 ml[kAtOnce];
+      float4 v[kAtOnce][kCols / 4];
 #pragma unroll
-      for (int c = 0; c < kCols; c += 4) {
-        const float4 v = gload<float4>(part + at * DP + d0 + c);
-        y[c] = y[c] * old + v.x * now, y[c + 1] = y[c + 1] * old + v.y * now;
-        y[c + 2] = y[c + 2] * old + v.z * now, y[c + 3] = y[c + 3] * old + v.w * now;
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int64_t at = (int64_t(u.slot + min(i0 + i, u.nsplit - 1)) * kv + head) * most_rows + r;
+        ml[i] = gload<float2>(stat + at * 2);
+#pragma unroll
+        for (int c = 0; c < kCols / 4; ++c) v[i][c] = gload<float4>(part + at * DP + d0 + 4 * c);
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (i0 + i >= u.nsplit) break;
+        const float top = fmaxf(M, ml[i].x), old = __builtin_amdgcn_exp2f(M - top), now = __builtin_amdgcn_exp2f(ml[i].x - top);
+        M = top;
+        l = l * old + ml[i].y * now;
+#pragma unroll
+        for (int c = 0; c < kCols / 4; ++c) {
+          y[4 * c] = y[4 * c] * old + v[i][c].x * now, y[4 * c + 1] = y[4 * c + 1] * old + v[i][c].y * now;
+          y[4 * c + 2] = y[4 * c + 2] * old + v[i][c].z * now, y[4 * c + 3] = y[4 * c + 3] * old + v[i][c].w * now;
+        }
       }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -517,13 +529,15 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
 }
 
 template <typename E>
-hipError_t launch_join(const AttnArgs &a, int kind, hipStream_t stream) {
-  const int rows = kind == ATTN_FEW ? a.s.few_rows : a.s.many_rows;
-  const int64_t n = int64_t(a.s.cut[kind]) * a.s.kv_heads * ((rows + kJoinRows - 1) / kJoinRows);
-  const dim3 grid(uint32_t(n < 16384 ? n : 16384));
-  if (a.s.dp == 64) attention_join_kernel<64, E><<<grid, kJoinThreads, 0, stream>>>(a, kind, rows);
-  else if (a.s.dp == 128) attention_join_kernel<128, E><<<grid, kJoinThreads, 0, stream>>>(a, kind, rows);
-  else attention_join_kernel<256, E><<<grid, kJoinThreads, 0, stream>>>(a, kind, rows);
+hipError_t launch_join(const AttnArgs &a, hipStream_t stream) {
+  const int few = a.s.cut[ATTN_FEW], many = a.s.cut[ATTN_MANY];
+  if (!few && !many) return hipSuccess;
+  const int first = few ? ATTN_FEW : ATTN_MANY, kinds = few && many ? 2 : 1;
+  const int most = std::max(few, many), rows = many ? a.s.many_rows : a.s.few_rows;
+  const dim3 grid((rows + kJoinRows - 1) / kJoinRows, a.s.kv_heads, most * kinds);
+  if (a.s.dp == 64) attention_join_kernel<64, E><<<grid, kJoinThreads, 0, stream>>>(a, first, kinds);
+  else if (a.s.dp == 128) attention_join_kernel<128, E><<<grid, kJoinThreads, 0, stream>>>(a, first, kinds);
+  else attention_join_kernel<256, E><<<grid, kJoinThreads, 0, stream>>>(a, first, kinds);
   return hipGetLastError();
 }
 
@@ -540,8 +554,7 @@ hipError_t launch_attention(const AttnArgs &a, int dtype, hipStream_t stream) {
   hipError_t e = hipSuccess;
   if (a.s.few_blocks) e = launch_attention_few(a, dtype, stream);
   if (e == hipSuccess && a.s.many_rows) e = launch_attention_many(a, dtype, stream);
-  for (int kind = 0; kind < ATTN_KINDS; ++kind)
-    if (e == hipSuccess && a.s.cut[kind]) e = dtype == LORA_BF16 ? launch_join<uint16_t>(a, kind, stream) : launch_join<float>(a, kind, stream);
+  if (e == hipSuccess) e = dtype == LORA_BF16 ? launch_join<uint16_t>(a, stream) : launch_join<float>(a, stream);
   return e;
 }
 

@@ -130,8 +130,9 @@ AttnShape attention_shape(const lora_attention &t, const lora_cache &c, const lo
   // 1562 of 256.
   const int blocks = f32 && s.dp == 256 ? 1 : 2;
   const int64_t q = b.max_q < s.T ? b.max_q : s.T, most = q * s.group;
-  // all sequences are short, or those of one token are
-  const int64_t few = most <= 16 * blocks ? most : s.group <= 16 * blocks ? s.group : 0;
+  // All sequences are short, or those of one token are; there are none of these where all sequences are as long as can be
+  // (else the launch costs the 4.5 us of a kernel that finds nothing to do).
+  const int64_t few = most <= 16 * blocks ? most : s.group <= 16 * blocks && s.T < s.S * q ? s.group : 0;
   s.few_blocks = few == 0 ? 0 : few <= 16 ? 1 : 2;
   s.few_rows = 16 * s.few_blocks;
   // Units of 128 rows, two workgroups a CU, where no sequence has more: 32 drafts of 24 tokens for 32 heads over 32768
