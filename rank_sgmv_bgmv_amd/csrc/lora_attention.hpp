@@ -189,34 +189,33 @@ __device__ __forceinline__ float to_float(E v) {
   else return bf_to_f(v);
 }
 
-// N values of a query head at p (any alignment of elements), of which n are there.
+// Values d0 .. d0 + N - 1 of a query head, of the D that it has (zeros behind them, and in rows that are not `live`).  No
+// lane branches: where there is nothing to read, the values at `safe`, a row of D, are read and not used.
 template <typename E, int N>
-__device__ __forceinline__ void load_query(const E *p, int n, float *f) {
-  if constexpr (sizeof(E) == 2) {
-    typedef uint32_t U __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ void load_query(const E *p, const E *safe, bool live, int d0, int D, float *f) {
+  constexpr int kWide = 16 / sizeof(E);
+  typedef uint32_t U __attribute__((ext_vector_type(4), aligned(2)));
+  const int left = live ? D - d0 : 0;
+  p += left > 0 ? d0 : 0;
+  if (D % kWide == 0) {
 #pragma unroll
-    for (int i = 0; i < N; i += 8) {
-      if (n >= i + 8) {
-        const U u = *(const LORA_GLOBAL U *)(p + i);
+    for (int i = 0; i < N; i += kWide) {
+      const bool ok = i < left;
+      const U u = *(const LORA_GLOBAL U *)(ok ? p + i : safe);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[i + 2 * j] = bf_lo(u[j]), f[i + 2 * j + 1] = bf_hi(u[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[i + j] = i + j < n ? bf_to_f(gload<uint16_t>(p + i + j)) : 0.f;
+      for (int j = 0; j < kWide; ++j) {
+        float x;
+        if constexpr (sizeof(E) == 4) x = __uint_as_float(u[j]);
+        else x = j % 2 ? bf_hi(u[j / 2]) : bf_lo(u[j / 2]);
+        f[i + j] = ok ? x : 0.f;
       }
     }
   } else {
-    typedef float U __attribute__((ext_vector_type(4), aligned(4)));
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      if (n >= i + 4) {
-        const U u = *(const LORA_GLOBAL U *)(p + i);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[i + j] = u[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f[i + j] = i + j < n ? gload<float>(p + i + j) : 0.f;
-      }
+    for (int i = 0; i < N; ++i) {
+      const bool ok = i < left;
+      const float x = to_float(gload<E>(ok ? p + i : safe));
+      f[i] = ok ? x : 0.f;
     }
   }
 }

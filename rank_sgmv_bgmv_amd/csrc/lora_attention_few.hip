@@ -45,20 +45,23 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
   __shared__ float lds_o[kFewWaves][16][kRowPitch];
   __shared__ float lds_m[kFewWaves][kBlocks * 16], lds_l[kFewWaves][kBlocks * 16];
 
+  // (what a workgroup begins with is read at once; its first item lies within the plan whatever that holds)
+  int n_items = gload<int>(a.plan + A_ITEMS + ATTN_FEW);
+  int2 im = load_item(a, ATTN_FEW, blockIdx.y);
   if (!plan_matches(a)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(a.plan + H_ERR, 1);
     return;
   }
   const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), col = lane % 16, quarter = lane / 16;
-  const int kv = a.s.kv_heads, D = a.s.head_dim;
-  const int n_items = uniform(gload<int>(a.plan + A_ITEMS + ATTN_FEW));
+  const int kv = a.s.kv_heads;
+  n_items = uniform(n_items);
 
   for (int item = blockIdx.y; item < n_items; item += gridDim.y) {
-    const int head = opaque(blockIdx.x);
-    const int2 im = load_item(a, ATTN_FEW, item);
+    const int head = opaque(blockIdx.x), D = opaque(a.s.head_dim);
     const AttnUnit u = load_unit(a, ATTN_FEW, uniform(im.x));
     int v0, v1;
-    piece_tiles(u, uniform(im.y), v0, v1);
+    const int piece = uniform(im.y);
+    piece_tiles(u, piece, v0, v1);
     const int blocks = (u.rows + 15) / 16;  // live row blocks
 
     // queries: lane (col, quarter) holds values quarter * DP / 4 .. of row col
@@ -67,13 +70,14 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
     const int p_lo = u.len - u.n, p_hi = u.len - 1;  // positions of the rows
     float shift;                                     // 2^-x of the queries' common power of two
     {
+      const E *safe = row_at<const E>(a, a.q, u, head, 0);
       float f[kBlocks][DP / 4];
       float top = 0.f;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
-        const int row = b * 16 + col, n = row < u.rows ? D - quarter * (DP / 4) : 0;
-        const E *p = n > 0 ? row_at<const E>(a, a.q, u, head, row) + quarter * (DP / 4) : nullptr;
-        load_query<E, DP / 4>(p, n, f[b]);
+        const int row = b * 16 + col;
+        const bool live = row < u.rows;
+        load_query<E, DP / 4>(row_at<const E>(a, a.q, u, head, live ? row : 0), safe, live, quarter * (DP / 4), D, f[b]);
 #pragma unroll
         for (int i = 0; i < DP / 4; ++i) {
           const float v = fabsf(f[b][i]);
@@ -124,6 +128,7 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
       ids = mine < v1 ? block_page(a, u, tile_key(u, mine) + (lane % 4) * 16) : -1;
     };
     auto page_of = [&](int turn, int kb) { return __builtin_amdgcn_readlane(ids, (turn % 16) * 4 + kb); };
+    // (what is past a row's end is read from its begin: it meets zeros of the queries, or makes outputs that are not there)
     auto load_k = [&](int v, int turn) {
       const int key = tile_key(u, v);
       bad = 0;
@@ -143,12 +148,13 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
 #pragma unroll
         for (int i = 0; i < kKB; ++i) {
           const int byte = quarter * (DP / 4) + i * 16;
-          if (byte < a.pitch) k_raw[kb][i] = gload_at<uint4>(base, uint32_t(col * a.pitch + byte));
+          k_raw[kb][i] = gload_at<uint4>(base, uint32_t(col * a.pitch + (byte < a.pitch ? byte : 0)));
         }
         ks[kb] = gload_at<float4>(a.c.k_scale + page * a.c.k_scale_page + at, uint32_t(quarter * 16));
         vs[kb] = gload_at<float4>(a.c.v_scale + page * a.c.v_scale_page + at, uint32_t(quarter * 16));
       }
     };
+    const uint32_t v_off = uint32_t(4 * quarter * a.pitch + (col * kCols < a.pitch ? col * kCols : 0));
     auto load_v = [&](int v, int turn) {
       const int key = tile_key(u, v);
 #pragma unroll
@@ -158,18 +164,17 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
         const int8_t *base = a.c.v + max(page, 0) * a.c.v_page + ((int64_t(head) << a.page_bits) + slot) * a.pitch;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t off = uint32_t((4 * quarter + i) * a.pitch + col * kCols);
           uint32_t *to = v_raw[4 * kb + i];
 #pragma unroll
           for (int j = 0; j < (kCols + 3) / 4; ++j) to[j] = 0u;
-          if (page >= 0 && col * kCols < a.pitch) {
+          if (page >= 0) {
             if constexpr (kCols == 4) {
-              to[0] = gload_at<uint32_t>(base, off);
+              to[0] = gload_at<uint32_t>(base + i * a.pitch, v_off);
             } else if constexpr (kCols == 8) {
-              const uint2 w = gload_at<uint2>(base, off);
+              const uint2 w = gload_at<uint2>(base + i * a.pitch, v_off);
               to[0] = w.x, to[1] = w.y;
             } else {
-              const uint4 w = gload_at<uint4>(base, off);
+              const uint4 w = gload_at<uint4>(base + i * a.pitch, v_off);
               to[0] = w.x, to[1] = w.y, to[2] = w.z, to[3] = w.w;
             }
           }
@@ -400,7 +405,7 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
               store_four(to + c, f, D - d0 - c);
             }
           } else {
-            const int64_t at = (int64_t(u.slot + uniform(im.y)) * kv + head) * a.s.few_rows + row;
+            const int64_t at = (int64_t(u.slot + piece) * kv + head) * a.s.few_rows + row;
             float *part = reinterpret_cast<float *>(a.ws + a.s.part[ATTN_FEW]) + at * DP + d0;
 #pragma unroll
             for (int c = 0; c < kCols; c += 4) gstore(part + c, make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]));
@@ -409,6 +414,7 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
         }
       }
     lds_barrier();  // the next item writes what was read here
+    if (item + int(gridDim.y) < n_items) im = load_item(a, ATTN_FEW, item + gridDim.y);
   }
 }
 

@@ -71,11 +71,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
     return;
   }
   const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64), col = lane % 32, half = lane / 32;
-  const int kv = a.s.kv_heads, D = a.s.head_dim;
+  const int kv = a.s.kv_heads;
   const int n_items = uniform(gload<int>(a.plan + A_ITEMS + ATTN_MANY));
 
   for (int item = blockIdx.y; item < n_items; item += gridDim.y) {
-    const int head = opaque(blockIdx.x);
+    const int head = opaque(blockIdx.x), D = opaque(a.s.head_dim);
     const int2 im = load_item(a, ATTN_MANY, item);
     const AttnUnit u = load_unit(a, ATTN_MANY, uniform(im.x));
     int v0, v1;
@@ -91,11 +91,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
     {
       float f[kSteps][8];
       float top = 0.f;
-      const E *p = row < row_end ? row_at<const E>(a, a.q, u, head, row) : nullptr;
+      const bool live = row < row_end;
+      const E *safe = row_at<const E>(a, a.q, u, head, u.row0), *p = row_at<const E>(a, a.q, u, head, live ? row : u.row0);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int d = 16 * s + 8 * half;
-        load_query<E, 8>(p + d, row < row_end ? D - d : 0, f[s]);
+        load_query<E, 8>(p, safe, live, 16 * s + 8 * half, D, f[s]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float v = fabsf(f[s][i]);
