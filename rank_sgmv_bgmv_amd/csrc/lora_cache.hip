@@ -2,9 +2,14 @@
 // and read back.
 //
 // A head is a row of its own: a = max |x|, scale = a / 127, q = rint(127 x / a),
-// by the same code as lora_quantize_rows.  kLanes lanes, a vector each, take a
-// head; nothing crosses more than a wave.  Bound by memory: each value is read
-// and written once.
+// by the same code as lora_quantize_rows.  kLanes neighbouring lanes take a head,
+// up to kVecs vectors each, and nothing crosses more than them.
+//
+// Each value is read and written once: 16997 tokens of 8 + 8 bf16 heads of 128
+// are 106 MB, 21 us at the rate of a large copy.  Writing them takes 30 us and
+// reading them back 18.5; half the vectors a lane, so twice the lanes that
+// compute addresses and scales, took 39 and 22: instructions bound the first.
+// 64 tokens take 4 and 3 us, the length of one chain of loads.
 
 #include "lora_layer.hpp"
 #include "lora_rows.hpp"
@@ -21,7 +26,7 @@ struct CacheRow {
   int head, value;  // value: 0 of the keys, 1 of the values
   __device__ __forceinline__ CacheRow(const CacheArgs &a, int64_t row) {
     const int per = 2 * a.c.n_heads;
-    token = row / per;
+    token = int64_t(a.T) * per <= 0x7fffffff ? int64_t(uint32_t(row) / uint32_t(per)) : row / per;
     const int rest = int(row - token * per);
     value = rest >= a.c.n_heads;
     head = rest - (value ? a.c.n_heads : 0);
@@ -46,85 +51,117 @@ __device__ __forceinline__ bool in_cache(const CacheArgs &a, int slot) {
   return slot >= 0 && (slot >> a.page_bits) < a.c.n_pages;
 }
 
-template <typename E, int kLanes>
+// The largest over the kLanes neighbouring lanes of a row (8, 16 or 32), by moves within the register file.
+template <int kLanes>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+#define LORA_DPP(how) v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), how, 0xf, 0xf, false)))
+  LORA_DPP(0xb1);   // neighbours
+  LORA_DPP(0x4e);   // pairs of a quad
+  LORA_DPP(0x141);  // mirrored halves of a row of 16
+  if constexpr (kLanes > 8) LORA_DPP(0x140);  // mirrored rows of 16
+#undef LORA_DPP
+  if constexpr (kLanes > 16) {
+    const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(uint32_t(s[0]), uint32_t(s[1]));
+  }
+  return v;
+}
+
+template <typename E, int kLanes, int kVecs>
 __global__ __launch_bounds__(kCacheThreads) void cache_write_kernel(CacheArgs a) {
   constexpr int kN = RowVec<E>::kN, kRows = kCacheThreads / kLanes;
-  const int lane = threadIdx.x % kLanes, c = lane * kN;
+  const int lane = threadIdx.x % kLanes;
   const int64_t rows = int64_t(a.T) * 2 * a.c.n_heads;
   for (int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / kLanes; row < rows; row += int64_t(gridDim.x) * kRows) {
     const CacheRow at(a, row);
     const int slot = gload<int>(a.slots + at.token);
-    RowVec<E> v = {{0u, 0u, 0u, 0u}};
-    if (c < a.c.head_dim) v = load_vec(at.outside<const E>(a) + c, a.c.head_dim - c);
-    uint32_t m = max_bits(v, 0u);
+    const E *from = at.outside<const E>(a);
+    RowVec<E> v[kVecs];
+    uint32_t m = 0;
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), o)));
+    for (int k = 0; k < kVecs; ++k) {
+      const int c = (k * kLanes + lane) * kN;
+      v[k] = c < a.c.head_dim ? load_vec(from + c, a.c.head_dim - c) : RowVec<E>{{0u, 0u, 0u, 0u}};
+      m = max_bits(v[k], m);
+    }
+    m = lanes_max<kLanes>(m);
     if (!in_cache(a, slot)) continue;
     const RowScale s(m, kMostBits);
-    if (c < a.pitch) store_vec(at.inside(a, slot) + c, v, s, kN);
+    int8_t *to = at.inside(a, slot);
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+      const int c = (k * kLanes + lane) * kN;
+      if (c < a.pitch) store_vec(to + c, v[k], s, kN);
+    }
     if (lane == 0) gstore(at.scale(a, slot), s.scale);
   }
 }
 
-template <typename E, int kLanes>
+template <typename E, int kLanes, int kVecs>
 __global__ __launch_bounds__(kCacheThreads) void cache_read_kernel(CacheArgs a) {
   constexpr int kN = RowVec<E>::kN, kRows = kCacheThreads / kLanes;
-  const int lane = threadIdx.x % kLanes, c = lane * kN;
+  const int lane = threadIdx.x % kLanes;
   const int64_t rows = int64_t(a.T) * 2 * a.c.n_heads;
   for (int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / kLanes; row < rows; row += int64_t(gridDim.x) * kRows) {
     const CacheRow at(a, row);
     const int slot = gload<int>(a.slots + at.token);
-    if (!in_cache(a, slot) || c >= a.c.head_dim) continue;
+    if (!in_cache(a, slot)) continue;
     const float scale = gload<float>(at.scale(a, slot));
-    const int8_t *p = at.inside(a, slot) + c;
-    uint32_t w[kN / 4];
-    if constexpr (kN == 8) {
-      const uint2 u = gload<uint2>(p);
-      w[0] = u.x, w[1] = u.y;
-    } else {
-      w[0] = gload<uint32_t>(p);
-    }
-    float f[kN];
+    const int8_t *from = at.inside(a, slot);
+    uint32_t w[kVecs][kN / 4];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) f[i] = float(int8_t(w[i / 4] >> (i % 4 * 8))) * scale;
-    E *to = at.outside<E>(a) + c;
-    const int n = a.c.head_dim - c;
-    if (n >= kN) {
-      typename RowVec<E>::U u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (kN == 8) u[i] = pack_bf2(f[2 * i], f[2 * i + 1]);
-        else u[i] = __float_as_uint(f[i]);
+    for (int k = 0; k < kVecs; ++k) {
+      const int8_t *p = from + min((k * kLanes + lane) * kN, a.pitch - kN);
+      if constexpr (kN == 8) {
+        const uint2 u = gload<uint2>(p);
+        w[k][0] = u.x, w[k][1] = u.y;
+      } else {
+        w[k][0] = gload<uint32_t>(p);
       }
-      *(LORA_GLOBAL typename RowVec<E>::U *)to = u;
-    } else {
+    }
 #pragma unroll
-      for (int i = 0; i < kN; ++i)
-        if (i < n) {
-          if constexpr (kN == 8) gstore(to + i, f_to_bf(f[i]));
-          else gstore(to + i, f[i]);
+    for (int k = 0; k < kVecs; ++k) {
+      const int c = (k * kLanes + lane) * kN, n = a.c.head_dim - c;
+      float f[kN];
+#pragma unroll
+      for (int i = 0; i < kN; ++i) f[i] = float(int8_t(w[k][i / 4] >> (i % 4 * 8))) * scale;
+      E *to = at.outside<E>(a) + c;
+      if (n >= kN) {
+        typename RowVec<E>::U u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (kN == 8) u[i] = pack_bf2(f[2 * i], f[2 * i + 1]);
+          else u[i] = __float_as_uint(f[i]);
         }
+        *(LORA_GLOBAL typename RowVec<E>::U *)to = u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          if (i < n) {
+            if constexpr (kN == 8) gstore(to + i, f_to_bf(f[i]));
+            else gstore(to + i, f[i]);
+          }
+      }
     }
   }
 }
 
-template <typename E, bool kWrite, int kLanes>
+template <typename E, bool kWrite, int kLanes, int kVecs>
 void launch_lanes(const CacheArgs &a, hipStream_t stream) {
   const int64_t rows = int64_t(a.T) * 2 * a.c.n_heads, groups = (rows - 1) / (kCacheThreads / kLanes) + 1;
   const dim3 grid(uint32_t(groups < (1 << 18) ? groups : 1 << 18));
-  if constexpr (kWrite) cache_write_kernel<E, kLanes><<<grid, kCacheThreads, 0, stream>>>(a);
-  else cache_read_kernel<E, kLanes><<<grid, kCacheThreads, 0, stream>>>(a);
+  if constexpr (kWrite) cache_write_kernel<E, kLanes, kVecs><<<grid, kCacheThreads, 0, stream>>>(a);
+  else cache_read_kernel<E, kLanes, kVecs><<<grid, kCacheThreads, 0, stream>>>(a);
 }
 
 template <typename E, bool kWrite>
 hipError_t launch_typed(const CacheArgs &a, hipStream_t stream) {
-  switch ((a.pitch - 1) / RowVec<E>::kN / 8) {  // vectors of a head, in eighths
-    case 0: launch_lanes<E, kWrite, 8>(a, stream); break;
-    case 1: launch_lanes<E, kWrite, 16>(a, stream); break;
-    case 2:
-    case 3: launch_lanes<E, kWrite, 32>(a, stream); break;
-    default: launch_lanes<E, kWrite, 64>(a, stream); break;
-  }
+  // two vectors a lane wherever eight lanes have them
+  const int vecs = (a.pitch - 1) / RowVec<E>::kN + 1;
+  if (vecs <= 8) launch_lanes<E, kWrite, 8, 1>(a, stream);
+  else if (vecs <= 16) launch_lanes<E, kWrite, 8, 2>(a, stream);
+  else if (vecs <= 32) launch_lanes<E, kWrite, 16, 2>(a, stream);
+  else launch_lanes<E, kWrite, 32, 2>(a, stream);
   return hipGetLastError();
 }
 
