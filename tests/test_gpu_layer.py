@@ -429,7 +429,7 @@ def test_attention_of_prompts(heads, kv, d, page, dtype):
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("n", [2, 4, 5, 8, 9, 16, 17, 33])
 def test_attention_rows_of_every_kernel(n, dtype):
-    """Few rows of one, two and four blocks of 16, and many."""
+    """Few rows of one and of two blocks of 16, and many."""
     Step([(n, n + 100), (1, 40), (n, n)], 4, 1, 64, 16, dtype).check()
     Step([(n, n + 100), (1, 40), (n, n)], 4, 1, 128, 16, dtype, window=50, sinks=2).check()
 
@@ -703,3 +703,176 @@ def test_cache_beyond_4_gib():
             # float32 throughout: scores to 1e-5, weights to 2^-22, sums of 512
             size = p @ vv[:, h // 2].abs() + (p @ vv[:, h // 2]).abs()
             assert bool(((out[:, h].cpu().double() - p @ vv[:, h // 2]).abs() <= 1e-4 * size).all())
+
+
+def test_attention_of_single_tokens_among_as_many_tokens_as_drafts():
+    """As many tokens as if every sequence had the most: a single token goes with the drafts, the rest belong to none."""
+    Step([(40, 100), (1, 3000)], 4, 2, 64, 16, torch.bfloat16, extra=39).check()
+    Step([(9, 100), (1, 3000), (9, 9)], 4, 1, 80, 16, torch.float32, extra=8).check()
+    Step([(24, 300), (0, 10), (1, 1)], 8, 2, 128, 16, torch.bfloat16, extra=47).check()
+
+
+# ----------------------------------------------------- as they are used together --
+class LayerRun:
+    """Norm, query, key and value projections with adapters, rotary positions, cache, attention: one layer's first half."""
+    D, HEADS, KV, HD = 256, 8, 2, 64
+
+    def __init__(self, seqs, tree=None, seed=0):
+        self.step = st = Step(seqs, self.HEADS, self.KV, self.HD, 16, torch.bfloat16, tree=tree, seed=seed)
+        st.load()
+        g = gen(seed + 100)
+        T, D, wide = st.T, self.D, (self.HEADS + 2 * self.KV) * self.HD
+        put = lambda t: t.to(torch.bfloat16).to(DEV)  # noqa: E731
+        self.x, self.r = put(torch.randn(T, D, generator=g)), put(torch.randn(T, D, generator=g))
+        self.total, self.y = torch.zeros_like(self.x), torch.zeros_like(self.x)
+        self.q8, self.scale = torch.zeros(T, D, dtype=torch.int8, device=DEV), torch.zeros(T, device=DEV)
+        self.norm = L.Norm((1 + 0.1 * torch.randn(D, generator=g)).to(DEV), 1e-5)
+        W = torch.randint(-127, 128, (wide, D), generator=g, dtype=torch.int8)
+        self.base = L.BaseWeight(W.to(DEV), torch.full((wide,), 1 / (73 * D ** 0.5), device=DEV))
+        self.pool = L.Pool(put(torch.randn(3, 16, D, generator=g) / 16), put(torch.randn(3, wide, 16, generator=g) / 8))
+        self.adapters = L.Batch(T, torch.randint(-1, 3, (T, 1), generator=g, dtype=torch.int32).to(DEV))
+        self.lora_ws = L.new_workspace(self.adapters, 3, DEV)
+        self.qkv = torch.zeros(T, wide, dtype=torch.bfloat16, device=DEV)
+        heads = self.qkv.view(T, -1, self.HD)
+        self.q, self.k, self.v = heads[:, :self.HEADS], heads[:, self.HEADS:-self.KV], heads[:, -self.KV:]
+        self.rotary = L.Rotary(torch.as_tensor(L.lora_rotary_frequencies(self.HD), dtype=torch.float64).to(DEV), self.HD)
+        self.pos, self.slots = (torch.zeros(T, dtype=torch.int32, device=DEV) for _ in range(2))
+        self.out = torch.full((T, self.HEADS, self.HD), 7.0, dtype=torch.bfloat16, device=DEV)
+        self.set_lens([x for _, x in seqs])
+
+    def set_lens(self, lens):
+        st = self.step
+        st.seqs = [(n, x) for (n, _), x in zip(st.seqs, lens)]
+        p = torch.cat([torch.arange(x - n, x) for n, x in st.seqs])
+        s = torch.cat([torch.full((n,), i) for i, (n, _) in enumerate(st.seqs)])
+        self.pos.copy_(p)
+        self.slots.copy_(st.pages[s, p // 16] * 16 + p % 16)
+        st.batch.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+
+    def run(self):
+        st = self.step
+        L.lora_attention_plan(st.attention, st.cache, st.batch, st.plan)
+        L.lora_norm_apply(self.norm, self.x, y=self.y, q=self.q8, scale=self.scale, residual=self.r, total=self.total)
+        L.lora_base_product(self.base, self.q8, self.scale, self.qkv)
+        L.lora_apply(self.pool, self.adapters, self.y, self.qkv, self.lora_ws)
+        L.lora_rotary_apply(self.rotary, self.pos, [self.q, self.k])
+        L.lora_cache_write(st.cache, self.slots, self.k, self.v)
+        L.lora_attention_apply(st.attention, st.cache, st.batch, st.plan, self.q, self.out, st.ws)
+
+    def state(self):
+        c = self.step.cache
+        return [t.clone() for t in (self.total, self.y, self.q8, self.scale, self.qkv, c.k, c.v, c.k_scale, c.v_scale, self.out)]
+
+
+SEQS = [[(1, 200), (40, 40), (3, 70)], [(1, 5000)], [(24, 300), (24, 24)], [(200, 260), (1, 16)]]
+
+
+@pytest.mark.parametrize("seqs", SEQS)
+@pytest.mark.parametrize("trees", [False, True])
+def test_layer(seqs, trees):
+    """Each of them against its formula, on what the one before it left on the device."""
+    if trees and max(n for n, _ in seqs) > 64:
+        seqs = [(60, 260), (1, 16)]
+    g = gen(5)
+    rows = [i for n, _ in seqs for i in range(n)]
+    tree = [1 << i | 1 | int(torch.randint(0, 1 << i, (1,), generator=g)) if i else 1 for i in rows] if trees else None
+    run = LayerRun(seqs, tree)
+    run.run()
+    st = run.step
+    h = run.x.cpu().double() + run.r.cpu().double()
+    total = run.total.cpu()
+    assert same(total, h.to(torch.bfloat16))
+    t = total.double()
+    y = t * run.norm.weight.cpu().double() / (t.square().mean(1, keepdim=True) + 1e-5).sqrt()
+    assert bool(((run.y.cpu().double() - y).abs() <= (half(torch.bfloat16) + V) * y.abs()).all())
+    q8, scale = ref_quantize(run.y.cpu())
+    assert same(run.q8.cpu(), q8) and same(run.scale.cpu(), scale)
+    slots = run.slots.cpu().long()
+    for heads, c, s in ((run.k, st.cache.k, st.cache.k_scale), (run.v, st.cache.v, st.cache.v_scale)):
+        q8, scale = ref_quantize(heads.cpu().reshape(-1, run.HD))
+        assert same(c.cpu()[slots // 16, :, slots % 16].reshape(-1, run.HD), q8)
+        assert same(s.cpu()[slots // 16, :, slots % 16].reshape(-1), scale)
+    st.q = run.q.cpu()
+    st.k, st.v, st.ks, st.vs = (x.cpu() for x in (st.cache.k, st.cache.v, st.cache.k_scale, st.cache.v_scale))
+    ref, tol = st.reference()
+    assert bool(((run.out.cpu().double() - ref).abs() <= tol).all())
+    assert L.lora_read_device_errors(st.plan) == 0
+
+
+def test_layer_in_a_graph():
+    """Captured once with the plan, replayed on new inputs, lengths and slots, with eager work and synchronizations between:
+    every replay leaves what an eager run leaves, in the cache too."""
+    seqs = [(1, 200), (40, 60), (3, 70), (1, 1)]
+    a, b = LayerRun(seqs), LayerRun(seqs)
+    a.run()
+    b.run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.run()
+    g = gen(3)
+    for lens in ([190, 45, 3, 16], [1, 40, 80, 1], [208, 64, 33, 2], [208, 64, 33, 2], [17, 50, 70, 9]):
+        x = torch.randn(a.x.shape, generator=g).to(torch.bfloat16).to(DEV)
+        for run in (a, b):
+            run.x.copy_(x)
+            run.set_lens(lens)
+        graph.replay()
+        b.run()
+        torch.cuda.synchronize()
+        assert all(same(s, t) for s, t in zip(a.state(), b.state())), lens
+        assert L.lora_read_device_errors(a.step.plan) == 0
+
+
+def test_layer_on_another_stream():
+    seqs = [(1, 4000), (70, 90)]
+    a, b = LayerRun(seqs), LayerRun(seqs)
+    torch.cuda.synchronize()
+    a.run()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        b.run()
+    torch.cuda.synchronize()
+    assert all(same(s, t) for s, t in zip(a.state(), b.state()))
+
+
+def test_attention_calls_at_once():
+    """Two calls on two streams that share a plan and a cache, each with a workspace of its own."""
+    st = Step([(1, 5000), (1, 300), (30, 3000)], 8, 2, 128, 16, torch.bfloat16).load()
+    g = gen(8)
+    qs = [torch.randn(st.T, 8, 128, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2)]
+    outs, want = [torch.zeros_like(q) for q in qs], []
+    for q in qs:
+        out = torch.zeros_like(q)
+        L.lora_attention_apply(st.attention, st.cache, st.batch, st.plan, q, out, st.ws)
+        want.append(out)
+    wss = [L.new_attention_workspace(st.attention, st.cache, st.batch) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for q, out, ws, stream in zip(qs, outs, wss, streams):
+            with torch.cuda.stream(stream):
+                L.lora_attention_apply(st.attention, st.cache, st.batch, st.plan, q, out, ws)
+    torch.cuda.synchronize()
+    assert all(same(out, w) for out, w in zip(outs, want))
+
+
+def test_attention_graphs_share_a_workspace():
+    """Two captured calls on one workspace, of different batches, replayed one after the other."""
+    steps = [Step(seqs, 8, 2, 128, 16, torch.bfloat16).load() for seqs in ([(1, 5000), (1, 300)], [(30, 3000), (1, 70)])]
+    ws = torch.empty(max(st.ws.numel() for st in steps), dtype=torch.uint8, device=DEV)
+    qs = [st.q.to(DEV) for st in steps]
+    outs, want, graphs = [torch.zeros_like(q) for q in qs], [], []
+    for st, q, out in zip(steps, qs, outs):
+        L.lora_attention_apply(st.attention, st.cache, st.batch, st.plan, q, out, ws)
+        want.append(out.clone())
+    torch.cuda.synchronize()
+    for st, q, out in zip(steps, qs, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            L.lora_attention_apply(st.attention, st.cache, st.batch, st.plan, q, out, ws)
+        graphs.append(graph)
+    for k in (0, 1, 1, 0, 1):
+        outs[k].zero_()
+        graphs[k].replay()
+        torch.cuda.synchronize()
+        assert same(outs[k], want[k])
