@@ -21,8 +21,6 @@
 // and weights are two float16 numbers each.  Maximum and sum as in the kernel
 // for few rows.
 
-#include <algorithm>
-
 #include "lora_attention.hpp"
 
 namespace lora {
@@ -475,21 +473,24 @@ hipError_t launch_many(const AttnArgs &a, hipStream_t stream) {
 constexpr int kJoinThreads = 256, kJoinRows = 16;
 
 // out = sum_i 2^(M_i - M) O_i / sum_i 2^(M_i - M) l_i over the pieces of a cut unit, in their order; 16 rows of a cache
-// head a workgroup, the cut units of both kinds in one launch.  Four pieces are on their way at once.
+// head a workgroup, the cut units of few rows (`few` workgroups a head) and those of many in one launch.  Four pieces are
+// on their way at once.
 template <int DP, typename E>
-__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a, int first_kind, int kinds) {
+__global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a, int few) {
   constexpr int kCols = DP / 16, kAtOnce = 4;
-  const int kind = first_kind + blockIdx.z % kinds, head = blockIdx.y;
-  const int most_rows = kind == ATTN_FEW ? a.s.few_rows : a.s.many_rows;
+  const int head = blockIdx.x % a.s.kv_heads, at_x = blockIdx.x / a.s.kv_heads;
+  const int kind = at_x < few ? ATTN_FEW : ATTN_MANY, x = at_x < few ? at_x : at_x - few;
+  const int most_rows = kind == ATTN_FEW ? a.s.few_rows : a.s.many_rows, tiles = (most_rows + kJoinRows - 1) / kJoinRows;
+  const int cut = x / tiles;
   int n = gload<int>(a.plan + A_CUT + kind);
   if (!plan_matches(a)) return;
   n = uniform(n);
   const int kv = a.s.kv_heads, D = a.s.head_dim;
-  const int r = blockIdx.x * kJoinRows + threadIdx.x / 16, d0 = threadIdx.x % 16 * kCols;
-  for (int cut = blockIdx.z / kinds; cut < n; cut += gridDim.z / kinds) {
+  const int r = x % tiles * kJoinRows + threadIdx.x / 16, d0 = threadIdx.x % 16 * kCols;
+  if (cut < n) {
     const int m = uniform(gload<int>(reinterpret_cast<const char *>(a.plan) + a.s.cutlist[kind] + size_t(cut) * 4));
     const AttnUnit u = load_unit(a, kind, m);
-    if (r >= u.rows) continue;
+    if (r >= u.rows) return;
     const float *part = reinterpret_cast<const float *>(a.ws + a.s.part[kind]);
     const float *stat = reinterpret_cast<const float *>(a.ws + a.s.stat[kind]);
     float M = kNoScore, l = 0.f, y[kCols];
@@ -530,14 +531,13 @@ __global__ __launch_bounds__(kJoinThreads) void attention_join_kernel(AttnArgs a
 
 template <typename E>
 hipError_t launch_join(const AttnArgs &a, hipStream_t stream) {
-  const int few = a.s.cut[ATTN_FEW], many = a.s.cut[ATTN_MANY];
+  const auto tiles = [&](int kind, int rows) { return a.s.cut[kind] * ((rows + kJoinRows - 1) / kJoinRows); };
+  const int few = tiles(ATTN_FEW, a.s.few_rows), many = tiles(ATTN_MANY, a.s.many_rows);
   if (!few && !many) return hipSuccess;
-  const int first = few ? ATTN_FEW : ATTN_MANY, kinds = few && many ? 2 : 1;
-  const int most = std::max(few, many), rows = many ? a.s.many_rows : a.s.few_rows;
-  const dim3 grid((rows + kJoinRows - 1) / kJoinRows, a.s.kv_heads, most * kinds);
-  if (a.s.dp == 64) attention_join_kernel<64, E><<<grid, kJoinThreads, 0, stream>>>(a, first, kinds);
-  else if (a.s.dp == 128) attention_join_kernel<128, E><<<grid, kJoinThreads, 0, stream>>>(a, first, kinds);
-  else attention_join_kernel<256, E><<<grid, kJoinThreads, 0, stream>>>(a, first, kinds);
+  const dim3 grid((few + many) * a.s.kv_heads);  // no more than 16 times the target of pieces
+  if (a.s.dp == 64) attention_join_kernel<64, E><<<grid, kJoinThreads, 0, stream>>>(a, few);
+  else if (a.s.dp == 128) attention_join_kernel<128, E><<<grid, kJoinThreads, 0, stream>>>(a, few);
+  else attention_join_kernel<256, E><<<grid, kJoinThreads, 0, stream>>>(a, few);
   return hipGetLastError();
 }
 

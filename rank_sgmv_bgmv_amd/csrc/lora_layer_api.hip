@@ -147,7 +147,11 @@ AttnShape attention_shape(const lora_attention &t, const lora_cache &c, const lo
     const int64_t seen = (int64_t(t.window) + b.max_q) / kKeyTile + 2 + (int64_t(t.sinks) + kKeyTile - 1) / kKeyTile;
     tiles = tiles < seen ? tiles : seen;
   }
-  const int total[ATTN_KINDS] = {1024, 512};
+  // Pieces of all heads that a launch aims at.  Few rows: four times as many as find room at once, which come out even
+  // however long the sequences are (64 of up to 32768 keys 531 us, 549 with half as many, 565 with four times as many).
+  // Many rows: of 256 one a CU (beside 256 single tokens four prompts of 512 after up to 4096 keys 744 us, 760 with two),
+  // of 128 three (32 drafts of 24 after up to 16384 keys 348 us; 381 with two, 357 with four, 568 with one).
+  const int total[ATTN_KINDS] = {2048, s.many_rows == 256 ? 256 : 768};
   size_t at = align256(sizeof(int) * H_WORDS), ws = 0;
   auto take = [](size_t &off, size_t bytes) { const size_t o = off; off = align256(off + bytes); return o; };
   s.toff = take(at, sizeof(int) * (size_t(s.S) + 1));
