@@ -46,15 +46,6 @@ __device__ __forceinline__ f16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32
   return __builtin_bit_cast(f16x8, u);
 }
 
-// v of the lane 32, and 16, away.
-__device__ __forceinline__ float other_half(float v) {
-  const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(threadIdx.x & 32 ? s[0] : s[1]);
-}
-__device__ __forceinline__ float other_quarter(float v) {
-  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(threadIdx.x & 16 ? s[0] : s[1]);
-}
 // over the lanes l, l ^ 32 (and the four l ^ 16, l ^ 32, l ^ 48)
 __device__ __forceinline__ float half_max(float v) {
   const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -250,10 +241,10 @@ __device__ __forceinline__ E *row_at(const AttnArgs &a, const lora_heads &h, con
   return static_cast<E *>(h.data) + int64_t(u.q0 + i) * h.token + int64_t(kv_head * a.s.group + g) * h.head;
 }
 
-// Workgroups of a kind: cache heads (times `share` that a head is divided among) x items, heads in turn, so that the units
-// of a sequence that read the same keys come to one XCD where there are 8 heads.
-inline dim3 item_grid(const AttnArgs &a, int kind, int share = 1) {
-  return dim3(uint32_t(a.s.kv_heads * share), uint32_t(a.s.items[kind] < 65535 ? a.s.items[kind] : 65535));
+// Workgroups of a kind: cache heads x items, heads in turn, so that the units of a sequence that read the same keys come to
+// one XCD where there are 8 heads.
+inline dim3 item_grid(const AttnArgs &a, int kind) {
+  return dim3(uint32_t(a.s.kv_heads), uint32_t(a.s.items[kind] < 65535 ? a.s.items[kind] : 65535));
 }
 
 hipError_t launch_attention_few(const AttnArgs &a, int dtype, hipStream_t stream);

@@ -1,25 +1,25 @@
-// Attention of many rows over the 8-bit cache (prompts, long drafts), and the
-// joining of cut units.
+// Attention of many rows over the 8-bit cache where the values of K and V stay
+// exact (fp32) or a head is longer than 128.
 //
-// A workgroup takes 32 rows a wave of a sequence's (query, query head) pairs for
-// one cache head, and goes over their key tiles of 64.  A tile is widened to
-// float16 once for all waves and laid in LDS, K as it is and V transposed, two
-// tiles in turn: while one is used the next is converted and the one after it is
-// on its way from memory.
+// As the kernel for many bf16 rows: 32 rows a wave, four waves, key tiles of 64
+// widened to float16 once for all of them and laid in LDS, two in turn.
 //
 //     S^T = K Q^T      32 x 32 x 16 products of float16: keys are rows, queries columns
 //     O^T += V^T P^T   the same; P^T comes out of S^T in the lanes that need it
 //
-// V^T's keys stand in LDS in the order in which a lane holds its weights, so
-// that an operand is 16 bytes in a row; pieces of 16 bytes are exchanged within
-// rows so that neighbouring lanes meet different banks.
+// For fp32 the 8-bit values are widened exactly, the scales meet scores and
+// weights in float32, and queries and weights are two float16 numbers each, 22
+// bits.  For bf16 the scales go into the float16 values, over a power of two
+// common to a tile (eK, eV): one rounding of at most 2^-11 a value, as the weights
+// have.  Maximum and sum as in the kernel for few rows.
 //
-// For bf16 the scales go into the float16 values, over a power of two common to
-// a tile (eK, eV): one rounding of 2^-12 a value, as many as the weights have,
-// and nothing is left to do per score but exp2.  For fp32 the 8-bit values are
-// widened exactly, the scales meet scores and weights in float32, and queries
-// and weights are two float16 numbers each.  Maximum and sum as in the kernel
-// for few rows.
+// One workgroup a CU, so one wave a SIMD with all 512 registers: the accumulators
+// stay in the upper half, where products read and write them (held to the lower
+// half by the scheduling that serves the other kernel, 711 of a tile's 1147
+// instructions were copies between the halves).  Products and the arithmetic
+// between them take turns; nothing of the next tile's runs beside them.  48 rows
+// of 32 sequences over 8192 keys, 8 heads: of 128 in fp32 377 us, of 256 in bf16
+// 801, in fp32 1406 (both of these spill, 200 and 430 bytes a lane).
 
 #include "lora_attention.hpp"
 
@@ -37,7 +37,7 @@ __device__ __forceinline__ void pin(T &x) {
 template <int DP, int NW, bool F32>
 __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnArgs a) {
   typedef std::conditional_t<F32, float, uint16_t> E;
-  constexpr int kVD = DP == 256 ? 128 : DP, kHalves = DP / kVD;  // columns of V that a workgroup takes
+  constexpr int kVD = DP == 256 ? 128 : DP;  // columns of V at a time
   constexpr int kThreads = 64 * NW, kSteps = DP / 16, kBlocks = kVD / 32, kTerms = F32 ? 2 : 1;
   constexpr int kChunks = DP / 8;               // 16-byte pieces of a K row
   constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
@@ -60,7 +60,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
   const int n_items = uniform(gload<int>(a.plan + A_ITEMS + ATTN_MANY));
 
   for (int item = blockIdx.y; item < n_items; item += gridDim.y) {
-    const int D = opaque(a.s.head_dim), share = opaque(blockIdx.x), head = share / kHalves, d0 = share % kHalves * kVD;
+    const int head = opaque(blockIdx.x), D = opaque(a.s.head_dim);
+    int d0 = 0;  // the columns of V at work
     const int2 im = load_item(a, ATTN_MANY, item);
     const AttnUnit u = load_unit(a, ATTN_MANY, uniform(im.x));
     int v0, v1;
@@ -113,11 +114,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
     const int p_hi = a.tree ? u.len - 1 : context + (min(row_first + 32, row_end) - 1) / a.s.group;
 
     f32x16 o[kBlocks];
-#pragma unroll
-    for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
-    float M = kNoScore, l = 0.f;
+    float M, l;
 
     const int in_page = (1 << a.page_bits) - 1;
     auto fetch_pages = [&](int v, int n) {  // of tiles v .. v + n - 1, to their places in the list
@@ -389,50 +386,60 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
       lds_barrier();
     };
 
-    if (v0 < v1) {
-      fetch_pages(v0, kPages / 4);
-      lds_barrier();
-      load_k(v0);
-      load_v(v0);
-      load_scales(v0 + wave);
-      put_scales(v0 + wave);
-      load_scales(v0 + NW + wave);
-      lds_barrier();
-      put_k(v0);
-      put_v(v0, 0, 4);
-      if (v0 + 1 < v1) {
-        load_k(v0 + 1);
-        load_v(v0 + 1);
+    // Heads beyond 128 go over their keys once for each half of the values, which leaves the outputs room in the registers;
+    // the queries stay, so that the outputs may take their place in memory.
+#pragma nounroll
+    for (; d0 < DP; d0 += kVD) {
+      M = kNoScore, l = 0.f;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
+      if (v0 < v1) {
+        fetch_pages(v0, kPages / 4);
+        lds_barrier();
+        load_k(v0);
+        load_v(v0);
+        load_scales(v0 + wave);
+        put_scales(v0 + wave);
+        load_scales(v0 + NW + wave);
+        lds_barrier();
+        put_k(v0);
+        put_v(v0, 0, 4);
+        if (v0 + 1 < v1) {
+          load_k(v0 + 1);
+          load_v(v0 + 1);
+        }
+        lds_barrier();
+        for (int v = v0; v < v1; ++v) step(v);
       }
-      lds_barrier();
-      for (int v = v0; v < v1; ++v) step(v);
-    }
 
-    // (V in float16 is value * scale / 2^eV; for fp32 value / 512 * scale / 2^eV)
-    l = half_sum(l);
-    const float up = F32 ? kByteScale : 1.f;
-    if (row < row_end) {
-      if (u.nsplit == 1) {
-        const float inv = l == 0.f ? 0.f : up / l;
-        E *to = row_at<E>(a, a.out, u, head, row);
+      // (V in float16 is value * scale / 2^eV; for fp32 value / 512 * scale / 2^eV)
+      l = half_sum(l);
+      const float up = F32 ? kByteScale : 1.f;
+      if (row < row_end) {
+        if (u.nsplit == 1) {
+          const float inv = l == 0.f ? 0.f : up / l;
+          E *to = row_at<E>(a, a.out, u, head, row);
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
+          for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int d = d0 + b * 32 + g * 8 + half * 4;
-            const float f[4] = {o[b][4 * g] * inv, o[b][4 * g + 1] * inv, o[b][4 * g + 2] * inv, o[b][4 * g + 3] * inv};
-            store_four(to + d, f, D - d);
-          }
-      } else {
-        const int64_t at = (int64_t(u.slot + uniform(im.y)) * kv + head) * a.s.many_rows + (row - u.row0);
-        float *part = reinterpret_cast<float *>(a.ws + a.s.part[ATTN_MANY]) + at * DP + d0;
+            for (int g = 0; g < 4; ++g) {
+              const int d = d0 + b * 32 + g * 8 + half * 4;
+              const float f[4] = {o[b][4 * g] * inv, o[b][4 * g + 1] * inv, o[b][4 * g + 2] * inv, o[b][4 * g + 3] * inv};
+              store_four(to + d, f, D - d);
+            }
+        } else {
+          const int64_t at = (int64_t(u.slot + uniform(im.y)) * kv + head) * a.s.many_rows + (row - u.row0);
+          float *part = reinterpret_cast<float *>(a.ws + a.s.part[ATTN_MANY]) + at * DP + d0;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
+          for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            gstore(part + b * 32 + g * 8 + half * 4,
-                   make_float4(o[b][4 * g] * up, o[b][4 * g + 1] * up, o[b][4 * g + 2] * up, o[b][4 * g + 3] * up));
-        if (half == 0 && d0 == 0) gstore(reinterpret_cast<float *>(a.ws + a.s.stat[ATTN_MANY]) + at * 2, make_float2(M, l));
+            for (int g = 0; g < 4; ++g)
+              gstore(part + b * 32 + g * 8 + half * 4,
+                     make_float4(o[b][4 * g] * up, o[b][4 * g + 1] * up, o[b][4 * g + 2] * up, o[b][4 * g + 3] * up));
+          if (half == 0 && d0 == 0) gstore(reinterpret_cast<float *>(a.ws + a.s.stat[ATTN_MANY]) + at * 2, make_float2(M, l));
+        }
       }
     }
   }
@@ -441,11 +448,10 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
 template <int DP, int NW, bool F32>
 hipError_t launch_exact(const AttnArgs &a, hipStream_t stream) {
   const auto kernel = attention_exact_kernel<DP, NW, F32>;
-  constexpr int kHalves = DP == 256 ? 2 : 1;
-  constexpr size_t smem = size_t(2) * 64 * (DP + DP / kHalves) * 2 + 2 * NW * (512 + 16) + 4096;
+  constexpr size_t smem = size_t(2) * 64 * (DP + (DP == 256 ? 128 : DP)) * 2 + 2 * NW * (512 + 16) + 4096;
   static const bool once = raise_lds_limit(reinterpret_cast<const void *>(kernel), smem);
   (void)once;
-  kernel<<<item_grid(a, ATTN_MANY, kHalves), 64 * NW, smem, stream>>>(a);
+  kernel<<<item_grid(a, ATTN_MANY), 64 * NW, smem, stream>>>(a);
   return hipGetLastError();
 }
 

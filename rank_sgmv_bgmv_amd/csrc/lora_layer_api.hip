@@ -126,8 +126,8 @@ AttnShape attention_shape(const lora_attention &t, const lora_cache &c, const lo
   const bool f32 = t.dtype == LORA_F32;
   // The kernel for few rows has registers for two row blocks of 16 (one of fp32 heads beyond 128).  32 sequences that
   // verify 4n drafted tokens over 8192 keys, 8 heads of 128, take 178 us there and 190 in the other kernel with 32 rows;
-  // with four blocks it spilled: 589 us against 204 for 48 rows.  fp32: 198 and 513 us for 32 rows of 128, 1570 against
-  // 1562 of 256.
+  // with four blocks it spilled: 589 us against 204 for 48 rows.  bf16 heads of 256: 576 us for 32 rows, in the other
+  // kernel 801.  fp32 heads of 128: 198 and 374 us.
   const int blocks = f32 && s.dp == 256 ? 1 : 2;
   const int64_t q = b.max_q < s.T ? b.max_q : s.T, most = q * s.group;
   // All sequences are short, or those of one token are; there are none of these where all sequences are as long as can be

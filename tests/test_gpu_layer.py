@@ -712,6 +712,15 @@ def test_attention_of_single_tokens_among_as_many_tokens_as_drafts():
     Step([(24, 300), (0, 10), (1, 1)], 8, 2, 128, 16, torch.bfloat16, extra=47).check()
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("d", [129, 200, 256])
+def test_attention_of_long_heads_in_place(d, dtype):
+    """Their values are taken in halves; all of a row's queries are read before any of its outputs is written."""
+    for seqs in ([(40, 300), (1, 5), (150, 150)], [(30, 3000), (1, 70)]):
+        step = Step(seqs, 4, 2, d, 16, dtype)
+        assert same(step.check(in_place=True), step.check())
+
+
 # ----------------------------------------------------- as they are used together --
 class LayerRun:
     """Norm, query, key and value projections with adapters, rotary positions, cache, attention: one layer's first half."""
