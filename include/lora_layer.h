@@ -172,6 +172,8 @@ lora_status lora_attention_plan(const lora_attention *attention, const lora_cach
 /* out = softmax(scale * q k^T) v over the keys that each query sees.  Scores,
  * sums and outputs are float32, the weights that meet the values are rounded
  * to 11 bits (dtype bfloat16) or 22 (float32), the output once to dtype.
+ * (With dtype bfloat16, rows that are computed many at a time meet keys and
+ * values that are rounded to 11 bits once their scales are multiplied in.)
  *   q, out  heads of the batch's rows: n_heads of head_dim values.  out may be
  *           q itself (the same strides), or memory that does not meet it
  *   plan    of lora_attention_plan for the same attention, cache sizes and

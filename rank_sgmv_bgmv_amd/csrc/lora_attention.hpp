@@ -16,6 +16,7 @@ constexpr float kNoScore = -3.0e38f;  // the running maximum before the first ke
 // the maximum is taken anew, so that float16 holds it.  Weights that are 2^-(14 + kHeadroom) of the largest and less are
 // held to a fixed 2^-(25 + kHeadroom) of it.  A slack of 7 takes a maximum anew 3 or 4 times a row instead of at every
 // new one; float32 calls, whose second float16 number begins 2^-11 lower, have the headroom instead.
+// The kernel for few rows follows every new maximum and has the float32 headroom in both types.
 template <bool F32> constexpr float kHeadroom = F32 ? 14.f : 8.f;
 template <bool F32> constexpr float kSlack = F32 ? 1.f : 7.f;
 

