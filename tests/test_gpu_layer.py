@@ -721,6 +721,34 @@ def test_attention_of_long_heads_in_place(d, dtype):
         assert same(step.check(in_place=True), step.check())
 
 
+@pytest.mark.parametrize("n, heads, dtype", [(1, 2, torch.bfloat16), (2, 40, torch.bfloat16), (1, 2, torch.float32),
+                                             (2, 20, torch.float32)])
+def test_attention_more_sequences_than_workgroups(n, heads, dtype):
+    """70000 short sequences whose queries see their own key alone: each output is that key's value, off by the rounding of
+    its weight and of the value (h each in bfloat16), of the sum (8 v) and of the output."""
+    S, d, page = 70000, 64, 16
+    T = S * n
+    g = gen(n)
+    cache = L.new_cache(S, 1, page, d, DEV)
+    pages = torch.randperm(S, generator=g).to(torch.int32)
+    slots = (pages[:, None] * page + torch.arange(n, dtype=torch.int32)).reshape(-1).to(DEV)
+    k, v = (torch.randn(T, 1, d, generator=g).to(dtype).to(DEV) for _ in range(2))
+    L.lora_cache_write(cache, slots, k, v)
+    back = [torch.empty(T, 1, d, device=DEV) for _ in range(2)]
+    L.lora_cache_read(cache, slots, *back)
+    att = L.Attention(heads, d ** -0.5, window=1, dtype=dtype)
+    batch = L.AttentionBatch(T, (torch.arange(S + 1, dtype=torch.int32) * n).to(DEV),
+                             torch.full((S,), n, dtype=torch.int32, device=DEV), pages[:, None].contiguous().to(DEV), n)
+    plan, ws = L.new_attention_plan(att, cache, batch), L.new_attention_workspace(att, cache, batch)
+    L.lora_attention_plan(att, cache, batch, plan)
+    q = torch.randn(T, heads, d, generator=g).to(dtype).to(DEV)
+    out = torch.full_like(q, 7.0)
+    L.lora_attention_apply(att, cache, batch, plan, q, out, ws)
+    assert L.lora_read_device_errors(plan) == 0
+    tol = 1.01 * (half(dtype) + 16 * V + (2 * H if dtype == torch.bfloat16 else 2 * H * H)) * back[1].abs()
+    assert bool(((out.float() - back[1]).abs() <= tol).all())
+
+
 # ----------------------------------------------------- as they are used together --
 class LayerRun:
     """Norm, query, key and value projections with adapters, rotary positions, cache, attention: one layer's first half."""
