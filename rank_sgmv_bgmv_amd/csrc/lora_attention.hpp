@@ -243,9 +243,11 @@ __device__ __forceinline__ E *row_at(const AttnArgs &a, const lora_heads &h, con
 }
 
 // Workgroups of a kind: cache heads x items, heads in turn, so that the units of a sequence that read the same keys come to
-// one XCD where there are 8 heads.
+// one XCD where there are 8 heads.  No more than 2^20 or so, however many heads and sequences there may be: each takes
+// items in turn.
 inline dim3 item_grid(const AttnArgs &a, int kind) {
-  return dim3(uint32_t(a.s.kv_heads), uint32_t(a.s.items[kind] < 65535 ? a.s.items[kind] : 65535));
+  const int most = (1 << 20) / a.s.kv_heads + 1, cap = most < 65535 ? most : 65535;
+  return dim3(uint32_t(a.s.kv_heads), uint32_t(a.s.items[kind] < cap ? a.s.items[kind] : cap));
 }
 
 hipError_t launch_attention_few(const AttnArgs &a, int dtype, hipStream_t stream);

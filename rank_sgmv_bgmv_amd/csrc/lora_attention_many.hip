@@ -3,9 +3,11 @@
 //
 // A workgroup takes 32 rows a wave of a sequence's (query, query head) pairs for
 // one cache head, and goes over their key tiles of 64.  A tile is widened to
-// float16 once for all waves and laid in LDS, K as it is and V transposed, two
-// tiles in turn: while one is used the next is converted and the one after it is
-// on its way from memory.
+// float16 once for all waves and laid in LDS, K as it is and V transposed: while
+// one is used the next is converted and the one after it is on its way from
+// memory.  Eight waves have four tiles in LDS and meet at a barrier every second
+// tile (a prompt of 16384: 1432 us, 1469 with two tiles and a barrier each), four
+// waves two tiles, so that two workgroups find room in a CU.
 //
 //     S^T = K Q^T      32 x 32 x 16 products of float16: keys are rows, queries columns
 //     O^T += V^T P^T   the same; P^T comes out of S^T in the lanes that need it
@@ -24,10 +26,10 @@
 // A step computes the scores of the next tile between the weights of this one,
 // and widens the tiles after them between the products with V, a piece after
 // each pair of products.  A prompt of 16384, window 4096, 32 heads of 128 takes
-// 1375 us, 9.6e11 operations at 0.70 POP/s where a large library product of
-// float16 reaches 1.35.  Matrix units are busy 30% of the clocks, vector units
+// 1340 to 1430 us on one card or another, 9.6e11 operations at 0.70 POP/s where a
+// large library product of float16 reaches 1.35.  Matrix units are busy 30% of the clocks, vector units
 // 45%: the two waves of a SIMD run into the same kind of work and wait for each
-// other and for the barrier of a step.  What it spends: without the products
+// other.  What it spends, of 1400 us: without the products
 // QK 236 us less, PV 226, exponentials 136, widening and loads 364.
 // 32 drafts of 24 tokens after up to 16384 keys take 329 us, 0.39 POP/s: a
 // quarter of their units' rows are empty, and 47 MB of pieces are written and
@@ -68,13 +70,15 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
   constexpr int kKUnits = 64 * DP / 16, kKPer = (kKUnits + kThreads - 1) / kThreads;
   constexpr int kVUnits = 16 * DP / 4, kVPer = (kVUnits + kThreads - 1) / kThreads;
   constexpr int kPages = 1024;                  // key blocks whose pages are looked up at once
-  // LDS: K [2][64][kChunks] and V^T [2][DP][8] in pieces of 16 bytes; of 2 NW tiles the scales of K and V, [2 NW][64]
+  // Tiles of V that are widened ahead of the one at work (of K one more), steps from one barrier to the next.
+  constexpr int kLead = NW == 8 ? 2 : 1, kBufs = 2 * kLead;
+  // LDS: K [kBufs][64][kChunks] and V^T [kBufs][DP][8] in pieces of 16 bytes; of 2 NW tiles the scales of K and V, [2 NW][64]
   // each, and what else is known of them; the pages of key blocks
   extern __shared__ __align__(1024) char lds[];
   // (addresses as whole numbers: an exclusive or of them is an address, with no base to be added behind it)
   const int base = int(uintptr_t((LORA_LDS char *)lds));
   constexpr int kRing = 2 * NW;
-  constexpr int kV = 2 * 64 * DP * 2, kKS = 2 * kV, kVS = kKS + kRing * 256, kMeta = kVS + kRing * 256, kList = kMeta + kRing * 16;
+  constexpr int kV = kBufs * 64 * DP * 2, kKS = 2 * kV, kVS = kKS + kRing * 256, kMeta = kVS + kRing * 256, kList = kMeta + kRing * 16;
   int *lds_pages = reinterpret_cast<int *>(lds + kList);
 
   if (!plan_matches(a)) {
@@ -210,7 +214,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
     };
     // .. and widened into their buffers
     auto put_k = [&](int v) {
-      int to = k_to + ((v - v0) & 1) * (64 * DP * 2), from = base + kKS + ((v - v0) % kRing * 64 + k_row) * 4;
+      int to = k_to + ((v - v0) & (kBufs - 1)) * (64 * DP * 2), from = base + kKS + ((v - v0) % kRing * 64 + k_row) * 4;
       pin(to);
       pin(from);
 #pragma unroll
@@ -228,7 +232,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
       }
     };
     auto put_v = [&](int v, int j0, int j1) {  // columns j0 .. j1 - 1 of a lane's four
-      int to = v_to + ((v - v0) & 1) * (64 * DP * 2), from = base + kVS + ((v - v0) % kRing * 16 + v_quad) * 16;
+      int to = v_to + ((v - v0) & (kBufs - 1)) * (64 * DP * 2), from = base + kVS + ((v - v0) % kRing * 16 + v_quad) * 16;
       pin(to);
       pin(from);
 #pragma unroll
@@ -266,7 +270,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
     };
     // The scores of K tile v, and between the groups of products what `between` does.  f: the first operands.
     auto first_k = [&](int v) {
-      int at = k_first + ((v - v0) & 1) * (64 * DP * 2);
+      int at = k_first + ((v - v0) & (kBufs - 1)) * (64 * DP * 2);
       pin(at);  // (else the places of all operands are kept in registers)
       return at;
     };
@@ -290,7 +294,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
       }
     };
 
-    // Tile v: its scores s become weights and outputs, those of v + 1 are computed, V of v + 1 and K of v + 2 are widened.
+    // Tile v: its scores s become weights and outputs, those of v + 1 are computed, V of v + kLead and K of the one after are widened.
     // (In the last tiles what is read and put for the next ones is of no use, and does no harm.)  What a step begins with
     // is read from LDS before the barrier in front of it: what is known of its tile, and the pages of its loads.
     int4 meta;
@@ -298,9 +302,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
     auto look_ahead = [&](int v) {
       meta = reinterpret_cast<const int4 *>(lds + kMeta)[(v - v0) % kRing];
 #pragma unroll
-      for (int i = 0; i < kKPer; ++i) page_k[i] = lds_pages[((v + 3 - v0) * 4 + (i * kThreads + wave * 64) / (DP / 16) / 16) % kPages];
+      for (int i = 0; i < kKPer; ++i) page_k[i] = lds_pages[((v + kLead + 2 - v0) * 4 + (i * kThreads + wave * 64) / (DP / 16) / 16) % kPages];
 #pragma unroll
-      for (int i = 0; i < kVPer; ++i) page_v[i] = lds_pages[((v + 2 - v0) * 4 + (i * kThreads + wave * 64) / (DP / 4) * 4 / 16) % kPages];
+      for (int i = 0; i < kVPer; ++i) page_v[i] = lds_pages[((v + kLead + 1 - v0) * 4 + (i * kThreads + wave * 64) / (DP / 4) * 4 / 16) % kPages];
     };
     auto step = [&](int v, f32x16 (&s)[2], f32x16 (&s_next)[2]) {
       const int word = uniform(meta.x), e_k = (word & 255) - 128, e_v = (word >> 8 & 255) - 128, bad = word >> 16;
@@ -346,7 +350,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
         const float less = M - float(e_v);
         float sum = 0.f;
         uint32_t r[16];
-        int at_v = v_first + ((v - v0) & 1) * (64 * DP * 2);
+        int at_v = v_first + ((v - v0) & (kBufs - 1)) * (64 * DP * 2);
         pin(at_v);
         f16x8 fv[2][kRead];
         scores(at_k, fk, s_next, [&](int g) {
@@ -376,17 +380,17 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
 #pragma unroll
           for (int j = 0; j < kRead; ++j) pin(o[(kRead * g + j) % kBlocks]);
           // the next tiles, in pieces between the products
-          if (g == kVGroups / 8) put_v(v + 1, 0, 2);
-          if (g == kVGroups * 3 / 8) put_v(v + 1, 2, 4);
-          if (g == kVGroups * 5 / 8) put_k(v + 2);
+          if (g == kVGroups / 8) put_v(v + kLead, 0, 2);
+          if (g == kVGroups * 3 / 8) put_v(v + kLead, 2, 4);
+          if (g == kVGroups * 5 / 8) put_k(v + kLead + 1);
           __builtin_amdgcn_sched_barrier(0);
         }
       } else {
-        put_v(v + 1, 0, 4);
-        put_k(v + 2);
+        put_v(v + kLead, 0, 4);
+        put_k(v + kLead + 1);
       }
-      if (v + 2 < v1) load_v(v + 2, pv);
-      if (v + 3 < v1) load_k(v + 3, pk);
+      if (v + kLead + 1 < v1) load_v(v + kLead + 1, pv);
+      if (v + kLead + 2 < v1) load_k(v + kLead + 2, pk);
       if ((v - v0) % NW == 0) {
         put_scales(v + NW + wave);
         load_scales(v + 2 * NW + wave);
@@ -396,7 +400,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
       const int next_half = (v - v0) / kHalf * kHalf + kHalf;
       if ((v - v0) % kHalf == kHalf / 2 && next_half >= 2 * kHalf && v0 + next_half < v1) fetch_pages(v0 + next_half, kHalf);
       look_ahead(v + 1);
-      lds_barrier();
+      if (kLead == 1 || (v - v0) & 1) lds_barrier();
     };
 
     if (v0 < v1) {
@@ -418,15 +422,18 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
       lds_barrier();
       put_k(v0);
       put_v(v0, 0, 4);
-      if (v0 + 1 < v1) {
-        pages_of(v0 + 1, pk, pv);
-        load_k(v0 + 1, pk);
-        put_k(v0 + 1);
-        load_v(v0 + 1, pv);
-        if (v0 + 2 < v1) {
-          pages_of(v0 + 2, pk, pv);
-          load_k(v0 + 2, pk);
+#pragma unroll
+      for (int t = 1; t <= kLead; ++t)
+        if (v0 + t < v1) {
+          pages_of(v0 + t, pk, pv);
+          load_k(v0 + t, pk);
+          load_v(v0 + t, pv);
+          put_k(v0 + t);
+          if (t < kLead) put_v(v0 + t, 0, 4);
         }
+      if (v0 + kLead + 1 < v1) {
+        pages_of(v0 + kLead + 1, pk, pv);
+        load_k(v0 + kLead + 1, pk);
       }
       lds_barrier();
       f32x16 s[2][2];
@@ -442,6 +449,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
         step(v, s[0], s[1]);
         s[0][0] = s[1][0], s[0][1] = s[1][1];
       }
+      if (kLead == 2 && (v1 - v0) & 1) lds_barrier();  // the next item writes what the last step read
     }
 
     // (V in float16 is value * scale / 2^eV)
@@ -476,7 +484,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
 template <int DP, int NW>
 hipError_t launch_many(const AttnArgs &a, hipStream_t stream) {
   const auto kernel = attention_many_kernel<DP, NW>;
-  constexpr size_t smem = size_t(2) * 64 * DP * 2 * 2 + 2 * NW * (512 + 16) + 4096;
+  constexpr size_t smem = size_t(NW == 8 ? 4 : 2) * 64 * DP * 2 * 2 + 2 * NW * (512 + 16) + 4096;
   static const bool once = raise_lds_limit(reinterpret_cast<const void *>(kernel), smem);
   (void)once;
   kernel<<<item_grid(a, ATTN_MANY), 64 * NW, smem, stream>>>(a);

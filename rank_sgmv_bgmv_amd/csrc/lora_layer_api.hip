@@ -158,6 +158,8 @@ AttnShape attention_shape(const lora_attention &t, const lora_cache &c, const lo
   for (int k = 0; k < ATTN_KINDS; ++k) {
     const int rows = k == ATTN_FEW ? s.few_rows : s.many_rows;
     s.target[k] = (total[k] - 1) / s.kv_heads + 1;
+    // (four tiles are one a wave of few rows: a request of 4097 keys takes 17.1 us, 19.3 with two or eight; seven fp32
+    // drafts of many rows 41.7 us with two, 47 with four, 55 with one, a second round)
     s.least[k] = k == ATTN_FEW ? 4 : 2;
     // a unit is cut into no more than twice its share of the target, and not at all where it has few tiles
     s.cut[k] = s.units[k] && tiles > s.least[k] ? (s.units[k] < s.target[k] ? s.units[k] : s.target[k]) : 0;
