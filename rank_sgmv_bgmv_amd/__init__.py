@@ -684,34 +684,50 @@ def lora_norm_apply(norm: Norm, x, y=None, q=None, scale=None, residual=None, to
     """h = x + residual (x without one), kept in total if given; y = h weight / sqrt(mean h^2 + eps), kept in y if given;
     the rows of y in 8 bits in q and scale if given (lora_quantize_rows).  x, residual, total, y [T][d] of one type
     (bfloat16 or float32), q int8 [T][d], scale float32 [T]; y or q or both.  total may be x or residual, y may be x."""
-    what, index, d = "lora_norm_apply", norm.index, norm.d
-    dtype = x.dtype
-    code = _REAL.get(dtype, -1) if _torch() else -1
+    torch, index, d = _torch(), norm.index, norm.d
+    dtype, shape, int8 = x.dtype, x.shape, torch.int8
+    ldx = _rows_like(x, dtype, index, shape)
+    ldr = 0 if residual is None else _rows_like(residual, dtype, index, shape)
+    ldt = 0 if total is None else _rows_like(total, dtype, index, shape)
+    ldy = 0 if y is None else _rows_like(y, dtype, index, shape)
+    ldq = 0 if q is None else _rows_like(q, int8, index, shape)
+    code = _REAL.get(dtype, -1)
+    if (ldx < d or (residual is not None and ldr < d) or (total is not None and ldt < d) or (y is not None and ldy < d)
+            or (q is not None and ldq < d) or code < 0 or shape[1] != d or shape[0] > _INT32_MAX):
+        ldx, ldr, ldt, ldy, ldq = _norm_rows(norm, x, residual, total, y, q, code)
+    T = shape[0]
+    if scale is not None and not _line(scale, torch.float32, index, T):
+        _vector("lora_norm_apply", "scale", scale, torch.float32, norm.device, T)
+    _launch(index, "lora_norm_apply", lib().lora_norm_apply, norm.ref, x.data_ptr(), ldx,
+            None if residual is None else residual.data_ptr(), ldr, None if total is None else total.data_ptr(), ldt,
+            None if y is None else y.data_ptr(), ldy, None if q is None else q.data_ptr(), ldq,
+            None if scale is None else scale.data_ptr(), T, code)
+
+
+def _rows_like(t, dtype, index: int, shape) -> int:
+    """The row stride of a tensor of this shape, type and device with unit column stride; 0 if t is not plainly one."""
+    s = t.stride()
+    return s[0] if t.dtype is dtype and t.get_device() == index and t.shape == shape and len(s) == 2 and s[1] == 1 else 0
+
+
+def _norm_rows(norm: Norm, x, residual, total, y, q, code: int):
+    """The row strides of lora_norm_apply's tensors, each checked by itself."""
+    what, d, dtype = "lora_norm_apply", norm.d, x.dtype
     if code < 0:
         raise LoraError(-2, f"{what}: x must be bfloat16 or float32 (got {dtype})")
-    ldx = _row(x, dtype, index)
-    if ldx < d or x.shape[1] != d:
-        ldx = _rows_2d(what, "x", x, (dtype,), norm.device, d)
+    lds = [_rows_2d(what, "x", x, (dtype,), norm.device, d)]
     T = x.shape[0]
     if x.shape[1] != d:
         raise LoraError(-2, f"{what}: x must be [T][{d}]")
-    if T > _INT32_MAX:
-        _fits_32(what, T)
-    args = [x.data_ptr(), ldx]
-    for name, t, kind in (("residual", residual, dtype), ("total", total, dtype), ("y", y, dtype),
-                          ("q", q, _torch().int8)):
+    _fits_32(what, T)
+    for name, t, kind in (("residual", residual, dtype), ("total", total, dtype), ("y", y, dtype), ("q", q, _torch().int8)):
         if t is None:
-            args += (None, 0)
+            lds.append(0)
             continue
-        ld = _row(t, kind, index)
-        if ld < d or t.shape[1] != d or t.shape[0] != T:
-            if t.dim() != 2 or tuple(t.shape) != (T, d):
-                raise LoraError(-2, f"{what}: {name} must be [{T}][{d}] (got {tuple(t.shape)})")
-            ld = _rows_2d(what, name, t, (kind,), norm.device, d, T)
-        args += (t.data_ptr(), ld)
-    if scale is not None and not _line(scale, _torch().float32, index, T):
-        _vector(what, "scale", scale, _torch().float32, norm.device, T)
-    _launch(index, what, lib().lora_norm_apply, norm.ref, *args, None if scale is None else scale.data_ptr(), T, code)
+        if t.dim() != 2 or tuple(t.shape) != (T, d):
+            raise LoraError(-2, f"{what}: {name} must be [{T}][{d}] (got {tuple(t.shape)})")
+        lds.append(_rows_2d(what, name, t, (kind,), norm.device, d, T))
+    return lds
 
 
 def lora_cache_pitch(head_dim: int) -> int:
@@ -756,13 +772,12 @@ def new_cache(n_pages: int, heads: int, page_size: int, head_dim: int, device) -
     return Cache(k, v, torch.zeros(shape, device=device), torch.zeros(shape, device=device), head_dim)
 
 
-def _head_bytes(what: str, name: str, t, dtype, index: int, T: int, heads: int, d: int) -> bytes:
-    """A tensor [T][heads][d] with a head's values side by side, as the bytes of a lora_heads."""
-    shape, s = t.shape, t.stride()
-    if (t.dtype is not dtype or t.get_device() != index or len(shape) != 3 or shape[0] != T or shape[1] != heads
-            or shape[2] != d or (s[2] != 1 and d > 1)):
-        raise LoraError(-2, f"{what}: {name} must be {dtype} [{T}][{heads}][{d}] on device {index}, a head's values side "
-                            f"by side (got {t.dtype} {tuple(shape)} on {t.device}, strides {s})")
+def _head_bytes(what: str, name: str, t, dtype, index: int, shape) -> bytes:
+    """A tensor of this shape, [T][heads][d], with a head's values side by side, as the bytes of a lora_heads."""
+    s = t.stride()
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or (s[2] != 1 and shape[2] > 1):
+        raise LoraError(-2, f"{what}: {name} must be {dtype} {list(shape)} on device {index}, a head's values side "
+                            f"by side (got {t.dtype} {list(t.shape)} on {t.device}, strides {s})")
     return _pack_heads(t.data_ptr(), s[0], s[1])
 
 
@@ -775,8 +790,9 @@ def _cache_call(what: str, f, cache: Cache, slots, k, v):
     code = _REAL.get(k.dtype, -1)
     if code < 0:
         raise LoraError(-2, f"{what}: k and v must be bfloat16 or float32 (got {k.dtype})")
-    kb = _head_bytes(what, "k", k, k.dtype, cache.index, T, cache.heads, cache.head_dim)
-    vb = _head_bytes(what, "v", v, k.dtype, cache.index, T, cache.heads, cache.head_dim)
+    shape = (T, cache.heads, cache.head_dim)
+    kb = _head_bytes(what, "k", k, k.dtype, cache.index, shape)
+    vb = _head_bytes(what, "v", v, k.dtype, cache.index, shape)
     _launch(cache.index, what, f, cache.ref, slots.data_ptr(), T, kb, vb, code)
 
 
@@ -876,9 +892,9 @@ def lora_attention_apply(attention: Attention, cache: Cache, batch: AttentionBat
     for name, t in (("plan", plan), ("ws", ws)):
         if not _line(t, torch.uint8, index, 0):
             _vector(what, name, t, torch.uint8, batch.device, 0)
-    T, heads, d = batch.T, attention.heads, cache.head_dim
-    qb = _head_bytes(what, "q", q, attention.dtype, index, T, heads, d)
-    ob = _head_bytes(what, "out", out, attention.dtype, index, T, heads, d)
+    shape = (batch.T, attention.heads, cache.head_dim)
+    qb = _head_bytes(what, "q", q, attention.dtype, index, shape)
+    ob = _head_bytes(what, "out", out, attention.dtype, index, shape)
     _launch(index, what, lib().lora_attention_apply, attention.ref, cache.ref, batch.ref, plan.data_ptr(), plan.shape[0], qb,
             ob, ws.data_ptr(), ws.shape[0])
 
