@@ -148,16 +148,18 @@ __device__ __forceinline__ int tile_key(const AttnUnit &u, int v) {
 struct RowSight {
   int pos, first_end;  // position; the end of the first keys that stay visible
   uint64_t mask;       // the drafted tokens of a tree
+  // (no lane branches, as for the queries: rows that are not there read the first one's mask)
   __device__ __forceinline__ void set(const AttnArgs &a, const AttnUnit &u, int row) {
-    const int i = row / a.s.group, context = u.len - u.n;
-    pos = -1, mask = 0;
-    if (row < u.row0 + u.rows) {
-      pos = context + i;
-      if (a.tree) {
-        mask = gload<uint64_t>(a.tree + u.q0 + i) & (~uint64_t(0) >> (LORA_MAX_TREE - u.n));
-        pos = context + __popcll(mask & ((uint64_t(1) << i) - 1));
-      }
+    const bool live = row < u.row0 + u.rows;
+    const int i = (live ? row : u.row0) / a.s.group, context = u.len - u.n;
+    int at = context + i;
+    mask = 0;
+    if (a.tree) {
+      mask = gload<uint64_t>(a.tree + u.q0 + i) & (~uint64_t(0) >> (LORA_MAX_TREE - u.n));
+      at = context + __popcll(mask & ((uint64_t(1) << i) - 1));
+      mask = live ? mask : 0;
     }
+    pos = live ? at : -1;
     first_end = min(a.sinks, pos + 1);
   }
   // (keys are not negative, so that none is within the window of a negative position)
