@@ -124,11 +124,13 @@ AttnShape attention_shape(const lora_attention &t, const lora_cache &c, const lo
   s.T = b.n_tokens, s.S = b.n_seqs, s.kv_heads = c.n_heads, s.group = t.n_heads / c.n_heads, s.head_dim = c.head_dim;
   s.dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
   const bool f32 = t.dtype == LORA_F32;
-  // The kernel for few rows has registers for two row blocks of 16 (one of fp32 heads beyond 128).  32 sequences that
-  // verify 4n drafted tokens over 8192 keys, 8 heads of 128, take 178 us there and 190 in the other kernel with 32 rows;
-  // with four blocks it spilled: 589 us against 204 for 48 rows.  bf16 heads of 256: 576 us for 32 rows, in the other
-  // kernel 801.  fp32 heads of 128: 198 and 374 us.
-  const int blocks = f32 && s.dp == 256 ? 1 : 2;
+  // The kernel for few rows has registers for two row blocks of 16 (one of fp32 heads beyond 128); with four it spilled:
+  // 48 rows of heads of 128 589 us against 204 in the other kernel.  Where both serve, 32 rows of 8 cache heads over 8192
+  // keys, bf16 heads of 128: one sequence 22 us here and 26 there, four 55 and 57, 32 of them 197 and 159 (heads of 64:
+  // 19 and 21, 141 and 103).  32 sequences with heads of 256: 578 and 765; fp32 heads of 64: 150 and 236, of 128: 220
+  // and 343.
+  const bool one = f32 ? s.dp == 256 : s.dp <= 128 && int64_t(s.S) * s.kv_heads > 32;
+  const int blocks = one ? 1 : 2;
   const int64_t q = b.max_q < s.T ? b.max_q : s.T, most = q * s.group;
   // All sequences are short, or those of one token are; there are none of these where all sequences are as long as can be
   // (else the launch costs the 4.5 us of a kernel that finds nothing to do).

@@ -435,6 +435,14 @@ def test_attention_rows_of_every_kernel(n, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("d", [64, 128, 200])
+def test_attention_of_many_short_drafts(d, dtype):
+    """17 to 32 rows of more sequences than go with the kernel for few rows in bfloat16."""
+    Step([(8, 8 + 7 * i) for i in range(36)], 4, 1, d, 16, dtype).check()
+    Step([(5 + i % 4, 8 + 5 * i) for i in range(20)] + [(1, 90)], 8, 2, d, 16, dtype, window=60, sinks=1).check()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("heads", [16, 17, 32, 33, 64, 65, 130])
 def test_attention_many_query_heads(heads, dtype):
     Step([(1, 100), (1, 3), (2, 70)], heads, 1, 64, 16, dtype).check()
