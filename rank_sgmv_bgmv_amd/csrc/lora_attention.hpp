@@ -19,6 +19,10 @@ constexpr float kNoScore = -3.0e38f;  // the running maximum before the first ke
 // The kernel for few rows follows every new maximum and has the float32 headroom in both types.
 template <bool F32> constexpr float kHeadroom = F32 ? 14.f : 8.f;
 template <bool F32> constexpr float kSlack = F32 ? 1.f : 7.f;
+// Kernels that sum weights after their rounding do so in tiles whose value exponent is no more than this below the largest
+// of the tiles before: what a key's weight can lose there is 2^-(25 + kHeadroom - kLowTile) of a row's sum, 2^-31.  (A tile
+// of zeros, whose exponent is -60, behind one of ordinary values would lose all of it.)
+constexpr int kLowTile = 2;
 
 // Two bytes of u (8-bit values plus 128, so 0 .. 255) as float16, (u - 128) /
 // 512 each.  The bytes are taken as the float16 numbers u * 2^-24 that their
@@ -181,6 +185,14 @@ template <typename E>
 __device__ __forceinline__ float to_float(E v) {
   if constexpr (sizeof(E) == 4) return v;
   else return bf_to_f(v);
+}
+
+// A lane's part of a tile's sum of 2^(score - M), from its 32 products s and what they are multiplied with.
+__device__ __forceinline__ float sum_exact(const f32x16 (&s)[2], float factor, float M) {
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) sum += __builtin_amdgcn_exp2f(fmaf(s[i / 16][i % 16], factor, -M));
+  return sum;
 }
 
 // Values d0 .. d0 + N - 1 of a query head, of the D that it has (zeros behind them, and in rows that are not `live`).  No

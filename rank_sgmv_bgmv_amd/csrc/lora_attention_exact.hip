@@ -11,7 +11,8 @@
 // weights in float32, and queries and weights are two float16 numbers each, 22
 // bits.  For bf16 the scales go into the float16 values, over a power of two
 // common to a tile (eK, eV): one rounding of at most 2^-11 a value, as the weights
-// have.  Maximum and sum as in the kernel for few rows.
+// have, and maximum and sum are those of that kernel; fp32 has them as the kernel
+// for few rows.
 //
 // One workgroup a CU, so one wave a SIMD with all 512 registers: the accumulators
 // stay in the upper half, where products read and write them (held to the lower
@@ -115,6 +116,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
 
     f32x16 o[kBlocks];
     float M, l;
+    int e_most;  // the largest eV of the piece's tiles so far
 
     const int in_page = (1 << a.page_bits) - 1;
     auto fetch_pages = [&](int v, int n) {  // of tiles v .. v + n - 1, to their places in the list
@@ -322,6 +324,9 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
           for (int b = 0; b < kBlocks; ++b) o[b] *= fade;
         }
         const float less = M - float(e_v);
+        e_most = max(e_most, e_v);
+        const bool low = !F32 && e_v < e_most - kLowTile;
+        if (low) l += sum_exact(s, factor, M);
         float sum = 0.f;
         uint32_t r[kTerms][16];
 #pragma unroll
@@ -346,7 +351,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
 #pragma unroll
           for (int t = 0; t < kTerms; ++t) pin(r[t][2 * n]), pin(r[t][2 * n + 1]);
         }
-        l = fmaf(sum, ldexpf(1.f, -e_v), l);
+        l = fmaf(sum, low ? 0.f : ldexpf(1.f, -e_v), l);
         f16x8 f[2][kRead];
         int at = v_first + ((v - v0) & 1) * (64 * kVD * 2);
         pin(at);
@@ -390,7 +395,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
     // the queries stay, so that the outputs may take their place in memory.
 #pragma nounroll
     for (; d0 < DP; d0 += kVD) {
-      M = kNoScore, l = 0.f;
+      M = kNoScore, l = 0.f, e_most = -128;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll

@@ -20,8 +20,10 @@
 // (eK, eV): one rounding of at most 2^-11 a value, as the weights have, and
 // nothing is left to do per score but exp2.  With t = scale k.q log2 e + eV the
 // weights are w = 2^(t - M), rounded to float16, and l = sum w 2^-eV takes them
-// rounded, so that weights and sum err alike.  M follows the running maximum
-// only when that has risen by 2^kSlack.
+// rounded, so that weights and sum err alike; where a tile's eV is so far below
+// an earlier one's that they would lose more than that, l = sum 2^(t - M - eV)
+// in float32.  M follows the running maximum only when that has risen by
+// 2^kSlack.
 //
 // A step computes the scores of the next tile between the weights of this one,
 // and widens the tiles after them between the products with V, a piece after
@@ -140,6 +142,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
     float M = kNoScore, l = 0.f;
+    int e_most = -128;  // the largest eV of the piece's tiles so far
 
     const int in_page = (1 << a.page_bits) - 1;
     auto fetch_pages = [&](int v, int n) {  // of tiles v .. v + n - 1, to their places in the list
@@ -348,6 +351,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
           for (int b = 0; b < kBlocks; ++b) o[b] *= fade;
         }
         const float less = M - float(e_v);
+        e_most = max(e_most, e_v);
+        const bool low = e_v < e_most - kLowTile;
+        if (low) l += sum_exact(s, factor, M);
         float sum = 0.f;
         uint32_t r[16];
         int at_v = v_first + ((v - v0) & (kBufs - 1)) * (64 * DP * 2);
@@ -366,7 +372,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
           }
           if (g == kKGroups - 1) read_v(at_v, 0, fv[0]);
         });
-        l = fmaf(sum, ldexpf(1.f, -e_v), l);
+        l = fmaf(sum, low ? 0.f : ldexpf(1.f, -e_v), l);
 #pragma unroll
         for (int g = 0; g < kVGroups; ++g) {
           if (g + 1 < kVGroups) read_v(at_v, g + 1, fv[(g + 1) % 2]);
