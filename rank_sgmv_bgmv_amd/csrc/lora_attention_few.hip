@@ -228,7 +228,9 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
       }
       const bool poisoned = __any(nans != 0);
 
-      // kPart key blocks of 16 at a time
+      // kPart key blocks of 16 at a time.  (Products are made for every row block, live or not.  With those of the second
+      // behind a branch the compiler counted the wait between a product and the first read of its result along the longer
+      // way alone: where the branch was taken, scores were read before they were there.)
 #pragma unroll
       for (int k0 = 0; k0 < 4; k0 += kPart) {
         // scores
@@ -249,11 +251,9 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
                                                        __builtin_shufflevector(h[2], h[3], 0, 1, 2, 3), 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
-              if (b == 0 || b < blocks) {
 #pragma unroll
-                for (int t = 0; t < kTerms; ++t)
-                  s[kb][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf16, q[b][t][st], s[kb][b], 0, 0, 0);
-              }
+              for (int t = 0; t < kTerms; ++t)
+                s[kb][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf16, q[b][t][st], s[kb][b], 0, 0, 0);
           }
         }
         if (k0 + kPart == 4 && next < v1) {
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
           load_k(next, turn + 1);
         }
         // weights
-        f16x8 w[kBlocks][kTerms][kPart / 2];
+        f16x8 w[kBlocks][kTerms][kPart / 2] = {};
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
           if (b == 0 || b < blocks) {
@@ -350,11 +350,9 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
                                                      __builtin_shufflevector(x[2], x[3], 0, 1, 2, 3), 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
-              if (b == 0 || b < blocks) {
 #pragma unroll
-                for (int t = 0; t < kTerms; ++t)
-                  o[b][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[b][t][h], o[b][c], 0, 0, 0);
-              }
+              for (int t = 0; t < kTerms; ++t)
+                o[b][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[b][t][h], o[b][c], 0, 0, 0);
           }
       }
       if (next < v1) load_v(next, turn + 1);

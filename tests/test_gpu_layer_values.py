@@ -19,6 +19,17 @@ def scale_keys(step, which, s, keys, factor):
     t[page, :, j % step.page] = t[page, :, j % step.page] * factor
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("d", [64, 128, 200, 256])
+def test_attention_of_single_tokens_among_drafts(d, dtype):
+    """Sequences of one row block in a launch for two, with and without masked tiles."""
+    for window, sinks in ((0, 0), (60, 1)):
+        Step([(8, 8 + 7 * i) for i in range(3)] + [(1, x) for x in (90, 1, 64, 63, 200)], 4, 1, d, 16, dtype, window=window,
+             sinks=sinks).check()
+        Step([(5 + i % 4, 8 + 5 * i) for i in range(20)] + [(1, 90), (1, 64), (2, 300)], 8, 2, d, 16, dtype, window=window,
+             sinks=sinks).check()
+
+
 # ------------------------------------------------- tiles whose values are small --
 @pytest.mark.parametrize("dtype", TYPES, ids=ids)
 @pytest.mark.parametrize("d", [64, 128, 200])
