@@ -136,8 +136,11 @@ typedef struct {
  * its own place), and sees keys j < lens[s] - n as above; the window does not
  * hide drafted tokens.
  *
- * Pages that no query sees are not looked up and may be anything.  Keys of a
- * page outside 0 .. n_pages - 1 are not seen.  A query that sees nothing gets
+ * Pages that no query sees are not looked up and may be anything, and so may
+ * slots of other pages that none sees (behind a sequence's last key, say; they
+ * need never have been written).  Keys of a page outside 0 .. n_pages - 1 are
+ * not seen.  A key that has NaN, an infinity or a negative number for a scale
+ * makes the outputs of its head NaN that see it.  A query that sees nothing gets
  * zeros; rows that belong to no sequence are left as they were. */
 typedef struct {
   int32_t n_tokens, n_seqs;

@@ -11,6 +11,8 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+constexpr uint32_t kNoScale = 0x7f800000u;  // from these bits on: infinite, NaN or negative
+
 constexpr float kNoScore = -3.0e38f;  // the running maximum before the first key
 // The largest weight of a row is 2^kHeadroom when its maximum is taken, and no more than 2^(kHeadroom + kSlack) before
 // the maximum is taken anew, so that float16 holds it.  Weights that are 2^-(14 + kHeadroom) of the largest and less are
@@ -137,9 +139,25 @@ __device__ __forceinline__ void piece_tiles(const AttnUnit &u, int part, int &v0
   v1 = int(int64_t(u.ntiles) * (part + 1) / u.nsplit);
 }
 
-// Which page a block of 16 keys lies in; -1 where its keys are not seen: past the sequence's end, or no page of the cache.
-__device__ __forceinline__ int block_page(const AttnArgs &a, const AttnUnit &u, int key) {
-  if (key >= u.len) return -1;
+// The keys that a unit's rows see, one or another of them: lo .. hi - 1, and below hi the first keys of the sequence.
+// Scales of others, which a former request may have left or nobody may ever have written, are not used for anything.
+struct UnitKeys {
+  int lo, hi;
+  // (first, last: the first and last query)
+  __device__ __forceinline__ void set(const AttnArgs &a, const AttnUnit &u, int first, int last) {
+    const int context = u.len - u.n, p = context + (a.tree ? 0 : first);
+    lo = p >= a.window ? p - a.window + 1 : 0;
+    hi = a.tree ? u.len : min(u.len, context + last + 1);
+  }
+  // whether one of the keys key .. key + more is seen
+  __device__ __forceinline__ bool seen(const AttnArgs &a, int key, int more = 0) const {
+    return key < hi && (key + more >= lo || key < a.sinks);
+  }
+};
+
+// Which page a block of 16 keys lies in; -1 where no row sees its keys, or in no page of the cache.
+__device__ __forceinline__ int block_page(const AttnArgs &a, const AttnUnit &u, const UnitKeys &keys, int key) {
+  if (!keys.seen(a, key, 15)) return -1;
   const int p = gload<int>(a.pages + int64_t(u.seq) * a.ld_pages + (key >> a.page_bits));
   return p >= 0 && p < a.c.n_pages ? p : -1;
 }

@@ -72,6 +72,8 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
     // queries: lane (col, quarter) holds values quarter * DP / 4 .. of row col
     f16x8 q[kBlocks][kTerms][kSteps];
     RowSight sight[kBlocks];
+    UnitKeys keys;
+    keys.set(a, u, 0, u.n - 1);
     const int p_lo = u.len - u.n, p_hi = u.len - 1;  // positions of the rows
     float shift;                                     // 2^-x of the queries' common power of two
     {
@@ -126,11 +128,11 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
     int ids = -1;
     uint4 k_raw[4][kKB];
     uint32_t v_raw[16][(kCols + 3) / 4];
-    float4 ks[4], vs[4];
+    float ks[4][4], vs[4][4];
     uint32_t bad = 0;  // key blocks of the loaded tile whose keys are not seen
     auto load_ids = [&](int v) {
       const int mine = v + (lane / 4) * kFewWaves;
-      ids = mine < v1 ? block_page(a, u, tile_key(u, mine) + (lane % 4) * 16) : -1;
+      ids = mine < v1 ? block_page(a, u, keys, tile_key(u, mine) + (lane % 4) * 16) : -1;
     };
     auto page_of = [&](int turn, int kb) { return __builtin_amdgcn_readlane(ids, (turn % 16) * 4 + kb); };
     // (what is past a row's end is read from its begin: it meets zeros of the queries, or makes outputs that are not there)
@@ -141,7 +143,8 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
       for (int kb = 0; kb < 4; ++kb) {
         const int page = page_of(turn, kb);
         const int slot = (key + kb * 16) & ((1 << a.page_bits) - 1);
-        ks[kb] = vs[kb] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ks[kb][i] = vs[kb][i] = 0.f;
 #pragma unroll
         for (int i = 0; i < kKB; ++i) k_raw[kb][i] = make_uint4(0u, 0u, 0u, 0u);
         if (page < 0) {
@@ -155,8 +158,10 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
           const int byte = quarter * (DP / 4) + i * 16;
           k_raw[kb][i] = gload_at<uint4>(base, uint32_t(col * a.pitch + (byte < a.pitch ? byte : 0)));
         }
-        ks[kb] = gload_at<float4>(a.c.k_scale + page * a.c.k_scale_page + at, uint32_t(quarter * 16));
-        vs[kb] = gload_at<float4>(a.c.v_scale + page * a.c.v_scale_page + at, uint32_t(quarter * 16));
+        const float4 k4 = gload_at<float4>(a.c.k_scale + page * a.c.k_scale_page + at, uint32_t(quarter * 16));
+        const float4 v4 = gload_at<float4>(a.c.v_scale + page * a.c.v_scale_page + at, uint32_t(quarter * 16));
+        ks[kb][0] = k4.x, ks[kb][1] = k4.y, ks[kb][2] = k4.z, ks[kb][3] = k4.w;
+        vs[kb][0] = v4.x, vs[kb][1] = v4.y, vs[kb][2] = v4.z, vs[kb][3] = v4.w;
       }
     };
     const uint32_t v_off = uint32_t(4 * quarter * a.pitch + (col * kCols < a.pitch ? col * kCols : 0));
@@ -201,30 +206,39 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
       // the tile's exponent, and its scales
       float kf[4][4], vm[4][4];
       int e;
-      uint32_t nans = 0;  // keys whose values are NaN
+      uint32_t nans = 0;  // keys whose scales are none
       {
-        float top = 0.f;
-        bool any = false;
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-          any = any || vs[kb].x != vs[kb].x || vs[kb].y != vs[kb].y || vs[kb].z != vs[kb].z || vs[kb].w != vs[kb].w;
-          top = fmaxf(top, fmaxf(fmaxf(vs[kb].x, vs[kb].y), fmaxf(vs[kb].z, vs[kb].w)));
-        }
-        if (__any(any)) {
+        if (!whole) {
 #pragma unroll
           for (int kb = 0; kb < 4; ++kb)
-            nans |= ((vs[kb].x != vs[kb].x ? 1u : 0u) | (vs[kb].y != vs[kb].y ? 2u : 0u) | (vs[kb].z != vs[kb].z ? 4u : 0u) |
-                     (vs[kb].w != vs[kb].w ? 8u : 0u)) << (4 * kb);
-        }
-        e = uniform(tile_exponent(quarters_max(top)));
-        const float down = ldexpf(1.f, -e);
-        // (the maximum makes a NaN zero: the rows that see it get theirs from the weight)
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
-          kf[kb][0] = ks[kb].x * score, kf[kb][1] = ks[kb].y * score, kf[kb][2] = ks[kb].z * score, kf[kb][3] = ks[kb].w * score;
-          vm[kb][0] = fmaxf(vs[kb].x, 0.f) * down, vm[kb][1] = fmaxf(vs[kb].y, 0.f) * down;
-          vm[kb][2] = fmaxf(vs[kb].z, 0.f) * down, vm[kb][3] = fmaxf(vs[kb].w, 0.f) * down;
+            for (int i = 0; i < 4; ++i) vs[kb][i] = keys.seen(a, key + kb * 16 + quarter * 4 + i) ? vs[kb][i] : 0.f;
         }
+        // (the bits of floats that are not negative are in their order)
+        uint32_t top = 0, most = 0;
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(vs[kb][i])), most = max(most, __float_as_uint(ks[kb][i]));
+        if (__any(max(top, most) >= kNoScale)) {
+          // (such values become zeros: the rows that see them get their NaN from the weight)
+          top = 0;
+#pragma unroll
+          for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const bool none = __float_as_uint(vs[kb][i]) >= kNoScale;
+              nans |= none || __float_as_uint(ks[kb][i]) >= kNoScale ? 1u << (4 * kb + i) : 0u;
+              vs[kb][i] = none ? 0.f : vs[kb][i];
+              top = max(top, __float_as_uint(vs[kb][i]));
+            }
+        }
+        e = uniform(tile_exponent(quarters_max(__uint_as_float(top))));
+        const float down = ldexpf(1.f, -e);
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) kf[kb][i] = ks[kb][i] * score, vm[kb][i] = vs[kb][i] * down;
       }
       const bool poisoned = __any(nans != 0);
 

@@ -131,6 +131,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
       }
     }
     const float score = a.scale * shift;
+    UnitKeys keys;
+    keys.set(a, u, u.row0 / a.s.group, (row_end - 1) / a.s.group);
     // positions of the wave's rows
     const int context = u.len - u.n;
     const int p_lo = a.tree ? context : context + row_first / a.s.group;
@@ -148,7 +150,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
     auto fetch_pages = [&](int v, int n) {  // of tiles v .. v + n - 1, to their places in the list
       for (int i = tid; i < 4 * n; i += kThreads) {
         const int t = v + i / 4;
-        lds_pages[((v - v0) * 4 + i) % kPages] = t < v1 ? block_page(a, u, tile_key(u, t) + (i % 4) * 16) : -1;
+        lds_pages[((v - v0) * 4 + i) % kPages] = t < v1 ? block_page(a, u, keys, tile_key(u, t) + (i % 4) * 16) : -1;
       }
     };
 
@@ -158,20 +160,19 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
     auto load_scales = [&](int v) {
       const int page = v < v1 ? lds_pages[((v - v0) * 4 + lane / 16) % kPages] : -1;
       sk = sv = 0;
-      if (page >= 0) {
+      if (page >= 0 && keys.seen(a, tile_key(u, v) + lane)) {
         const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + lane) & in_page);
         sk = gload<uint32_t>(a.c.k_scale + page * a.c.k_scale_page + slot);
         sv = gload<uint32_t>(a.c.v_scale + page * a.c.v_scale_page + slot);
       }
     };
     auto put_scales = [&](int v) {
-      constexpr uint32_t kInf = 0x7f800000u;
       const int at = (v - v0) % kRing;
-      const uint64_t seen = __ballot(lds_pages[((v - v0) * 4 + lane / 16) % kPages] >= 0), nan = __ballot(sv > kInf);
-      const uint32_t v_fine = sv > kInf ? 0u : sv, k_fine = sk > kInf ? 0u : sk;
+      const uint64_t seen = __ballot(lds_pages[((v - v0) * 4 + lane / 16) % kPages] >= 0), nan = __ballot(sv >= kNoScale);
+      const uint32_t v_fine = sv >= kNoScale ? 0u : sv, k_fine = sk >= kNoScale ? 0u : sk;
       const int e_k = tile_exponent(__uint_as_float(wave_max_bits(k_fine))), e_v = tile_exponent(__uint_as_float(wave_max_bits(v_fine)));
-      // (NaN scales of V become zeros: the rows that see the key get their NaN from its score)
-      const float ks = __uint_as_float(sk);
+      // (scales of V that are none become zeros: the rows that see the key get their NaN from its score)
+      const float ks = sk >= kNoScale ? __builtin_nanf("") : __uint_as_float(sk);
       reinterpret_cast<float *>(lds + kKS)[at * 64 + lane] = ks * ldexpf(1.f, -e_k);
       reinterpret_cast<float *>(lds + kVS)[at * 64 + lane] = __uint_as_float(v_fine) * ldexpf(1.f, -e_v);
       const int hidden = (seen & 1 ? 0 : 1) | (seen >> 16 & 1 ? 0 : 2) | (seen >> 32 & 1 ? 0 : 4) | (seen >> 48 & 1 ? 0 : 8);

@@ -3,7 +3,7 @@ slots that nobody sees hold anything.  The reference and its tolerances are thos
 import pytest
 import torch
 
-from test_gpu_layer import TYPES, Step, ids
+from test_gpu_layer import TYPES, Step, ids, same
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,83 @@ def test_attention_values_that_shrink_from_tile_to_tile(dtype):
                 for t in range(0, x, 64):
                     scale_keys(step, "vs", s, range(t, min(t + 64, x)), factor ** (t // 64))
             step.check()
+
+
+# ------------------------------------------------------ slots that nobody sees --
+ODD = [1e30, 1e-30, float("inf"), -float("inf"), -3.0, float("nan")]
+
+
+def fill_unseen(step, value, pages=True):
+    """Scales of keys that no query of the batch sees, in the pages of those that are seen and (pages) in the whole of the
+    others; what is in them is what a former request left."""
+    seen = torch.zeros(step.k.shape[0], step.page, dtype=torch.bool)
+    for s, (n, x) in enumerate(step.seqs):
+        any_row = torch.stack([step.sees(s, i) for i in range(n)]).any(0)
+        j = torch.arange(x)[any_row]
+        seen[step.pages[s].long()[j // step.page], j % step.page] = True
+    if not pages:
+        seen |= ~seen.any(1, keepdim=True)
+    for t in (step.ks, step.vs):
+        t.transpose(1, 2)[~seen] = value
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("value", ODD, ids=str)
+@pytest.mark.parametrize("d", [64, 128, 200])
+def test_attention_slots_behind_a_sequence_may_hold_anything(d, value, dtype):
+    """Never written, or left by a former request: the same bits as with ordinary scales there."""
+    for seqs in ([(1, 50), (3, 17), (2, 129), (1, 16)], [(100, 250), (40, 41)], [(2, 5003)], [(60, 3001)]):
+        step = Step(seqs, 4, 2, d, 16, dtype)
+        clean = step.check()
+        fill_unseen(step, value)
+        assert same(step.run(), clean)
+        step = Step(seqs, 4, 2, d, 64, dtype)
+        clean = step.run()
+        fill_unseen(step, value)
+        assert same(step.run(), clean)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("value", ODD, ids=str)
+@pytest.mark.parametrize("window, sinks", [(100, 5), (37, 0), (1, 70), (130, 129)])
+def test_attention_slots_before_a_window_may_hold_anything(window, sinks, value, dtype):
+    for seqs in ([(1, 1000), (1, 700), (2, 333)], [(20, 900), (50, 401)], [(130, 700)]):
+        for page in (16, 64):
+            step = Step(seqs, 4, 2, 64, page, dtype, window=window, sinks=sinks)
+            clean = step.check()
+            fill_unseen(step, value)
+            assert same(step.run(), clean)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("value", ODD, ids=str)
+def test_attention_pages_that_are_not_seen_may_be_any_page(value, dtype):
+    """Entries of the page table that no query sees name a page of scales that would do harm."""
+    for seqs in ([(1, 1000), (2, 333)], [(20, 900), (50, 401)]):
+        step = Step(seqs, 4, 2, 64, 16, dtype, window=100, sinks=5)
+        clean = step.check()
+        free = sorted(set(range(step.k.shape[0])) - set(step.pages.flatten().tolist()))[0]
+        step.ks[free] = step.vs[free] = value
+        for s, (n, x) in enumerate(seqs):
+            live = torch.zeros(step.pages.shape[1], dtype=torch.bool)
+            live[0] = True
+            live[(x - n - 100 + 1) // 16:-(-x // 16)] = True
+            step.pages[s, ~live] = free
+        assert same(step.run(), clean)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("value", ODD[2:], ids=str)
+@pytest.mark.parametrize("which", ["ks", "vs"])
+def test_attention_a_key_without_a_finite_scale(which, value, dtype):
+    """Scales that are no scales make the rows NaN that see the key, in its cache head, and no others."""
+    for seqs in ([(4, 150)], [(100, 150)]):
+        step = Step(seqs, 4, 2, 64, 16, dtype)
+        n, x = seqs[0]
+        getattr(step, which)[int(step.pages[0, (x - 2) // 16]), 1, (x - 2) % 16] = value
+        got = step.run()
+        want = torch.zeros(n, 4, dtype=torch.bool)
+        want[n - 2:, 2:] = True
+        assert torch.equal(got.isnan().all(2), want) and torch.equal(got.isnan().any(2), want)
+        ref, tol = Step(seqs, 4, 2, 64, 16, dtype).reference()
+        assert bool(((got.double() - ref).abs() <= tol)[~want].all())
