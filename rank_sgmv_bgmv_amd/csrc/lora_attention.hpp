@@ -96,9 +96,13 @@ __device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
 }
 
 // An exponent e with |v| in [2^(e-1), 2^e), held to -60 .. 100: what tiles are scaled by on their way to float16.
+constexpr int kLeastExponent = -60;
 __device__ __forceinline__ int tile_exponent(float v) {
-  return v > 0.f ? min(max(__builtin_amdgcn_frexp_expf(v), -60), 100) : -60;
+  return v > 0.f ? min(max(__builtin_amdgcn_frexp_expf(v), kLeastExponent), 100) : kLeastExponent;
 }
+// Scales of a tile that are less than 2^-kSpread of its largest would lose bits to it (an 8-bit value over 2^13 is a normal
+// float16 number), which a row may not even see: in such a tile each key has an exponent of its own.
+constexpr int kSpread = 12;
 
 // The plan made for this call.
 __device__ __forceinline__ bool plan_matches(const AttnArgs &a) {
@@ -205,11 +209,39 @@ __device__ __forceinline__ float to_float(E v) {
   else return bf_to_f(v);
 }
 
-// A lane's part of a tile's sum of 2^(score - M), from its 32 products s and what they are multiplied with.
-__device__ __forceinline__ float sum_exact(const f32x16 (&s)[2], float factor, float M) {
+// What is kept of the keys of a tile that have exponents of their own: those of K and of V, less the tile's.
+__device__ __forceinline__ uint32_t pack_exponents(int k, int v) { return uint32_t(k & 0xffff) | uint32_t(v) << 16; }
+__device__ __forceinline__ int k_exponent(uint32_t e) { return int(int16_t(e)); }
+__device__ __forceinline__ int v_exponent(uint32_t e) { return int(e) >> 16; }
+
+// A lane's products of such a tile become scores plus exponents of V (less the tile's).  e: the tile's, groups of four keys
+// a lane, two groups apart.
+__device__ __forceinline__ void scale_apart(f32x16 (&s)[2], float factor, const uint4 *e) {
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const uint4 w = e[2 * n];
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      s[n / 4][n % 4 * 4 + i] = fmaf(s[n / 4][n % 4 * 4 + i], ldexpf(factor, k_exponent(x[i])), float(v_exponent(x[i])));
+  }
+}
+
+// A lane's part of a tile's sum of 2^(score - M), from its 32 products s and what they are multiplied with; apart: from what
+// scale_apart made of them.
+__device__ __forceinline__ float sum_exact(const f32x16 (&s)[2], float factor, float M, bool apart, const uint4 *e) {
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) sum += __builtin_amdgcn_exp2f(fmaf(s[i / 16][i % 16], factor, -M));
+  for (int n = 0; n < 8; ++n) {
+    uint32_t x[4] = {0u, 0u, 0u, 0u};
+    if (apart) {
+      const uint4 w = e[2 * n];
+      x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sum += __builtin_amdgcn_exp2f(fmaf(s[n / 4][n % 4 * 4 + i], factor, -M) - float(v_exponent(x[i])));
+  }
   return sum;
 }
 

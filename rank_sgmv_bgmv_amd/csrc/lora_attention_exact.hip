@@ -46,11 +46,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
   constexpr int kVUnits = 16 * kVD / 4, kVPer = (kVUnits + kThreads - 1) / kThreads;
   constexpr int kPages = 1024;                  // key blocks whose pages are looked up at once
   // LDS: K [2][64][kChunks] and V^T [2][kVD][8] in pieces of 16 bytes; of 2 NW tiles the scales of K and V, [2 NW][64]
-  // each, and what else is known of them; the pages of key blocks
+  // each, what else is known of them and (where they differ much) the keys' exponents; the pages of key blocks
   extern __shared__ __align__(16) char lds[];
   constexpr int kRing = 2 * NW;
-  constexpr int kV = 2 * 64 * DP * 2, kKS = kV + 2 * 64 * kVD * 2, kVS = kKS + kRing * 256, kMeta = kVS + kRing * 256, kList = kMeta + kRing * 16;
+  constexpr int kV = 2 * 64 * DP * 2, kKS = kV + 2 * 64 * kVD * 2, kVS = kKS + kRing * 256, kMeta = kVS + kRing * 256, kExps = kMeta + kRing * 16, kList = kExps + kRing * 256;
   int *lds_pages = reinterpret_cast<int *>(lds + kList);
+  const uint4 *exps = reinterpret_cast<const uint4 *>(lds + kExps) + threadIdx.x % 64 / 32;  // of a lane's keys
 
   if (!plan_matches(a)) {
     if (!a.s.few_blocks && blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(a.plan + H_ERR, 1);  // (else counted there)
@@ -147,11 +148,18 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
       const int e_k = tile_exponent(__uint_as_float(wave_max_bits(k_fine))), e_v = tile_exponent(__uint_as_float(wave_max_bits(v_fine)));
       // (scales of V that are none become zeros: the rows that see the key get their NaN from its score)
       const float ks = sk >= kNoScale ? __builtin_nanf("") : __uint_as_float(sk);
-      reinterpret_cast<float *>(lds + kKS)[at * 64 + lane] = F32 ? ks : ks * ldexpf(1.f, -e_k);
-      reinterpret_cast<float *>(lds + kVS)[at * 64 + lane] = __uint_as_float(v_fine) * ldexpf(1.f, -e_v);
+      int x_k = e_k, x_v = e_v;
+      const int own_k = tile_exponent(__uint_as_float(k_fine)), own_v = tile_exponent(__uint_as_float(v_fine));
+      const bool apart = __any((!F32 && k_fine && own_k < e_k - kSpread) || (v_fine && own_v < e_v - kSpread));
+      if (apart) {
+        x_k = own_k, x_v = own_v;
+        reinterpret_cast<uint32_t *>(lds + kExps)[at * 64 + lane] = pack_exponents(F32 ? 0 : x_k - e_k, x_v - e_v);
+      }
+      reinterpret_cast<float *>(lds + kKS)[at * 64 + lane] = F32 ? ks : ks * ldexpf(1.f, -x_k);
+      reinterpret_cast<float *>(lds + kVS)[at * 64 + lane] = __uint_as_float(v_fine) * ldexpf(1.f, -x_v);
       const int hidden = (seen & 1 ? 0 : 1) | (seen >> 16 & 1 ? 0 : 2) | (seen >> 32 & 1 ? 0 : 4) | (seen >> 48 & 1 ? 0 : 8);
       if (lane == 0)
-        reinterpret_cast<int4 *>(lds + kMeta)[at] = make_int4((e_k + 128) | (e_v + 128) << 8 | hidden << 16, 0, int(nan), int(nan >> 32));
+        reinterpret_cast<int4 *>(lds + kMeta)[at] = make_int4((e_k + 128) | (e_v + 128) << 8 | hidden << 16 | int(apart) << 20, 0, int(nan), int(nan >> 32));
     };
 
     // Raw values of a tile of K and one of V on their way.  A wave's rows lie in one block of 16 keys.  What is past a
@@ -285,7 +293,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
         scores(v, s);
         const int key = tile_key(u, v), turn = (v - v0) % kRing;
         const int4 meta = reinterpret_cast<const int4 *>(lds + kMeta)[turn];
-        const int word = uniform(meta.x), e_k = (word & 255) - 128, e_v = (word >> 8 & 255) - 128, bad = word >> 16;
+        const int word = uniform(meta.x), e_k = (word & 255) - 128, e_v = (word >> 8 & 255) - 128, bad = word >> 16 & 15;
+        const bool apart = word >> 20;
         const uint64_t nan = uint32_t(uniform(meta.z)) | uint64_t(uint32_t(uniform(meta.w))) << 32;
         const bool whole = bad == 0 && nan == 0 && all_seen(a, u, key, p_lo, p_hi);
         if constexpr (F32) {
@@ -296,6 +305,12 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
               const float4 f = reinterpret_cast<const float4 *>(lds + kKS)[turn * 16 + kb * 8 + g * 2 + half];
               s[kb][4 * g] *= f.x, s[kb][4 * g + 1] *= f.y, s[kb][4 * g + 2] *= f.z, s[kb][4 * g + 3] *= f.w;
             }
+        }
+        // (held away from zero, where a hidden key's score would be NaN; it is what scores near zero are multiplied with)
+        float factor = fminf(fmaxf(F32 ? score : ldexpf(score, e_k), 1e-37f), 1e37f);
+        if (apart) {
+          scale_apart(s, factor, exps + turn * 16);
+          factor = 1.f;
         }
         if (!whole) {
           uint32_t seen = 0, hit = 0;
@@ -311,8 +326,6 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
             s[i / 16][i % 16] = seen >> i & 1 ? x : -__builtin_inff();
           }
         }
-        // (held away from zero, where a hidden key's score would be NaN; it is what scores near zero are multiplied with)
-        const float factor = fminf(fmaxf(F32 ? score : ldexpf(score, e_k), 1e-37f), 1e37f);
         float top = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
@@ -326,8 +339,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
         }
         const float less = M - float(e_v);
         e_most = max(e_most, e_v);
-        const bool low = !F32 && e_v < e_most - kLowTile;
-        if (low) l += sum_exact(s, factor, M);
+        const bool low = apart || (!F32 && e_v < e_most - kLowTile);
+        if (low) l += sum_exact(s, factor, M, apart, exps + turn * 16);
         float sum = 0.f;
         uint32_t r[kTerms][16];
 #pragma unroll
@@ -454,7 +467,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
 template <int DP, int NW, bool F32>
 hipError_t launch_exact(const AttnArgs &a, hipStream_t stream) {
   const auto kernel = attention_exact_kernel<DP, NW, F32>;
-  constexpr size_t smem = size_t(2) * 64 * (DP + (DP == 256 ? 128 : DP)) * 2 + 2 * NW * (512 + 16) + 4096;
+  constexpr size_t smem = size_t(2) * 64 * (DP + (DP == 256 ? 128 : DP)) * 2 + 2 * NW * (512 + 16 + 256) + 4096;
   static const bool once = raise_lds_limit(reinterpret_cast<const void *>(kernel), smem);
   (void)once;
   kernel<<<item_grid(a, ATTN_MANY), 64 * NW, smem, stream>>>(a);

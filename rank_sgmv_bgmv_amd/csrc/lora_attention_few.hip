@@ -19,8 +19,9 @@
 // float32: those of K multiply the scores, those of V, as m = scale / 2^e with e
 // common to a tile, the weights.  With s = scale k.q log2 e and t = s + e the
 // weights are w = 2^(t - M) m in float16, M the running maximum of t less 14, and
-// l = sum 2^(t - M) 2^-e.  So a weight keeps 11 bits while it is above 2^-28 of
-// the largest contribution, whatever the values' size.
+// l = sum 2^(t - M) 2^-e.  So a weight keeps 11 bits while it is above 2^-16 of
+// the largest contribution, whatever the values' size: where the scales of a tile
+// lie more than 2^kSpread apart, M takes each key's own e.
 //
 // Bound by memory: 64 requests of up to 32768 keys, 8 heads of 128, read 2.94 GB
 // in 527 us, 5.6 TB/s, above the rate of a large copy (4.9); 256 requests with a
@@ -207,6 +208,7 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
       float kf[4][4], vm[4][4];
       int e;
       uint32_t nans = 0;  // keys whose scales are none
+      bool apart;         // keys have exponents of their own
       {
         if (!whole) {
 #pragma unroll
@@ -215,11 +217,14 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
             for (int i = 0; i < 4; ++i) vs[kb][i] = keys.seen(a, key + kb * 16 + quarter * 4 + i) ? vs[kb][i] : 0.f;
         }
         // (the bits of floats that are not negative are in their order)
-        uint32_t top = 0, most = 0;
+        uint32_t top = 0, most = 0, least = ~0u;  // (of scales that are not zero, less one)
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(vs[kb][i])), most = max(most, __float_as_uint(ks[kb][i]));
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x = __float_as_uint(vs[kb][i]);
+            top = max(top, x), most = max(most, __float_as_uint(ks[kb][i])), least = min(least, x - 1);
+          }
         if (__any(max(top, most) >= kNoScale)) {
           // (such values become zeros: the rows that see them get their NaN from the weight)
           top = 0;
@@ -234,6 +239,7 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
             }
         }
         e = uniform(tile_exponent(quarters_max(__uint_as_float(top))));
+        apart = __any(least < __float_as_uint(ldexpf(1.f, e - 1 - kSpread)) - 1);
         const float down = ldexpf(1.f, -e);
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb)
@@ -304,6 +310,18 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
             for (int kb = 0; kb < kPart; ++kb)
 #pragma unroll
               for (int i = 0; i < 4; ++i) top = fmaxf(top, s[kb][b][i]);
+            if (apart) {
+              // each with its own exponent: those of small scales may have large weights, which float32 holds
+              const int least_own = max(kLeastExponent - e, -100);
+              top = -__builtin_inff();
+#pragma unroll
+              for (int kb = 0; kb < kPart; ++kb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float m = vm[k0 + kb][i];
+                  top = fmaxf(top, s[kb][b][i] + float(m > 0.f ? max(__builtin_amdgcn_frexp_expf(m), least_own) : least_own));
+                }
+            }
             top = quarters_max(top) + float(e) - kHeadroom<true>;
             const float m = fmaxf(M[b], top), less = m - float(e);
             const float fade = __builtin_amdgcn_exp2f(M[b] - m);

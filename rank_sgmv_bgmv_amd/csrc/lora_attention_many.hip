@@ -23,7 +23,8 @@
 // rounded, so that weights and sum err alike; where a tile's eV is so far below
 // an earlier one's that they would lose more than that, l = sum 2^(t - M - eV)
 // in float32.  M follows the running maximum only when that has risen by
-// 2^kSlack.
+// 2^kSlack.  In a tile whose scales lie more than 2^kSpread apart, the keys have
+// eK and eV of their own, which meet the scores.
 //
 // A step computes the scores of the next tile between the weights of this one,
 // and widens the tiles after them between the products with V, a piece after
@@ -75,13 +76,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
   // Tiles of V that are widened ahead of the one at work (of K one more), steps from one barrier to the next.
   constexpr int kLead = NW == 8 ? 2 : 1, kBufs = 2 * kLead;
   // LDS: K [kBufs][64][kChunks] and V^T [kBufs][DP][8] in pieces of 16 bytes; of 2 NW tiles the scales of K and V, [2 NW][64]
-  // each, and what else is known of them; the pages of key blocks
+  // each, what else is known of them and (where they differ much) the keys' exponents; the pages of key blocks
   extern __shared__ __align__(1024) char lds[];
   // (addresses as whole numbers: an exclusive or of them is an address, with no base to be added behind it)
   const int base = int(uintptr_t((LORA_LDS char *)lds));
   constexpr int kRing = 2 * NW;
-  constexpr int kV = kBufs * 64 * DP * 2, kKS = 2 * kV, kVS = kKS + kRing * 256, kMeta = kVS + kRing * 256, kList = kMeta + kRing * 16;
+  constexpr int kV = kBufs * 64 * DP * 2, kKS = 2 * kV, kVS = kKS + kRing * 256, kMeta = kVS + kRing * 256, kExps = kMeta + kRing * 16, kList = kExps + kRing * 256;
   int *lds_pages = reinterpret_cast<int *>(lds + kList);
+  const uint4 *exps = reinterpret_cast<const uint4 *>(lds + kExps) + threadIdx.x % 64 / 32;  // of a lane's keys
 
   if (!plan_matches(a)) {
     if (!a.s.few_blocks && blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(a.plan + H_ERR, 1);  // (else counted there)
@@ -173,11 +175,18 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
       const int e_k = tile_exponent(__uint_as_float(wave_max_bits(k_fine))), e_v = tile_exponent(__uint_as_float(wave_max_bits(v_fine)));
       // (scales of V that are none become zeros: the rows that see the key get their NaN from its score)
       const float ks = sk >= kNoScale ? __builtin_nanf("") : __uint_as_float(sk);
-      reinterpret_cast<float *>(lds + kKS)[at * 64 + lane] = ks * ldexpf(1.f, -e_k);
-      reinterpret_cast<float *>(lds + kVS)[at * 64 + lane] = __uint_as_float(v_fine) * ldexpf(1.f, -e_v);
+      int x_k = e_k, x_v = e_v;
+      const int own_k = tile_exponent(__uint_as_float(k_fine)), own_v = tile_exponent(__uint_as_float(v_fine));
+      const bool apart = __any((k_fine && own_k < e_k - kSpread) || (v_fine && own_v < e_v - kSpread));
+      if (apart) {
+        x_k = own_k, x_v = own_v;
+        reinterpret_cast<uint32_t *>(lds + kExps)[at * 64 + lane] = pack_exponents(x_k - e_k, x_v - e_v);
+      }
+      reinterpret_cast<float *>(lds + kKS)[at * 64 + lane] = ks * ldexpf(1.f, -x_k);
+      reinterpret_cast<float *>(lds + kVS)[at * 64 + lane] = __uint_as_float(v_fine) * ldexpf(1.f, -x_v);
       const int hidden = (seen & 1 ? 0 : 1) | (seen >> 16 & 1 ? 0 : 2) | (seen >> 32 & 1 ? 0 : 4) | (seen >> 48 & 1 ? 0 : 8);
       if (lane == 0)
-        reinterpret_cast<int4 *>(lds + kMeta)[at] = make_int4((e_k + 128) | (e_v + 128) << 8 | hidden << 16, 0, int(nan), int(nan >> 32));
+        reinterpret_cast<int4 *>(lds + kMeta)[at] = make_int4((e_k + 128) | (e_v + 128) << 8 | hidden << 16 | int(apart) << 20, 0, int(nan), int(nan >> 32));
     };
 
     // Raw values of a tile of K and one of V on their way.  A wave's rows lie in one block of 16 keys.  What is past a
@@ -311,7 +320,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
       for (int i = 0; i < kVPer; ++i) page_v[i] = lds_pages[((v + kLead + 1 - v0) * 4 + (i * kThreads + wave * 64) / (DP / 4) * 4 / 16) % kPages];
     };
     auto step = [&](int v, f32x16 (&s)[2], f32x16 (&s_next)[2]) {
-      const int word = uniform(meta.x), e_k = (word & 255) - 128, e_v = (word >> 8 & 255) - 128, bad = word >> 16;
+      const int word = uniform(meta.x), e_k = (word & 255) - 128, e_v = (word >> 8 & 255) - 128, bad = word >> 16 & 15;
+      const bool apart = word >> 20;
       const uint64_t nan = uint32_t(uniform(meta.z)) | uint64_t(uint32_t(uniform(meta.w))) << 32;
       const int key = tile_key(u, v);
       int pk[kKPer], pv[kVPer];
@@ -323,6 +333,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
         const int at_k = first_k(v + 1);
         f16x8 fk[2][kRead];
         read_k(at_k, 0, fk[0]);
+        // (held away from zero, where a hidden key's score would be NaN; it is what scores near zero are multiplied with)
+        float factor = fminf(fmaxf(ldexpf(score, e_k), 1e-37f), 1e37f);
+        if (apart) {
+          scale_apart(s, factor, exps + (v - v0) % kRing * 16);
+          factor = 1.f;
+        }
         const bool whole = bad == 0 && nan == 0 && all_seen(a, u, key, p_lo, p_hi);
         if (!whole) {
           uint32_t seen = 0, hit = 0;
@@ -338,8 +354,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
             s[i / 16][i % 16] = seen >> i & 1 ? x : -__builtin_inff();
           }
         }
-        // (held away from zero, where a hidden key's score would be NaN; it is what scores near zero are multiplied with)
-        const float factor = fminf(fmaxf(ldexpf(score, e_k), 1e-37f), 1e37f);
         float top = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
@@ -353,8 +367,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
         }
         const float less = M - float(e_v);
         e_most = max(e_most, e_v);
-        const bool low = e_v < e_most - kLowTile;
-        if (low) l += sum_exact(s, factor, M);
+        const bool low = apart || e_v < e_most - kLowTile;
+        if (low) l += sum_exact(s, factor, M, apart, exps + (v - v0) % kRing * 16);
         float sum = 0.f;
         uint32_t r[16];
         int at_v = v_first + ((v - v0) & (kBufs - 1)) * (64 * DP * 2);
@@ -491,7 +505,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
 template <int DP, int NW>
 hipError_t launch_many(const AttnArgs &a, hipStream_t stream) {
   const auto kernel = attention_many_kernel<DP, NW>;
-  constexpr size_t smem = size_t(NW == 8 ? 4 : 2) * 64 * DP * 2 * 2 + 2 * NW * (512 + 16) + 4096;
+  constexpr size_t smem = size_t(NW == 8 ? 4 : 2) * 64 * DP * 2 * 2 + 2 * NW * (512 + 16 + 256) + 4096;
   static const bool once = raise_lds_limit(reinterpret_cast<const void *>(kernel), smem);
   (void)once;
   kernel<<<item_grid(a, ATTN_MANY), 64 * NW, smem, stream>>>(a);

@@ -3,7 +3,7 @@ slots that nobody sees hold anything.  The reference and its tolerances are thos
 import pytest
 import torch
 
-from test_gpu_layer import TYPES, Step, ids, same
+from test_gpu_layer import TYPES, Step, branches, gen, ids, same
 
 pytestmark = pytest.mark.gpu
 
@@ -160,3 +160,94 @@ def test_attention_a_key_without_a_finite_scale(which, value, dtype):
         assert torch.equal(got.isnan().all(2), want) and torch.equal(got.isnan().any(2), want)
         ref, tol = Step(seqs, 4, 2, 64, 16, dtype).reference()
         assert bool(((got.double() - ref).abs() <= tol)[~want].all())
+
+
+# --------------------------------------- keys of very different sizes in a tile --
+class Apart(Step):
+    """Where contributions c = p scale lie far apart, the smallest step of float16, 2^-24, counts too.  A row's weights are
+    2^x c with x such that its largest c has a weight of 2^7 at least (bfloat16, many rows: 2^8 times a scale over a power of
+    two, 1/2 or more) or 2^13 (others).  So each is off by 2^-25 at most, which is 2^-32 (2^-38) of the largest c, and the
+    output by that times the sum of the 8-bit values of the keys seen.  (The second number of float32 weights has the same
+    smallest step.)"""
+
+    def reference(self):
+        out, tol = super().reference()
+        least = 2.0 ** (-38 if self.dtype == torch.float32 else -32)
+        for s, (n, x) in enumerate(self.seqs):
+            lo, j = int(self.q_off[s]), torch.arange(x)
+            page = self.pages[s].long()[j // self.page]
+            k, _ = self.rows(s)
+            seen = torch.stack([self.sees(s, i) for i in range(n)])
+            for h in range(self.heads):
+                c = h // (self.heads // self.kv)
+                y = torch.where(seen, self.q[lo:lo + n, h].double() @ k[c].T * self.scale, -torch.inf)
+                most = (torch.softmax(y, 1).nan_to_num(0.0) * self.vs[page, c, j % self.page].double()).amax(1, keepdim=True)
+                v8 = self.v[page, c, j % self.page, :self.d].double().abs()
+                tol[lo:lo + n, h] += 1.05 * least * most * (seen.double() @ v8)
+        return out, tol
+
+    def check_but(self, keys):
+        """Rows that see none of the keys range(*keys[s]) of their sequence s, whose scores are too large for errors of the first
+        order."""
+        got, (ref, tol) = self.run(), self.reference()
+        some = False
+        for s, (n, x) in enumerate(self.seqs):
+            for i in range(n):
+                if not bool(self.sees(s, i)[keys[s][0]:keys[s][1]].any()):
+                    r = int(self.q_off[s]) + i
+                    assert bool(((got[r].double() - ref[r]).abs() <= tol[r]).all()), (s, i)
+                    some = True
+        assert some
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("d", [64, 128, 200])
+@pytest.mark.parametrize("which, factor", [("vs", 2.0 ** 40), ("vs", 2.0 ** -40), ("ks", 2.0 ** 30), ("vs", 2.0 ** 18), ("ks", 2.0 ** -30)])
+def test_attention_keys_that_some_rows_do_not_see(which, factor, d, dtype):
+    """The last keys are 2^40 times the others, or their fraction: queries before them are none the worse for it."""
+    for seqs in ([(4, 100), (2, 64), (1, 30)], [(100, 150), (40, 40)], [(2, 5003)], [(60, 3001)]):
+        step = Apart(seqs, 4, 2, d, 16, dtype)
+        keys = [(x - max(1, n // 2), x) for n, x in seqs]
+        for s, at in enumerate(keys):
+            scale_keys(step, which, s, range(*at), factor)
+        step.check() if factor < 2.0 ** 30 or which == "vs" else step.check_but(keys)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("which, factor", [("vs", 2.0 ** 40), ("ks", 2.0 ** 30)])
+def test_attention_keys_that_leave_the_window(which, factor, dtype):
+    """The first keys of a window are large: rows whose window begins behind them are none the worse for it."""
+    for seqs in ([(4, 100), (2, 64)], [(100, 250), (40, 140)]):
+        step = Apart(seqs, 4, 2, 64, 16, dtype, window=33, sinks=2)
+        keys = [(x - n - 32, x - n - 32 + n // 2) for n, x in seqs]
+        for s, at in enumerate(keys):
+            scale_keys(step, which, s, range(*at), factor)
+        step.check() if which == "vs" else step.check_but(keys)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("n", [6, 40])
+def test_attention_other_branches_of_a_tree_may_be_large(n, dtype):
+    tree = [m for _ in range(3) for m in branches(n, gen(n))]
+    for which, factor in (("vs", 2.0 ** 40), ("ks", 2.0 ** 30)):
+        step = Apart([(n, n), (n, n + 63), (n, n + 300)], 4, 2, 64, 16, dtype, tree=tree)
+        keys = [(x - n // 2, x) for _, x in step.seqs]
+        for s, at in enumerate(keys):
+            scale_keys(step, which, s, range(*at), factor)
+        step.check() if which == "vs" else step.check_but(keys)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("d", [64, 128, 200])
+def test_attention_a_large_value_of_no_weight(d, dtype):
+    """A key whose score lies far below the others' has a value 2^40 times theirs: it takes no bits from them."""
+    for n in (1, 100):
+        for at in (5, 130, n + 190):
+            step = Apart([(n, n + 200)], 4, 2, d, 16, dtype)
+            page = int(step.pages[0, at // 16])
+            step.q[:] = step.q[:1]
+            step.k[page, :, at % 16, :d] = (step.q[0, ::2].float() * -40).round().clamp(-127, 127).to(torch.int8)
+            step.q[:, 1::2] = step.q[:, ::2]
+            scale_keys(step, "ks", 0, [at], 8.0)
+            scale_keys(step, "vs", 0, [at], 2.0 ** 40)
+            step.check()
