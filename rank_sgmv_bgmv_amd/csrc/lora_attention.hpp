@@ -70,17 +70,6 @@ __device__ __forceinline__ float quarters_sum(float v) {
   const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return half_sum(__uint_as_float(s[0]) + __uint_as_float(s[1]));
 }
-__device__ __forceinline__ float wave_max_f(float v) {
-#define LORA_ROR(n) \
-  v = fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0u, __float_as_uint(v), 0x120 + (n), 0xf, 0xf, false)))
-  LORA_ROR(1);
-  LORA_ROR(2);
-  LORA_ROR(4);
-  LORA_ROR(8);
-#undef LORA_ROR
-  return quarters_max(v);
-}
-
 // The largest over the wave, of the bits of floats that are not negative too.
 __device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
 #define LORA_ROR(n) v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x120 + (n), 0xf, 0xf, false)))

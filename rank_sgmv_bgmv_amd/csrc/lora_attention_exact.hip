@@ -90,7 +90,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
           top = fmaxf(top, v < __uint_as_float(0x7f800000u) ? v : 0.f);
         }
       }
-      top = wave_max_f(top);
+      top = half_max(top);  // (a power of two for each row: a large query takes no bits from others)
       const int x = top > 0.f ? min(15 - __builtin_amdgcn_frexp_expf(top), 100) : 0;
       shift = ldexpf(1.f, -x);
 #pragma unroll

@@ -76,28 +76,29 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
     UnitKeys keys;
     keys.set(a, u, 0, u.n - 1);
     const int p_lo = u.len - u.n, p_hi = u.len - 1;  // positions of the rows
-    float shift;                                     // 2^-x of the queries' common power of two
+    float score[kBlocks];  // what a row's products are multiplied with: its queries are over a power of two, 2^-x
     {
       const E *safe = row_at<const E>(a, a.q, u, head, 0);
       float f[kBlocks][DP / 4];
-      float top = 0.f;
+      float top[kBlocks];
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b) {
+        top[b] = 0.f;
         const int row = b * 16 + col;
         const bool live = row < u.rows;
         load_query<E, DP / 4>(row_at<const E>(a, a.q, u, head, live ? row : 0), safe, live, quarter * (DP / 4), D, f[b]);
 #pragma unroll
         for (int i = 0; i < DP / 4; ++i) {
           const float v = fabsf(f[b][i]);
-          top = fmaxf(top, v < __uint_as_float(0x7f800000u) ? v : 0.f);
+          top[b] = fmaxf(top[b], v < __uint_as_float(0x7f800000u) ? v : 0.f);
         }
         sight[b].set(a, u, row);
       }
-      top = wave_max_f(top);
-      const int x = top > 0.f ? min(15 - __builtin_amdgcn_frexp_expf(top), 100) : 0;
-      shift = ldexpf(1.f, -x);
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
+      for (int b = 0; b < kBlocks; ++b) {
+        top[b] = quarters_max(top[b]);
+        const int x = top[b] > 0.f ? min(15 - __builtin_amdgcn_frexp_expf(top[b]), 100) : 0;
+        score[b] = a.scale * ldexpf(1.f, -x) * kByteScale;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           uint32_t w[kTerms][4];
@@ -113,8 +114,8 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
 #pragma unroll
           for (int t = 0; t < kTerms; ++t) q[b][t][s] = frag(w[t][0], w[t][1], w[t][2], w[t][3]);
         }
+      }
     }
-    const float score = a.scale * shift * kByteScale;
 
     f32x4 o[kBlocks][kCols];
     float M[kBlocks], l[kBlocks];
@@ -244,7 +245,7 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) kf[kb][i] = ks[kb][i] * score, vm[kb][i] = vs[kb][i] * down;
+          for (int i = 0; i < 4; ++i) kf[kb][i] = kBlocks == 1 ? ks[kb][i] * score[0] : ks[kb][i], vm[kb][i] = vs[kb][i] * down;
       }
       const bool poisoned = __any(nans != 0);
 
@@ -290,7 +291,7 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
 #pragma unroll
             for (int kb = 0; kb < kPart; ++kb)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) s[kb][b][i] *= kf[k0 + kb][i];
+              for (int i = 0; i < 4; ++i) s[kb][b][i] *= kBlocks == 1 ? kf[k0 + kb][i] : kf[k0 + kb][i] * score[b];
             if (!whole) {
               seen = 0;
 #pragma nounroll

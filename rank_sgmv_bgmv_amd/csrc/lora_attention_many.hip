@@ -121,7 +121,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
           top = fmaxf(top, v < __uint_as_float(0x7f800000u) ? v : 0.f);
         }
       }
-      top = wave_max_f(top);
+      top = half_max(top);  // (a power of two for each row: a large query takes no bits from others)
       const int x = top > 0.f ? min(15 - __builtin_amdgcn_frexp_expf(top), 100) : 0;
       shift = ldexpf(1.f, -x);
 #pragma unroll

@@ -251,3 +251,17 @@ def test_attention_a_large_value_of_no_weight(d, dtype):
             scale_keys(step, "ks", 0, [at], 8.0)
             scale_keys(step, "vs", 0, [at], 2.0 ** 40)
             step.check()
+
+
+# -------------------------------------------------- queries of different sizes --
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("d", [64, 128, 200])
+def test_attention_a_large_query_takes_no_bits_from_others(d, dtype):
+    """One head of one token is 2^32 times the others, which lie in its row block."""
+    for seqs in ([(4, 100), (1, 30)], [(8, 90), (1, 30)], [(100, 150), (40, 40)]):
+        step = Step(seqs, 4, 2, d, 16, dtype)
+        step.q[2, 1] = (step.q[2, 1].float() * 2.0 ** 32).to(dtype)
+        got, (ref, tol) = step.run(), step.reference()
+        keep = torch.ones(step.T, 4, dtype=torch.bool)
+        keep[2, 1] = False
+        assert bool(((got.double() - ref).abs() <= tol)[keep].all())
