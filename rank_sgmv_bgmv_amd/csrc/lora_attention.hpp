@@ -93,6 +93,21 @@ __device__ __forceinline__ int tile_exponent(float v) {
 // float16 number), which a row may not even see: in such a tile each key has an exponent of its own.
 constexpr int kSpread = 12;
 
+// Scores beyond this, where float32 has steps of 1/8 and more: a weight is then 2 to the difference of two rounded numbers,
+// which may lie above or below what the headroom is for by some steps.  The product with the scales is rounded before the
+// maximum is taken off it, so that the largest score keeps a weight, and weights are held to what float16 holds.
+constexpr float kFarScore = 0x1p20f, kMostWeight = 15.f;  // (2^kMostWeight)
+// a * b, rounded (not part of a fused multiply-add)
+__device__ __forceinline__ float product(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
+// s - less, no more than most (NaN stays)
+__device__ __forceinline__ float far_score(float s, float less, float most) {
+  const float x = s - less;
+  return x > most ? most : x;
+}
+
 // The plan made for this call.
 __device__ __forceinline__ bool plan_matches(const AttnArgs &a) {
   bool ok = true;

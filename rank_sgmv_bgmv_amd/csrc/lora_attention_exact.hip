@@ -120,6 +120,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
     f32x16 o[kBlocks];
     float M, l;
     int e_most;  // the largest eV of the piece's tiles so far
+    bool far;    // scores are beyond kFarScore
 
     const int in_page = (1 << a.page_bits) - 1;
     auto fetch_pages = [&](int v, int n) {  // of tiles v .. v + n - 1, to their places in the list
@@ -296,7 +297,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
         const int word = uniform(meta.x), e_k = (word & 255) - 128, e_v = (word >> 8 & 255) - 128, bad = word >> 16 & 15;
         const bool apart = word >> 20;
         const uint64_t nan = uint32_t(uniform(meta.z)) | uint64_t(uint32_t(uniform(meta.w))) << 32;
-        const bool whole = bad == 0 && nan == 0 && all_seen(a, u, key, p_lo, p_hi);
+        const bool whole = bad == 0 && !apart && nan == 0 && all_seen(a, u, key, p_lo, p_hi);
         if constexpr (F32) {
 #pragma unroll
           for (int kb = 0; kb < 2; ++kb)
@@ -308,11 +309,11 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
         }
         // (held away from zero, where a hidden key's score would be NaN; it is what scores near zero are multiplied with)
         float factor = fminf(fmaxf(F32 ? score : ldexpf(score, e_k), 1e-37f), 1e37f);
-        if (apart) {
-          scale_apart(s, factor, exps + turn * 16);
-          factor = 1.f;
-        }
         if (!whole) {
+          if (apart) {
+            scale_apart(s, factor, exps + turn * 16);
+            factor = 1.f;
+          }
           uint32_t seen = 0, hit = 0;
 #pragma nounroll
           for (int n = 0; n < 32; ++n) {
@@ -329,18 +330,28 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
         float top = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
-        top = half_max(top) * factor + (float(e_v) - kHeadroom<F32>);
+        const float most = half_max(top);
+        top = most * factor + (float(e_v) - kHeadroom<F32>);
         if (__any(top > M + kSlack<F32>)) {
+          if (fabsf(top) > kFarScore) top = product(most, factor) + (float(e_v) - kHeadroom<F32>);
           const float m = fmaxf(M, top), fade = __builtin_amdgcn_exp2f(M - m);
           M = m;
+          far = __any(fabsf(M) > kFarScore && M != kNoScore);
           l *= fade;
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b) o[b] *= fade;
         }
-        const float less = M - float(e_v);
+        float less = M - float(e_v);
         e_most = max(e_most, e_v);
         const bool low = apart || (!F32 && e_v < e_most - kLowTile);
-        if (low) l += sum_exact(s, factor, M, apart, exps + turn * 16);
+        if (low || far) {
+          if (far) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i / 16][i % 16] = far_score(product(s[i / 16][i % 16], factor), less, kMostWeight);
+            factor = 1.f, less = 0.f;
+          }
+          if (low) l += sum_exact(s, factor, far ? float(e_v) : M, apart, exps + turn * 16);
+        }
         float sum = 0.f;
         uint32_t r[kTerms][16];
 #pragma unroll
@@ -409,7 +420,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
     // the queries stay, so that the outputs may take their place in memory.
 #pragma nounroll
     for (; d0 < DP; d0 += kVD) {
-      M = kNoScore, l = 0.f, e_most = -128;
+      M = kNoScore, l = 0.f, e_most = -128, far = false;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll

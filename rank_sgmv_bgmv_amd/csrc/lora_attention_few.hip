@@ -291,7 +291,10 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
 #pragma unroll
             for (int kb = 0; kb < kPart; ++kb)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) s[kb][b][i] *= kBlocks == 1 ? kf[k0 + kb][i] : kf[k0 + kb][i] * score[b];
+              for (int i = 0; i < 4; ++i) {
+                const float f = kBlocks == 1 ? kf[k0 + kb][i] : kf[k0 + kb][i] * score[b];
+                s[kb][b][i] = product(s[kb][b][i], f);
+              }
             if (!whole) {
               seen = 0;
 #pragma nounroll
@@ -311,9 +314,9 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
             for (int kb = 0; kb < kPart; ++kb)
 #pragma unroll
               for (int i = 0; i < 4; ++i) top = fmaxf(top, s[kb][b][i]);
+            const int least_own = max(kLeastExponent - e, -100);
             if (apart) {
               // each with its own exponent: those of small scales may have large weights, which float32 holds
-              const int least_own = max(kLeastExponent - e, -100);
               top = -__builtin_inff();
 #pragma unroll
               for (int kb = 0; kb < kPart; ++kb)
@@ -324,9 +327,18 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
                 }
             }
             top = quarters_max(top) + float(e) - kHeadroom<true>;
-            const float m = fmaxf(M[b], top), less = m - float(e);
+            const float m = fmaxf(M[b], top);
+            float less = m - float(e);
             const float fade = __builtin_amdgcn_exp2f(M[b] - m);
             M[b] = m;
+            if (__any(fabsf(less) > kFarScore && m != kNoScore)) {
+#pragma unroll
+              for (int kb = 0; kb < kPart; ++kb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  s[kb][b][i] = far_score(s[kb][b][i], less, kMostWeight - fmaxf(__builtin_amdgcn_logf(vm[k0 + kb][i]), float(least_own)));
+              less = 0.f;
+            }
             float sum = 0.f;
 #pragma unroll
             for (int kb = 0; kb < kPart; ++kb)

@@ -147,6 +147,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
       for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
     float M = kNoScore, l = 0.f;
     int e_most = -128;  // the largest eV of the piece's tiles so far
+    bool far = false;   // scores are beyond kFarScore
 
     const int in_page = (1 << a.page_bits) - 1;
     auto fetch_pages = [&](int v, int n) {  // of tiles v .. v + n - 1, to their places in the list
@@ -335,12 +336,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
         read_k(at_k, 0, fk[0]);
         // (held away from zero, where a hidden key's score would be NaN; it is what scores near zero are multiplied with)
         float factor = fminf(fmaxf(ldexpf(score, e_k), 1e-37f), 1e37f);
-        if (apart) {
-          scale_apart(s, factor, exps + (v - v0) % kRing * 16);
-          factor = 1.f;
-        }
-        const bool whole = bad == 0 && nan == 0 && all_seen(a, u, key, p_lo, p_hi);
+        const bool whole = bad == 0 && !apart && nan == 0 && all_seen(a, u, key, p_lo, p_hi);
         if (!whole) {
+          if (apart) {
+            scale_apart(s, factor, exps + (v - v0) % kRing * 16);
+            factor = 1.f;
+          }
           uint32_t seen = 0, hit = 0;
 #pragma nounroll
           for (int n = 0; n < 32; ++n) {
@@ -357,18 +358,28 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
         float top = -__builtin_inff();
 #pragma unroll
         for (int i = 0; i < 32; ++i) top = fmaxf(top, s[i / 16][i % 16]);
-        top = half_max(top) * factor + (float(e_v) - kHeadroom<false>);
+        const float most = half_max(top);
+        top = most * factor + (float(e_v) - kHeadroom<false>);
         if (__any(top > M + kSlack<false>)) {
+          if (fabsf(top) > kFarScore) top = product(most, factor) + (float(e_v) - kHeadroom<false>);
           const float m = fmaxf(M, top), fade = __builtin_amdgcn_exp2f(M - m);
           M = m;
+          far = __any(fabsf(M) > kFarScore && M != kNoScore);
           l *= fade;
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b) o[b] *= fade;
         }
-        const float less = M - float(e_v);
+        float less = M - float(e_v);
         e_most = max(e_most, e_v);
         const bool low = apart || e_v < e_most - kLowTile;
-        if (low) l += sum_exact(s, factor, M, apart, exps + (v - v0) % kRing * 16);
+        if (low || far) {
+          if (far) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i / 16][i % 16] = far_score(product(s[i / 16][i % 16], factor), less, kMostWeight);
+            factor = 1.f, less = 0.f;
+          }
+          if (low) l += sum_exact(s, factor, far ? float(e_v) : M, apart, exps + (v - v0) % kRing * 16);
+        }
         float sum = 0.f;
         uint32_t r[16];
         int at_v = v_first + ((v - v0) & (kBufs - 1)) * (64 * DP * 2);

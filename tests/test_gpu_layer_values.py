@@ -3,7 +3,7 @@ slots that nobody sees hold anything.  The reference and its tolerances are thos
 import pytest
 import torch
 
-from test_gpu_layer import TYPES, Step, branches, gen, ids, same
+from test_gpu_layer import H, TYPES, V, Step, branches, gen, half, ids, same
 
 pytestmark = pytest.mark.gpu
 
@@ -265,3 +265,29 @@ def test_attention_a_large_query_takes_no_bits_from_others(d, dtype):
         keep = torch.ones(step.T, 4, dtype=torch.bool)
         keep[2, 1] = False
         assert bool(((got.double() - ref).abs() <= tol)[keep].all())
+
+
+# ------------------------------------------------------------------ large scores --
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("d", [64, 128, 200])
+def test_attention_large_scores(d, dtype):
+    """Scores up to 2^45, of which one lies above all others by a third and more: the output is that key's value, off by its
+    rounding and its weight's (2 h in bfloat16), float32 roundings and the output's own."""
+    tol = 1.01 * ((2 * H if dtype == torch.bfloat16 else 2 * H * H) + 16 * V + half(dtype))
+    for seqs in ([(1, 200), (3, 200)], [(60, 200)], [(1, 4000)], [(50, 3000)]):
+        for size in range(8, 42, 3):
+            step = Step(seqs, 4, 2, d, 16, dtype)
+            step.q[:] = step.q[:1]
+            step.q[:, 1::2] = step.q[:, ::2]
+            step.ks[:] = 0.02 * 2.0 ** size
+            at = 7 * size % 140
+            for s in range(len(seqs)):
+                page = int(step.pages[s, at // 16])
+                step.k[page, :, at % 16, :d] = (step.q[0, ::2].float() * 40).round().clamp(-127, 127).to(torch.int8)
+            got = step.run()
+            for s, (n, x) in enumerate(seqs):
+                lo = int(step.q_off[s])
+                _, v = step.rows(s)
+                want = v[:, at].repeat_interleave(2, 0)[None].expand(n, 4, d)
+                ok = (got[lo:lo + n].double() - want).abs() <= tol * want.abs()
+                assert bool(ok.all()), (seqs, s, size)
