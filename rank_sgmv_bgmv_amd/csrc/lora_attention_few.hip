@@ -55,7 +55,7 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
   int n_items = gload<int>(a.plan + A_ITEMS + ATTN_FEW);
   int2 im = load_item(a, ATTN_FEW, blockIdx.y);
   if (!plan_matches(a)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(a.plan + H_ERR, 1);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicAdd(a.plan + H_ERR, 1);
     return;
   }
   const int lane = threadIdx.x % 64, wave = uniform(threadIdx.x / 64), col = lane % 16, quarter = lane / 16;

@@ -86,7 +86,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
   const uint4 *exps = reinterpret_cast<const uint4 *>(lds + kExps) + threadIdx.x % 64 / 32;  // of a lane's keys
 
   if (!plan_matches(a)) {
-    if (!a.s.few_blocks && blockIdx.x == 0 && threadIdx.x == 0) atomicAdd(a.plan + H_ERR, 1);  // (else counted there)
+    if (!a.s.few_blocks && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicAdd(a.plan + H_ERR, 1);  // (else counted there)
     return;
   }
   const int tid = threadIdx.x, lane = tid % 64, wave = uniform(tid / 64), col = lane % 32, half = lane / 32;

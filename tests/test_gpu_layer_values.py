@@ -3,6 +3,7 @@ slots that nobody sees hold anything.  The reference and its tolerances are thos
 import pytest
 import torch
 
+import rank_sgmv_bgmv_amd as L
 from test_gpu_layer import H, TYPES, V, Step, branches, gen, half, ids, same
 
 pytestmark = pytest.mark.gpu
@@ -291,3 +292,19 @@ def test_attention_large_scores(d, dtype):
                 want = v[:, at].repeat_interleave(2, 0)[None].expand(n, 4, d)
                 ok = (got[lo:lo + n].double() - want).abs() <= tol * want.abs()
                 assert bool(ok.all()), (seqs, s, size)
+
+
+# ---------------------------------------------------------------- another plan --
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("d", [64, 256])
+def test_attention_counts_a_call_on_another_plan_once(d, dtype):
+    for n in (1, 100):
+        a = Step([(n, 150 + 20 * i) for i in range(5)] + [(1, 700)], 4, 2, d, 16, dtype).load()
+        b = Step([(n, 150 + 20 * i) for i in range(5)] + [(1, 700)], 4, 2, d, 16, dtype, window=2 ** 20).load()
+        out = torch.full(a.q.shape, 7.0, dtype=dtype, device="cuda:0")
+        plan = torch.zeros(max(a.plan.numel(), b.plan.numel()), dtype=torch.uint8, device="cuda:0")
+        plan[:b.plan.numel()] = b.plan
+        for calls in (1, 2, 3):
+            L.lora_attention_apply(a.attention, a.cache, a.batch, plan, a.q.to("cuda:0"), out, a.ws)
+            assert L.lora_read_device_errors(plan) == calls
+        assert bool((out == 7).all())
