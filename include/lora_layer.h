@@ -179,8 +179,12 @@ lora_status lora_attention_plan(const lora_attention *attention, const lora_cach
  * values that are rounded to 11 bits once their scales are multiplied in.)
  *   q, out  heads of the batch's rows: n_heads of head_dim values.  out may be
  *           q itself (the same strides), or memory that does not meet it
- *   plan    of lora_attention_plan for the same attention, cache sizes and
- *           batch; on any other nothing is written and the plan's error word counts it
+ *   plan    of lora_attention_plan for this attention and batch, and a cache of
+ *           these sizes.  On a plan made for other sizes (heads, head_dim, dtype,
+ *           window, sinks, n_tokens, n_seqs, max_q, keys of max_pages, tree or
+ *           none) nothing is written and its error word counts the call; one made
+ *           from other contents of q_off or lens cannot be told from the right one:
+ *           after they change, plan anew
  *   ws      16-byte aligned, written before it is read; calls that may overlap
  *           in time need one each (a plan may be shared)
  * n_tokens == 0 launches nothing.  Errors as above. */
