@@ -20,8 +20,9 @@
 // common to a tile, the weights.  With s = scale k.q log2 e and t = s + e the
 // weights are w = 2^(t - M) m in float16, M the running maximum of t less 14, and
 // l = sum 2^(t - M) 2^-e.  So a weight keeps 11 bits while it is above 2^-16 of
-// the largest contribution, whatever the values' size: where the scales of a tile
-// lie more than 2^kSpread apart, M takes each key's own e.
+// the largest contribution, whatever the values' size down to scales of 2^-60
+// (below, e stays): where those of a tile lie more than 2^kSpread apart, M takes
+// each key's own e.
 //
 // Bound by memory: 64 requests of up to 32768 keys, 8 heads of 128, read 2.94 GB
 // in 527 us, 5.6 TB/s, above the rate of a large copy (4.9); 256 requests with a

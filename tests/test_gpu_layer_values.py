@@ -308,3 +308,20 @@ def test_attention_counts_a_call_on_another_plan_once(d, dtype):
             L.lora_attention_apply(a.attention, a.cache, a.batch, plan, a.q.to("cuda:0"), out, a.ws)
             assert L.lora_read_device_errors(plan) == calls
         assert bool((out == 7).all())
+
+
+# -------------------------------------------------------------------- tiny values --
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("d", [64, 128, 200])
+@pytest.mark.parametrize("size", [-58, -64, -72, -84, -96])
+def test_attention_tiny_values(size, d, dtype):
+    """Scales of values below 2^-60 lose bits: an output is off by 2^-85 more (values as float16 over 2^-60, whose smallest
+    step is 2^-24) and by 2^-92 a key (weights over 2^-60, which are 2^14 at most)."""
+    for seqs in ([(1, 300), (2, 90)], [(100, 150)], [(2, 5000)]):
+        step = Step(seqs, 4, 2, d, 16, dtype)
+        step.vs *= 2.0 ** size / 0.02
+        got, (ref, tol) = step.run(), step.reference()
+        for s, (n, x) in enumerate(seqs):
+            lo = int(step.q_off[s])
+            more = 1.05 * (2.0 ** -85 + x * 2.0 ** -92) if size < -59 else 0.0
+            assert bool(((got[lo:lo + n].double() - ref[lo:lo + n]).abs() <= tol[lo:lo + n] + more).all())
