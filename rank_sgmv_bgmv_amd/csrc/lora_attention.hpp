@@ -159,19 +159,27 @@ struct UnitKeys {
   }
   // whether one of the keys key .. key + more is seen
   __device__ __forceinline__ bool seen(const AttnArgs &a, int key, int more = 0) const {
-    return key < hi && (key + more >= lo || key < a.sinks);
+    return (key < hi) & ((key + more >= lo) | (key < a.sinks));
   }
 };
 
-// Which page a block of 16 keys lies in; -1 where no row sees its keys, or in no page of the cache.
-__device__ __forceinline__ int block_page(const AttnArgs &a, const AttnUnit &u, const UnitKeys &keys, int key) {
-  if (!keys.seen(a, key, 15)) return -1;
-  const int p = gload<int>(a.pages + int64_t(u.seq) * a.ld_pages + (key >> a.page_bits));
-  return p >= 0 && p < a.c.n_pages ? p : -1;
+// Which page a block of 16 keys lies in; -1 where no row sees its keys, or in no page of the cache.  (No lane branches here,
+// nor elsewhere while a kernel's operands are in registers: where lanes come back from one, the compiler has put copies of
+// registers before the instruction that brings them back, and what the other lanes held was lost.)
+__device__ __forceinline__ int block_page(const AttnArgs &a, const AttnUnit &u, const UnitKeys &keys, int key, bool there) {
+  there = there & keys.seen(a, key, 15);
+  const int p = gload<int>(a.pages + int64_t(u.seq) * a.ld_pages + (there ? key >> a.page_bits : 0));
+  return (there & (p >= 0) & (p < a.c.n_pages)) ? p : -1;
 }
 
 __device__ __forceinline__ int tile_key(const AttnUnit &u, int v) {
   return (v < u.sink_tiles ? v : u.main + v - u.sink_tiles) * kKeyTile;
+}
+
+// The first n bits: none for a negative n, all from 64 on.
+__device__ __forceinline__ uint64_t bits_below(int n) {
+  const uint64_t some = ~uint64_t(0) >> ((64 - min(max(n, 0), 64)) & 63);
+  return n > 0 ? some : 0;
 }
 
 // What a row sees: keys up to its position within the window, the first ones, and of a tree's drafted tokens those of its mask.
@@ -192,12 +200,18 @@ struct RowSight {
     pos = live ? at : -1;
     first_end = min(a.sinks, pos + 1);
   }
-  // (keys are not negative, so that none is within the window of a negative position)
-  __device__ __forceinline__ bool sees(const AttnArgs &a, const AttnUnit &u, int key) const {
-    const bool near = uint32_t(pos - key) < uint32_t(a.window) || key < first_end;
-    const int draft = key - (u.len - u.n);
-    if (!a.tree || draft < 0) return near;
-    return draft < LORA_MAX_TREE && (mask >> draft & 1);
+  // The keys of a tile that it sees, a bit each.  hidden: the blocks of 16 that nobody sees.
+  __device__ __forceinline__ uint64_t seen(const AttnArgs &a, const AttnUnit &u, int key, uint32_t hidden) const {
+    const int lo = pos >= a.window ? pos - a.window + 1 : 0, context = u.len - u.n;
+    uint64_t keys = (bits_below(pos + 1 - key) & ~bits_below(lo - key)) | bits_below(first_end - key);
+    if (a.tree && key + kKeyTile > context) {
+      const int c = context - key;  // less than 64
+      const uint64_t drafts = c >= 0 ? mask << (c & 63) : mask >> (-c & 63);
+      keys = (keys & bits_below(c)) | ((c > -64 ? drafts : 0) & ~bits_below(c));
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) keys &= hidden >> b & 1 ? ~(uint64_t(0xffff) << 16 * b) : ~uint64_t(0);
+    return keys;
   }
 };
 

@@ -45,6 +45,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
   constexpr int kKUnits = 64 * DP / 16, kKPer = (kKUnits + kThreads - 1) / kThreads;
   constexpr int kVUnits = 16 * kVD / 4, kVPer = (kVUnits + kThreads - 1) / kThreads;
   constexpr int kPages = 1024;                  // key blocks whose pages are looked up at once
+  static_assert(kPages / 2 % kThreads == 0, "looked up by all threads, half of them at a time");
   // LDS: K [2][64][kChunks] and V^T [2][kVD][8] in pieces of 16 bytes; of 2 NW tiles the scales of K and V, [2 NW][64]
   // each, what else is known of them and (where they differ much) the keys' exponents; the pages of key blocks
   extern __shared__ __align__(16) char lds[];
@@ -123,28 +124,28 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
     bool far;    // scores are beyond kFarScore
 
     const int in_page = (1 << a.page_bits) - 1;
-    auto fetch_pages = [&](int v, int n) {  // of tiles v .. v + n - 1, to their places in the list
-      for (int i = tid; i < 4 * n; i += kThreads) {
-        const int t = v + i / 4;
-        lds_pages[((v - v0) * 4 + i) % kPages] = t < v1 ? block_page(a, u, keys, tile_key(u, t) + (i % 4) * 16) : -1;
-      }
+    auto fetch_pages = [&](int v, int n) {  // of tiles v .. v + n - 1, as far as there are, to their places in the list
+      // (as many for every thread: no lane branch)
+      for (int t = v; t < min(v + n, v1); t += kThreads / 4)
+        lds_pages[((t - v0) * 4 + tid) % kPages] = block_page(a, u, keys, tile_key(u, t + tid / 4) + (tid % 4) * 16, t + tid / 4 < v1);
     };
 
     // The scales of a tile, a key a lane, are one wave's work: over a power of two that leaves them below 1 (fp32: those
     // of V), to LDS.  All waves do a tile each at once, NW tiles ahead, so that none waits for another.
     uint32_t sk = 0, sv = 0;
     auto load_scales = [&](int v) {
-      const int page = v < v1 ? lds_pages[((v - v0) * 4 + lane / 16) % kPages] : -1;
-      sk = sv = 0;
-      if (page >= 0 && keys.seen(a, tile_key(u, v) + lane)) {
-        const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + lane) & in_page);
+      const int page = max(lds_pages[((v - v0) * 4 + lane / 16) % kPages], 0);
+      const int64_t slot = (int64_t(head) << a.page_bits) + ((tile_key(u, v) + lane) & in_page);
+      if (v < v1) {
         sk = gload<uint32_t>(a.c.k_scale + page * a.c.k_scale_page + slot);
         sv = gload<uint32_t>(a.c.v_scale + page * a.c.v_scale_page + slot);
       }
     };
     auto put_scales = [&](int v) {
       const int at = (v - v0) % kRing;
-      const uint64_t seen = __ballot(lds_pages[((v - v0) * 4 + lane / 16) % kPages] >= 0), nan = __ballot(sv >= kNoScale);
+      const bool paged = lds_pages[((v - v0) * 4 + lane / 16) % kPages] >= 0, there = paged & keys.seen(a, tile_key(u, v) + lane);
+      sk = there ? sk : 0u, sv = there ? sv : 0u;
+      const uint64_t seen = __ballot(paged), nan = __ballot(sv >= kNoScale);
       const uint32_t v_fine = sv >= kNoScale ? 0u : sv, k_fine = sk >= kNoScale ? 0u : sk;
       const int e_k = tile_exponent(__uint_as_float(wave_max_bits(k_fine))), e_v = tile_exponent(__uint_as_float(wave_max_bits(v_fine)));
       // (scales of V that are none become zeros: the rows that see the key get their NaN from its score)
@@ -159,8 +160,8 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
       reinterpret_cast<float *>(lds + kKS)[at * 64 + lane] = F32 ? ks : ks * ldexpf(1.f, -x_k);
       reinterpret_cast<float *>(lds + kVS)[at * 64 + lane] = __uint_as_float(v_fine) * ldexpf(1.f, -x_v);
       const int hidden = (seen & 1 ? 0 : 1) | (seen >> 16 & 1 ? 0 : 2) | (seen >> 32 & 1 ? 0 : 4) | (seen >> 48 & 1 ? 0 : 8);
-      if (lane == 0)
-        reinterpret_cast<int4 *>(lds + kMeta)[at] = make_int4((e_k + 128) | (e_v + 128) << 8 | hidden << 16 | int(apart) << 20, 0, int(nan), int(nan >> 32));
+      // (all lanes the same)
+      reinterpret_cast<int4 *>(lds + kMeta)[at] = make_int4((e_k + 128) | (e_v + 128) << 8 | hidden << 16 | int(apart) << 20, 0, int(nan), int(nan >> 32));
     };
 
     // Raw values of a tile of K and one of V on their way.  A wave's rows lie in one block of 16 keys.  What is past a
@@ -314,17 +315,13 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
             scale_apart(s, factor, exps + turn * 16);
             factor = 1.f;
           }
-          uint32_t seen = 0, hit = 0;
-#pragma nounroll
-          for (int n = 0; n < 32; ++n) {
-            const int at = n / 4 * 8 + half * 4 + n % 4;
-            seen |= !(bad >> (at / 16) & 1) && sight.sees(a, u, key + at) ? 1u << n : 0u;
-            hit |= uint32_t(nan >> at & 1) << n;
-          }
+          // (a lane's keys are four of each eight)
+          const uint64_t seen = sight.seen(a, u, key, bad) >> 4 * half, hit = nan >> 4 * half;
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float x = hit >> i & 1 ? __builtin_nanf("") : s[i / 16][i % 16];
-            s[i / 16][i % 16] = seen >> i & 1 ? x : -__builtin_inff();
+            const int at = i / 4 * 8 + i % 4;
+            const float x = hit >> at & 1 ? __builtin_nanf("") : s[i / 16][i % 16];
+            s[i / 16][i % 16] = seen >> at & 1 ? x : -__builtin_inff();
           }
         }
         float top = -__builtin_inff();

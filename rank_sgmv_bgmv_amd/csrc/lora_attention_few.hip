@@ -135,7 +135,7 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
     uint32_t bad = 0;  // key blocks of the loaded tile whose keys are not seen
     auto load_ids = [&](int v) {
       const int mine = v + (lane / 4) * kFewWaves;
-      ids = mine < v1 ? block_page(a, u, keys, tile_key(u, mine) + (lane % 4) * 16) : -1;
+      ids = block_page(a, u, keys, tile_key(u, mine) + (lane % 4) * 16, mine < v1);
     };
     auto page_of = [&](int turn, int kb) { return __builtin_amdgcn_readlane(ids, (turn % 16) * 4 + kb); };
     // (what is past a row's end is read from its begin: it meets zeros of the queries, or makes outputs that are not there)
@@ -297,13 +297,11 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
                 s[kb][b][i] = product(s[kb][b][i], f);
               }
             if (!whole) {
+              // (a lane's keys are four of each sixteen)
+              const uint64_t keys_seen = sight[b].seen(a, u, key, hidden) >> 4 * quarter;
               seen = 0;
-#pragma nounroll
-              for (int n = 0; n < 4 * kPart; ++n) {
-                const int kb = k0 + n / 4;
-                const bool ok = !(hidden >> kb & 1) && sight[b].sees(a, u, key + kb * 16 + quarter * 4 + n % 4);
-                seen |= ok ? 1u << (4 * k0 + n) : 0u;
-              }
+#pragma unroll
+              for (int kb = 0; kb < 4; ++kb) seen |= uint32_t(keys_seen >> 16 * kb & 15) << 4 * kb;
 #pragma unroll
               for (int kb = 0; kb < kPart; ++kb)
 #pragma unroll
