@@ -108,8 +108,8 @@ typedef struct {
 lora_status lora_cache_write(const lora_cache *cache, const int32_t *slots, int32_t n_tokens, const lora_heads *k,
                              const lora_heads *v, lora_dtype dtype, hipStream_t stream);
 
-/* Reads slots back: k[t], v[t] = the values times their scale, rounded once to
- * dtype.  Tokens of a slot that is negative or not in the cache are left as
+/* Reads slots back: k[t], v[t] = the values times their scale, rounded to
+ * dtype (through float32 on its way to bfloat16).  Tokens of a slot that is negative or not in the cache are left as
  * they were.  Errors as above; k and v must keep their values apart. */
 lora_status lora_cache_read(const lora_cache *cache, const int32_t *slots, int32_t n_tokens, const lora_heads *k,
                             const lora_heads *v, lora_dtype dtype, hipStream_t stream);

@@ -19,8 +19,8 @@
 // half by the scheduling that serves the other kernel, 711 of a tile's 1147
 // instructions were copies between the halves).  Products and the arithmetic
 // between them take turns; nothing of the next tile's runs beside them.  48 rows
-// of 32 sequences over 8192 keys, 8 heads: of 128 in fp32 352 us, of 256 in bf16
-// 795, in fp32 1400 (both of these spill, 200 and 430 bytes a lane).
+// of 32 sequences over 8192 keys each, 8 heads: of 128 in fp32 469 us, of 256 in
+// bf16 1066, in fp32 1835 (both of these spill, 288 and 436 bytes a lane).
 
 #include "lora_attention.hpp"
 

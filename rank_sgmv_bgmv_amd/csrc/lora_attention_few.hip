@@ -25,12 +25,14 @@
 // each key's own e.
 //
 // Bound by memory: 64 requests of up to 32768 keys, 8 heads of 128, read 2.94 GB
-// in 527 us, 5.6 TB/s, above the rate of a large copy (4.9); 256 requests with a
-// window of 4096 take 393 us (5.65 TB/s).  One request over 4097 keys takes 15.8
-// us, two launches whose loads wait for each other: plan, item, unit, pages,
-// keys.  Two workgroups a CU (launch bounds) have the loads of a tile and of its
-// follower on their way; a register more than 256 costs 5%, which is why what
-// depends on the head is computed anew for each item.
+// in 521 us, 5.6 TB/s, above the rate of a large copy (4.9); 256 requests with a
+// window of 4096 take 383 us (5.8 TB/s).  Heads of 64 take 321 us (4.7 TB/s) for
+// the 64 requests, of 256 1017 (5.7); in fp32, of 64 352 (4.3), of 128 652 (4.5)
+// and of 256 1044 (5.6).  One request over 4097 keys takes 15.5 us, two launches
+// whose loads wait for each other: plan, item, unit, pages, keys.  Two workgroups
+// a CU (launch bounds) have the loads of a tile and of its follower on their way; a
+// register more than 256 costs 5%, which is why what depends on the head is
+// computed anew for each item.
 
 #include "lora_attention.hpp"
 

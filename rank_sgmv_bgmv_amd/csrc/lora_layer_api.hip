@@ -124,11 +124,11 @@ AttnShape attention_shape(const lora_attention &t, const lora_cache &c, const lo
   s.T = b.n_tokens, s.S = b.n_seqs, s.kv_heads = c.n_heads, s.group = t.n_heads / c.n_heads, s.head_dim = c.head_dim;
   s.dp = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
   const bool f32 = t.dtype == LORA_F32;
-  // The kernel for few rows has registers for two row blocks of 16 (one of fp32 heads beyond 128); with four it spilled:
-  // 48 rows of heads of 128 589 us against 204 in the other kernel.  Where both serve, 32 rows of 8 cache heads over 8192
-  // keys, bf16 heads of 128: one sequence 22 us here and 26 there, four 55 and 57, 32 of them 197 and 159 (heads of 64:
-  // 19 and 21, 141 and 103).  32 sequences with heads of 256: 578 and 765; fp32 heads of 64: 150 and 236, of 128: 220
-  // and 343.
+  // The kernel for few rows has registers for two row blocks of 16 (one of fp32 heads beyond 128); with four it spilled
+  // and took near three times the other kernel's time.  Where both serve, 32 rows of 8 cache heads over 8192 keys each, bf16
+  // heads of 128: one sequence 26 us here and 38 there, four 68 and 60, 32 of them 230 and 220 (heads of 64: 22 and 27, 55
+  // and 44, 171 and 145).  32 sequences with heads of 256: 698 and 1039; fp32 heads of 64: 181 and 326, of 128: 255 and
+  // 455.
   const bool one = f32 ? s.dp == 256 : s.dp <= 128 && int64_t(s.S) * s.kv_heads > 32;
   const int blocks = one ? 1 : 2;
   const int64_t q = b.max_q < s.T ? b.max_q : s.T, most = q * s.group;
@@ -137,8 +137,8 @@ AttnShape attention_shape(const lora_attention &t, const lora_cache &c, const lo
   const int64_t few = most <= 16 * blocks ? most : s.group <= 16 * blocks && s.T < s.S * q ? s.group : 0;
   s.few_blocks = few == 0 ? 0 : few <= 16 ? 1 : 2;
   s.few_rows = 16 * s.few_blocks;
-  // Units of 128 rows, two workgroups a CU, where no sequence has more: 32 drafts of 24 tokens for 32 heads over 32768
-  // keys take 394 us, 417 in units of 256; a prompt of 16384 takes 1388 us in units of 256 and 1515 in those of 128.
+  // Units of 128 rows, two workgroups a CU, where no sequence has more: 32 drafts of 24 tokens for 32 heads after up to
+  // 16384 keys take 315 us, 447 in units of 256; a prompt of 16384 takes 1261 us in units of 256 and 1391 in those of 128.
   s.many_rows = most <= s.few_rows ? 0 : s.dp == 256 || f32 || most <= 128 ? 128 : 256;
   const int64_t wide = int64_t(s.T) * s.group;
   s.units[ATTN_FEW] = s.few_rows ? s.S : 0;
@@ -150,9 +150,10 @@ AttnShape attention_shape(const lora_attention &t, const lora_cache &c, const lo
     tiles = tiles < seen ? tiles : seen;
   }
   // Pieces of all heads that a launch aims at.  Few rows: four times as many as find room at once, which come out even
-  // however long the sequences are (64 of up to 32768 keys 531 us, 549 with half as many, 565 with four times as many).
-  // Many rows: of 256 one a CU (beside 256 single tokens four prompts of 512 after up to 4096 keys 744 us, 760 with two),
-  // of 128 three (32 drafts of 24 after up to 16384 keys 348 us; 381 with two, 357 with four, 568 with one).
+  // however long the sequences are (64 of up to 32768 keys 522 us, 541 with half as many, 543 with four times as many; the
+  // builds of one workgroup a CU: fp32 heads of 128 652, 680 and 811, bf16 heads of 256 1017, 1013 and 1188).
+  // Many rows: of 256 one a CU (beside 256 single tokens four prompts of 512 after up to 4096 keys 730 us, with two as
+  // well), of 128 three (32 drafts of 24 after up to 16384 keys 315 us; 368 with two, 329 with four, 382 with one).
   const int total[ATTN_KINDS] = {2048, s.many_rows == 256 ? 256 : 768};
   size_t at = align256(sizeof(int) * H_WORDS), ws = 0;
   auto take = [](size_t &off, size_t bytes) { const size_t o = off; off = align256(off + bytes); return o; };
@@ -160,8 +161,8 @@ AttnShape attention_shape(const lora_attention &t, const lora_cache &c, const lo
   for (int k = 0; k < ATTN_KINDS; ++k) {
     const int rows = k == ATTN_FEW ? s.few_rows : s.many_rows;
     s.target[k] = (total[k] - 1) / s.kv_heads + 1;
-    // (four tiles are one a wave of few rows: a request of 4097 keys takes 17.1 us, 19.3 with two or eight; seven fp32
-    // drafts of many rows 41.7 us with two, 47 with four, 55 with one, a second round)
+    // (four tiles are one a wave of few rows: a request of 4097 keys takes 15.0 us, 18.0 with two, 16.9 with eight; seven
+    // fp32 drafts of many rows 25.1 us with two, 28.9 with four, 38.4 with one, a second round)
     s.least[k] = k == ATTN_FEW ? 4 : 2;
     // a unit is cut into no more than twice its share of the target, and not at all where it has few tiles
     s.cut[k] = s.units[k] && tiles > s.least[k] ? (s.units[k] < s.target[k] ? s.units[k] : s.target[k]) : 0;
