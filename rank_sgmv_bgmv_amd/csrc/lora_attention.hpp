@@ -89,9 +89,11 @@ constexpr int kLeastExponent = -60;
 __device__ __forceinline__ int tile_exponent(float v) {
   return v > 0.f ? min(max(__builtin_amdgcn_frexp_expf(v), kLeastExponent), 100) : kLeastExponent;
 }
-// Scales of a tile that are less than 2^-kSpread of its largest would lose bits to it (an 8-bit value over 2^13 is a normal
-// float16 number), which a row may not even see: in such a tile each key has an exponent of its own.
-constexpr int kSpread = 12;
+// Scales of a tile that are much less than its largest lose bits to it, which a row may not even see: in such a tile each
+// key has an exponent of its own.  Keys lose none down to 2^-kSpreadK (an 8-bit value over 2^13 is a normal float16
+// number); of values, what is left of a weight's range is smaller by as much, and one that is zero leaves none where its
+// key takes most of the weight.
+constexpr int kSpreadK = 12, kSpreadV = 4;
 
 // Scores beyond this, where float32 has steps of 1/8 and more: a weight is then 2 to the difference of two rounded numbers,
 // which may lie above or below what the headroom is for by some steps.  The product with the scales is rounded before the

@@ -19,9 +19,9 @@
 // float32: those of K multiply the scores, those of V, as m = scale / 2^e with e
 // common to a tile, the weights.  With s = scale k.q log2 e and t = s + e the
 // weights are w = 2^(t - M) m in float16, M the running maximum of t less 14, and
-// l = sum 2^(t - M) 2^-e.  So a weight keeps 11 bits while it is above 2^-16 of
+// l = sum 2^(t - M) 2^-e.  So a weight keeps 11 bits while it is above 2^-23 of
 // the largest contribution, whatever the values' size down to scales of 2^-60
-// (below, e stays): where those of a tile lie more than 2^kSpread apart, M takes
+// (below, e stays): where those of a tile lie more than 2^kSpreadV apart, M takes
 // each key's own e.
 //
 // Bound by memory: 64 requests of up to 32768 keys, 8 heads of 128, read 2.94 GB
@@ -214,20 +214,24 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
       uint32_t nans = 0;  // keys whose scales are none
       bool apart;         // keys have exponents of their own
       {
+        // (the bits of floats that are not negative are in their order)
+        uint32_t top = 0, most = 0, all_least = ~0u, least = ~0u;  // of V, of K, of V, of V's keys that are seen
         if (!whole) {
 #pragma unroll
           for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) vs[kb][i] = keys.seen(a, key + kb * 16 + quarter * 4 + i) ? vs[kb][i] : 0.f;
+            for (int i = 0; i < 4; ++i) {
+              const bool there = keys.seen(a, key + kb * 16 + quarter * 4 + i) & !(hidden >> kb & 1);
+              least = min(least, there ? __float_as_uint(vs[kb][i]) : ~0u);
+              vs[kb][i] = there ? vs[kb][i] : 0.f;
+            }
         }
-        // (the bits of floats that are not negative are in their order)
-        uint32_t top = 0, most = 0, least = ~0u;  // (of scales that are not zero, less one)
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t x = __float_as_uint(vs[kb][i]);
-            top = max(top, x), most = max(most, __float_as_uint(ks[kb][i])), least = min(least, x - 1);
+            top = max(top, x), most = max(most, __float_as_uint(ks[kb][i])), all_least = min(all_least, x);
           }
         if (__any(max(top, most) >= kNoScale)) {
           // (such values become zeros: the rows that see them get their NaN from the weight)
@@ -243,7 +247,8 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
             }
         }
         e = uniform(tile_exponent(quarters_max(__uint_as_float(top))));
-        apart = __any(least < __float_as_uint(ldexpf(1.f, e - 1 - kSpread)) - 1);
+        if (whole) least = all_least;
+        apart = e > kLeastExponent && __any(least < __float_as_uint(ldexpf(1.f, e - 1 - kSpreadV)));
         const float down = ldexpf(1.f, -e);
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb)

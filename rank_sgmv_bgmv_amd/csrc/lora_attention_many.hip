@@ -23,8 +23,8 @@
 // rounded, so that weights and sum err alike; where a tile's eV is so far below
 // an earlier one's that they would lose more than that, l = sum 2^(t - M - eV)
 // in float32.  M follows the running maximum only when that has risen by
-// 2^kSlack.  In a tile whose scales lie more than 2^kSpread apart, the keys have
-// eK and eV of their own, which meet the scores.
+// 2^kSlack.  In a tile whose scales lie far apart (kSpreadK, kSpreadV), the keys
+// have eK and eV of their own, which meet the scores.
 //
 // A step computes the scores of the next tile between the weights of this one,
 // and widens the tiles after them between the products with V, a piece after
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attention_many_kernel(AttnArgs a) 
       const float ks = sk >= kNoScale ? __builtin_nanf("") : __uint_as_float(sk);
       int x_k = e_k, x_v = e_v;
       const int own_k = tile_exponent(__uint_as_float(k_fine)), own_v = tile_exponent(__uint_as_float(v_fine));
-      const bool apart = __any((k_fine && own_k < e_k - kSpread) || (v_fine && own_v < e_v - kSpread));
+      const bool apart = __any((k_fine && own_k < e_k - kSpreadK) || (there && own_v < e_v - kSpreadV));
       if (apart) {
         x_k = own_k, x_v = own_v;
         reinterpret_cast<uint32_t *>(lds + kExps)[at * 64 + lane] = pack_exponents(x_k - e_k, x_v - e_v);

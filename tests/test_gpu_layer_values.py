@@ -165,15 +165,17 @@ def test_attention_a_key_without_a_finite_scale(which, value, dtype):
 
 # --------------------------------------- keys of very different sizes in a tile --
 class Apart(Step):
-    """Where contributions c = p scale lie far apart, the smallest step of float16, 2^-24, counts too.  A row's weights are
-    2^x c with x such that its largest c has a weight of 2^7 at least (bfloat16, many rows: 2^8 times a scale over a power of
-    two, 1/2 or more) or 2^13 (others).  So each is off by 2^-25 at most, which is 2^-32 (2^-38) of the largest c, and the
-    output by that times the sum of the 8-bit values of the keys seen.  (The second number of float32 weights has the same
-    smallest step.)"""
+    """Where contributions c = p scale lie far apart, the smallest step of float16, 2^-24, counts too.  Scales are taken as m
+    over a power of two of their tile, 2^-5 <= m < 1 (or over their own, 1/2 <= m).  In float32 weights are p m 2^x with x such
+    that the largest p over that power has p 2^x = 2^14, so that the largest c has a weight of 2^9 or more; each is off by
+    2^-25 at most, half the smallest step (of its second number too), which is 2^-34 of the largest c.  In bfloat16 weights are
+    p 2^x with the largest 2^8 or more and meet values m v: 2^-25 m of at least 2^8 m', which is 2^-33 m / m' <= 2^-28.  (Few
+    rows are as float32.)  The output is off by that times the sum of the 8-bit values of the keys seen.  Where a scale is zero,
+    which counts as 2^-60, 2^-85 and 2^-92 a key come to it (test_attention_tiny_values)."""
 
     def reference(self):
         out, tol = super().reference()
-        least = 2.0 ** (-38 if self.dtype == torch.float32 else -32)
+        least = 2.0 ** (-34 if self.dtype == torch.float32 else -28)
         for s, (n, x) in enumerate(self.seqs):
             lo, j = int(self.q_off[s]), torch.arange(x)
             page = self.pages[s].long()[j // self.page]
@@ -184,7 +186,8 @@ class Apart(Step):
                 y = torch.where(seen, self.q[lo:lo + n, h].double() @ k[c].T * self.scale, -torch.inf)
                 most = (torch.softmax(y, 1).nan_to_num(0.0) * self.vs[page, c, j % self.page].double()).amax(1, keepdim=True)
                 v8 = self.v[page, c, j % self.page, :self.d].double().abs()
-                tol[lo:lo + n, h] += 1.05 * least * most * (seen.double() @ v8)
+                zero = 2.0 ** -85 + x * 2.0 ** -92 if bool((self.vs[page, c, j % self.page] == 0).any()) else 0.0
+                tol[lo:lo + n, h] += 1.05 * (least * most * (seen.double() @ v8) + zero)
         return out, tol
 
     def check_but(self, keys):
@@ -325,3 +328,20 @@ def test_attention_tiny_values(size, d, dtype):
             lo = int(step.q_off[s])
             more = 1.05 * (2.0 ** -85 + x * 2.0 ** -92) if size < -59 else 0.0
             assert bool(((got[lo:lo + n].double() - ref[lo:lo + n]).abs() <= tol[lo:lo + n] + more).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("d", [64, 128, 200])
+def test_attention_a_zero_value_of_most_weight(d, dtype):
+    """A key takes nearly all of the softmax and adds nothing: what the others add is small, and right all the same."""
+    for n in (1, 100):
+        for at in (5, 130):
+            for factor in (1.0, 2.0):
+                step = Apart([(n, n + 200)], 4, 2, d, 16, dtype)
+                page = int(step.pages[0, at // 16])
+                step.q[:] = step.q[:1]
+                step.q[:, 1::2] = step.q[:, ::2]
+                step.k[page, :, at % 16, :d] = (step.q[0, ::2].float() * 40).round().clamp(-127, 127).to(torch.int8)
+                scale_keys(step, "ks", 0, [at], factor)
+                scale_keys(step, "vs", 0, [at], 0.0)
+                step.check()
