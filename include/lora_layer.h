@@ -177,9 +177,9 @@ lora_status lora_attention_plan(const lora_attention *attention, const lora_cach
  * to 11 bits (dtype bfloat16) or 22 (float32), the output once to dtype.
  * (With dtype bfloat16, rows that are computed many at a time meet keys and
  * values that are rounded to 11 bits once their scales are multiplied in.)
- * A key keeps those bits while its weight times its value's scale is above 2^-17
+ * A key keeps those bits while its weight times its value's scale is above 2^-13
  * (float32: 2^-12) of the row's largest such product, and is off by no more than
- * 2^-28 (2^-34) of that below.  Scales below 2^-60 lose bits too: of values, an
+ * 2^-24 (2^-34) of that below.  Scales below 2^-60 lose bits too: of values, an
  * output is then off by 2^-85 more and by 2^-92 for each key that it sees; of keys
  * (dtype bfloat16), a score by 2^-85 scale sum |q|.
  *   q, out  heads of the batch's rows: n_heads of head_dim values.  out may be

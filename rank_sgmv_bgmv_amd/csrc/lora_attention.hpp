@@ -22,9 +22,10 @@ constexpr float kNoScore = -3.0e38f;  // the running maximum before the first ke
 template <bool F32> constexpr float kHeadroom = F32 ? 14.f : 8.f;
 template <bool F32> constexpr float kSlack = F32 ? 1.f : 7.f;
 // Kernels that sum weights after their rounding do so in tiles whose value exponent is no more than this below the largest
-// of the tiles before: what a key's weight can lose there is 2^-(25 + kHeadroom - kLowTile) of a row's sum, 2^-31.  (A tile
-// of zeros, whose exponent is -60, behind one of ordinary values would lose all of it.)
-constexpr int kLowTile = 2;
+// of the tiles before: what a key's weight can lose there is 2^-(25 + kHeadroom - kLowTile) of a row's sum, 2^-29.  (A tile
+// of zeros, whose exponent is -60, behind one of ordinary values would lose all of it.)  Where all tiles of a prompt but the
+// first take the other way, 16384 tokens take 1600 us for 1240.
+constexpr int kLowTile = 4;
 
 // Two bytes of u (8-bit values plus 128, so 0 .. 255) as float16, (u - 128) /
 // 512 each.  The bytes are taken as the float16 numbers u * 2^-24 that their
@@ -92,8 +93,10 @@ __device__ __forceinline__ int tile_exponent(float v) {
 // Scales of a tile that are much less than its largest lose bits to it, which a row may not even see: in such a tile each
 // key has an exponent of its own.  Keys lose none down to 2^-kSpreadK (an 8-bit value over 2^13 is a normal float16
 // number); of values, what is left of a weight's range is smaller by as much, and one that is zero leaves none where its
-// key takes most of the weight.
-constexpr int kSpreadK = 12, kSpreadV = 4;
+// key takes most of the weight.  bfloat16 has less to lose; where every tile is such a one, a prompt of 16384 takes 2070 us
+// for 1300, drafts 490 for 319, single tokens what they take else.
+constexpr int kSpreadK = 12;
+template <bool F32> constexpr int kSpreadV = F32 ? 4 : 8;
 
 // Scores beyond this, where float32 has steps of 1/8 and more: a weight is then 2 to the difference of two rounded numbers,
 // which may lie above or below what the headroom is for by some steps.  The product with the scales is rounded before the
@@ -247,9 +250,9 @@ __device__ __forceinline__ void scale_apart(f32x16 (&s)[2], float factor, const 
   }
 }
 
-// A lane's part of a tile's sum of 2^(score - M), from its 32 products s and what they are multiplied with; apart: from what
-// scale_apart made of them.
-__device__ __forceinline__ float sum_exact(const f32x16 (&s)[2], float factor, float M, bool apart, const uint4 *e) {
+// A lane's part of a tile's sum of 2^(score - M): its weights 2^(s factor - less), of which the exponents of V are taken off
+// again, so that they err as the outputs' do.  apart: s is what scale_apart made of it.
+__device__ __forceinline__ float sum_exact(const f32x16 (&s)[2], float factor, float less, int e_v, bool apart, const uint4 *e) {
   float sum = 0.f;
 #pragma unroll
   for (int n = 0; n < 8; ++n) {
@@ -260,7 +263,7 @@ __device__ __forceinline__ float sum_exact(const f32x16 (&s)[2], float factor, f
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      sum += __builtin_amdgcn_exp2f(fmaf(s[n / 4][n % 4 * 4 + i], factor, -M) - float(v_exponent(x[i])));
+      sum += ldexpf(__builtin_amdgcn_exp2f(fmaf(s[n / 4][n % 4 * 4 + i], factor, -less)), -e_v - v_exponent(x[i]));
   }
   return sum;
 }

@@ -152,7 +152,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
       const float ks = sk >= kNoScale ? __builtin_nanf("") : __uint_as_float(sk);
       int x_k = e_k, x_v = e_v;
       const int own_k = tile_exponent(__uint_as_float(k_fine)), own_v = tile_exponent(__uint_as_float(v_fine));
-      const bool apart = __any((!F32 && k_fine && own_k < e_k - kSpreadK) || (there && own_v < e_v - kSpreadV));
+      const bool apart = __any((!F32 && k_fine && own_k < e_k - kSpreadK) || (there && own_v < e_v - kSpreadV<F32>));
       if (apart) {
         x_k = own_k, x_v = own_v;
         reinterpret_cast<uint32_t *>(lds + kExps)[at * 64 + lane] = pack_exponents(F32 ? 0 : x_k - e_k, x_v - e_v);
@@ -347,7 +347,7 @@ __global__ __launch_bounds__(64 * NW, NW / 4) void attention_exact_kernel(AttnAr
             for (int i = 0; i < 32; ++i) s[i / 16][i % 16] = far_score(product(s[i / 16][i % 16], factor), less, kMostWeight);
             factor = 1.f, less = 0.f;
           }
-          if (low) l += sum_exact(s, factor, far ? float(e_v) : M, apart, exps + turn * 16);
+          if (low) l += sum_exact(s, factor, less, e_v, apart, exps + turn * 16);
         }
         float sum = 0.f;
         uint32_t r[kTerms][16];

@@ -21,7 +21,7 @@
 // weights are w = 2^(t - M) m in float16, M the running maximum of t less 14, and
 // l = sum 2^(t - M) 2^-e.  So a weight keeps 11 bits while it is above 2^-23 of
 // the largest contribution, whatever the values' size down to scales of 2^-60
-// (below, e stays): where those of a tile lie more than 2^kSpreadV apart, M takes
+// (below, e stays): where those of a tile lie more than 2^4 apart, M takes
 // each key's own e.
 //
 // Bound by memory: 64 requests of up to 32768 keys, 8 heads of 128, read 2.94 GB
@@ -248,7 +248,7 @@ __global__ __launch_bounds__(kFewThreads, DP <= 128 && kBlocks == 1 && !F32 ? 2 
         }
         e = uniform(tile_exponent(quarters_max(__uint_as_float(top))));
         if (whole) least = all_least;
-        apart = e > kLeastExponent && __any(least < __float_as_uint(ldexpf(1.f, e - 1 - kSpreadV)));
+        apart = e > kLeastExponent && __any(least < __float_as_uint(ldexpf(1.f, e - 1 - kSpreadV<true>)));
         const float down = ldexpf(1.f, -e);
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb)

@@ -166,16 +166,16 @@ def test_attention_a_key_without_a_finite_scale(which, value, dtype):
 # --------------------------------------- keys of very different sizes in a tile --
 class Apart(Step):
     """Where contributions c = p scale lie far apart, the smallest step of float16, 2^-24, counts too.  Scales are taken as m
-    over a power of two of their tile, 2^-5 <= m < 1 (or over their own, 1/2 <= m).  In float32 weights are p m 2^x with x such
-    that the largest p over that power has p 2^x = 2^14, so that the largest c has a weight of 2^9 or more; each is off by
-    2^-25 at most, half the smallest step (of its second number too), which is 2^-34 of the largest c.  In bfloat16 weights are
-    p 2^x with the largest 2^8 or more and meet values m v: 2^-25 m of at least 2^8 m', which is 2^-33 m / m' <= 2^-28.  (Few
-    rows are as float32.)  The output is off by that times the sum of the 8-bit values of the keys seen.  Where a scale is zero,
+    over a power of two of their tile, 2^-5 (bfloat16, many rows: 2^-9) <= m < 1, or over their own, 1/2 <= m.  In float32
+    weights are p m 2^x with x such that the largest p over that power has p 2^x = 2^14, so that the largest c has a weight of
+    2^9 or more; each is off by 2^-25 at most, half the smallest step (of its second number too), which is 2^-34 of the largest
+    c.  In bfloat16 weights are p 2^x with the largest 2^8 or more and meet values m v: 2^-25 m of at least 2^8 m', which is
+    2^-33 m / m' <= 2^-24.  (Few rows are as float32.)  The output is off by that times the sum of the 8-bit values of the keys seen.  Where a scale is zero,
     which counts as 2^-60, 2^-85 and 2^-92 a key come to it (test_attention_tiny_values)."""
 
     def reference(self):
         out, tol = super().reference()
-        least = 2.0 ** (-34 if self.dtype == torch.float32 else -28)
+        least = 2.0 ** (-34 if self.dtype == torch.float32 else -24)
         for s, (n, x) in enumerate(self.seqs):
             lo, j = int(self.q_off[s]), torch.arange(x)
             page = self.pages[s].long()[j // self.page]
