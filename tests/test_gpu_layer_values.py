@@ -345,3 +345,19 @@ def test_attention_a_zero_value_of_most_weight(d, dtype):
                 scale_keys(step, "ks", 0, [at], factor)
                 scale_keys(step, "vs", 0, [at], 0.0)
                 step.check()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=ids)
+@pytest.mark.parametrize("d", [64, 128, 200])
+def test_attention_one_key_of_a_tile_of_many_sizes(d, dtype):
+    """Each query sees its own key alone, among others of 2^-20 to 2^20 of its size: the output is that key's value, off by the
+    roundings of its weight (h^2 in float32; in bfloat16 h, and h of the value), 8 float32 roundings and the output's own."""
+    tol = 1.01 * ((2 * H if dtype == torch.bfloat16 else H * H) + 8 * V + half(dtype))
+    for seqs in ([(3, 100), (2, 40), (1, 9)], [(100, 300), (40, 40)]):
+        step = Step(seqs, 4, 2, d, 16, dtype, window=1)
+        step.vs *= 2.0 ** torch.randint(-20, 21, step.vs.shape, generator=gen(d))
+        got = step.run()
+        for s, (n, x) in enumerate(seqs):
+            lo = int(step.q_off[s])
+            want = step.rows(s)[1][:, x - n:].repeat_interleave(2, 0).transpose(0, 1)
+            assert bool(((got[lo:lo + n].double() - want).abs() <= tol * want.abs()).all()), (seqs, s)
