@@ -71,6 +71,7 @@ __device__ __forceinline__ float quarters_sum(float v) {
   const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return half_sum(__uint_as_float(s[0]) + __uint_as_float(s[1]));
 }
+
 // The largest over the wave, of the bits of floats that are not negative too.
 __device__ __forceinline__ uint32_t wave_max_bits(uint32_t v) {
 #define LORA_ROR(n) v = max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x120 + (n), 0xf, 0xf, false)))
@@ -90,6 +91,7 @@ constexpr int kLeastExponent = -60;
 __device__ __forceinline__ int tile_exponent(float v) {
   return v > 0.f ? min(max(__builtin_amdgcn_frexp_expf(v), kLeastExponent), 100) : kLeastExponent;
 }
+
 // Scales of a tile that are much less than its largest lose bits to it, which a row may not even see: in such a tile each
 // key has an exponent of its own.  Keys lose none down to 2^-kSpreadK (an 8-bit value over 2^13 is a normal float16
 // number); of values, what is left of a weight's range is smaller by as much, and one that is zero leaves none where its
