@@ -29,12 +29,12 @@
 // A step computes the scores of the next tile between the weights of this one,
 // and widens the tiles after them between the products with V, a piece after
 // each pair of products.  A prompt of 16384, window 4096, 32 heads of 128 takes
-// 1260 to 1360 us on one card or another, 9.6e11 operations at 0.74 POP/s where a
+// 1240 to 1360 us on one card or another, 9.6e11 operations at 0.74 POP/s where a
 // large library product of float16 reaches 1.39.  Matrix units are busy 33% of
 // the clocks, vector units 50%: the two waves of a SIMD run into the same kind of
 // work and wait for each other.  What it spends, taken apart at 1400 us: without
 // the products QK 236 us less, PV 226, exponentials 136, widening and loads 364.
-// 32 drafts of 24 tokens after up to 16384 keys take 309 us, 0.41 POP/s: a
+// 32 drafts of 24 tokens after up to 16384 keys take 306 us, 0.42 POP/s: a
 // quarter of their units' rows are empty, and 47 MB of pieces are written and
 // joined.
 
